@@ -1,0 +1,364 @@
+// fl_evict.cu -- eviction from a cache by accumulated attention weight.
+//
+// Two launches.  The selection finds, per (sequence, KV head), the keep-th key in
+// the order (protected, weight bits descending, slot ascending) by a radix select
+// and writes the source slot of every destination slot; the move copies rows.  A kept row
+// below the budget stays where it is and the freed slots take the kept rows from
+// beyond it, so in place the sources (slots >= keep) and the destinations (slots
+// < keep) never meet and no order of the copies matters.
+#include <algorithm>
+#include <climits>
+#include <cooperative_groups.h>
+
+#include "fl_device.cuh"
+#include "fl_serving.h"
+
+namespace cg = cooperative_groups;
+
+namespace fl {
+namespace {
+
+constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
+constexpr int kEvCluster = 8;             // CTAs of one (sequence, KV head) at most
+constexpr int kEvKeys = 32768;            // keys one CTA holds in shared memory (128 KB)
+constexpr int kEvSlots = kEvCluster * kEvKeys;
+
+struct EvictArgs {
+  flashloop_evict_args c;
+  int cap;              // min(keep, S): slots of a segment's map
+  int chunk;            // slots per CTA of the selection
+  int32_t* src;         // [B * Hkv][cap] source slot of each destination slot
+  int32_t* from;        // [B * Hkv][cap] kept slots >= keep, ascending
+  int32_t* to;          // [B * Hkv][cap] freed slots < keep, ascending
+  int32_t* n_kept;      // [B * Hkv]
+};
+
+// ============================================================================
+// Selection: a cluster of 1-8 CTAs per (sequence, KV head), each with a contiguous
+// chunk of slots, its keys in shared memory.  Key: 0xFFFFFFFF when protected, else the
+// weight's bits (at most 0xFFFFFFFE).  Four 8-bit digits, largest first: every
+// CTA histograms the keys that match the digits found so far, and after a
+// cluster barrier reads all CTAs' histograms over distributed shared memory and
+// finds the next digit by itself.  Latency-bound (13 cluster barriers at most);
+// the chunk keeps every pass over the keys short.
+// ============================================================================
+__global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) {
+  cg::cluster_group cl = cg::this_cluster();
+  extern __shared__ uint32_t keys[];        // [chunk]
+  __shared__ int hist[2][256];              // one per digit parity: a barrier per digit suffices
+  __shared__ int tot[256];
+  __shared__ int newest_sm, sel_digit, sel_before;
+  __shared__ int warp_a[kEvWarps], warp_b[kEvWarps];
+  __shared__ int cta_eq, cta_hole, cta_move;
+  const flashloop_evict_args& c = a.c;
+  const int nc = cl.num_blocks(), rank = cl.block_rank();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const long long seg = static_cast<long long>(b) * c.Hkv + g;
+  const int n = min(max(c.lens[b], 0), c.S);
+  int32_t* src = a.src + seg * a.cap;
+  if (rank == 0 && tid == 0) a.n_kept[seg] = min(n, c.keep);
+  if (n <= c.keep) {   // the whole cluster alike
+    for (int i = rank * kEvThreads + tid; i < n; i += nc * kEvThreads) src[i] = i;
+    return;
+  }
+  const int lo = min(n, rank * a.chunk), hi = min(n, lo + a.chunk), m = hi - lo;
+  const float* acc = c.acc + b * c.acc_stride[0] + g * c.acc_stride[1] + lo;
+  const int32_t* pos = c.pos + b * c.pos_stride[0] + g * c.pos_stride[1] + lo;
+  // ---- the newest token
+  if (tid == 0) newest_sm = INT_MIN;
+  for (int i = tid; i < 512; i += kEvThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  int newest = INT_MIN;
+  for (int i = tid; i < m; i += kEvThreads) newest = max(newest, pos[i]);
+  newest = __reduce_max_sync(0xffffffffu, newest);
+  if (lane == 0) atomicMax(&newest_sm, newest);
+  cl.sync();
+  for (int r = 0; r < nc; ++r) newest = max(newest, *cl.map_shared_rank(&newest_sm, r));
+  const long long oldest_safe = static_cast<long long>(newest) - c.recent;   // protected above it
+  // ---- keys, and the digits of the keep-th one
+  for (int i = tid; i < m; i += kEvThreads) {
+    const int p = pos[i];
+    keys[i] = p < c.sinks || p > oldest_safe ? 0xFFFFFFFFu : min(__float_as_uint(acc[i]), 0xFFFFFFFEu);
+  }
+  uint32_t prefix = 0, mask = 0;
+  int k_rem = c.keep;
+#pragma unroll 1
+  for (int d = 0; d < 4; ++d) {
+    const int shift = 24 - 8 * d;
+    int* h = hist[d & 1];
+    __syncthreads();
+    for (int i0 = warp * 32; i0 < m; i0 += kEvThreads) {
+      const uint32_t u = i0 + lane < m ? keys[i0 + lane] : 0u;
+      const bool in = i0 + lane < m && (u & mask) == prefix;
+      const int bin = in ? static_cast<int>((u >> shift) & 0xFF) : 256;
+      // weights of one magnitude share their leading digits: one atomic per distinct digit of the warp
+      const unsigned same = __match_any_sync(0xffffffffu, bin);
+      if (in && lane == __ffs(same) - 1) atomicAdd(&h[bin], __popc(same));
+    }
+    cl.sync();
+    if (tid < 256) {
+      int s = 0;
+      for (int r = 0; r < nc; ++r) s += cl.map_shared_rank(h, r)[tid];
+      tot[tid] = s;
+      hist[(d & 1) ^ 1][tid] = 0;   // the other digit's: every CTA read it before the last barrier but one
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int cnt[8], mine = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        cnt[e] = tot[255 - 8 * lane - e];
+        mine += cnt[e];
+      }
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      int before = incl - mine;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (before < k_rem && before + cnt[e] >= k_rem) {
+          sel_digit = 255 - 8 * lane - e;
+          sel_before = before;
+        }
+        before += cnt[e];
+      }
+    }
+    __syncthreads();
+    k_rem -= sel_before;
+    prefix |= static_cast<uint32_t>(sel_digit) << shift;
+    mask |= 0xFFu << shift;
+  }
+  // ---- kept: every key above the keep-th, and the k_rem lowest slots equal to it.
+  // Warp w owns a contiguous run of the chunk's slots; counts per warp, then per CTA, give every slot's rank.
+  const int per = (m + kEvWarps - 1) / kEvWarps;
+  const int w0 = min(m, warp * per), w1 = min(m, w0 + per);
+  int eq = 0;
+  for (int i0 = w0; i0 < w1; i0 += 32) eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && keys[i0 + lane] == prefix));
+  if (lane == 0) warp_a[warp] = eq;
+  __syncthreads();
+  if (tid == 0) {
+    int s = 0;
+    for (int w = 0; w < kEvWarps; ++w) {
+      const int x = warp_a[w];
+      warp_a[w] = s;
+      s += x;
+    }
+    cta_eq = s;
+  }
+  cl.sync();
+  int eq_seen = warp_a[warp];
+  for (int r = 0; r < rank; ++r) eq_seen += *cl.map_shared_rank(&cta_eq, r);
+  const unsigned below = (1u << lane) - 1u;
+  auto kept_at = [&](int i0, int& seen) {   // of this lane's slot in [i0, i0 + 32); seen: equal keys before i0
+    const bool there = i0 + lane < w1;
+    const uint32_t u = there ? keys[i0 + lane] : 0u;
+    const unsigned eqb = __ballot_sync(0xffffffffu, there && u == prefix);
+    const bool k = there && (u > prefix || (u == prefix && seen + __popc(eqb & below) < k_rem));
+    seen += __popc(eqb);
+    return k;
+  };
+  int holes = 0, moves = 0, seen = eq_seen;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const bool k = kept_at(i0, seen), low = lo + i0 + lane < c.keep, there = i0 + lane < w1;
+    holes += __popc(__ballot_sync(0xffffffffu, there && low && !k));
+    moves += __popc(__ballot_sync(0xffffffffu, k && !low));
+  }
+  __syncthreads();   // warp_a read
+  if (lane == 0) {
+    warp_a[warp] = holes;
+    warp_b[warp] = moves;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int s = 0, t = 0;
+    for (int w = 0; w < kEvWarps; ++w) {
+      const int x = warp_a[w], y = warp_b[w];
+      warp_a[w] = s;
+      warp_b[w] = t;
+      s += x;
+      t += y;
+    }
+    cta_hole = s;
+    cta_move = t;
+  }
+  cl.sync();
+  int h0 = warp_a[warp], m0 = warp_b[warp], all = 0;
+  for (int r = 0; r < nc; ++r) {
+    const int x = *cl.map_shared_rank(&cta_hole, r), y = *cl.map_shared_rank(&cta_move, r);
+    if (r < rank) {
+      h0 += x;
+      m0 += y;
+    }
+    all += x;
+  }
+  seen = eq_seen;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int slot = lo + i0 + lane;
+    const bool k = kept_at(i0, seen), low = slot < c.keep, there = i0 + lane < w1;
+    const unsigned hb = __ballot_sync(0xffffffffu, there && low && !k), mb = __ballot_sync(0xffffffffu, k && !low);
+    if (k && low) src[slot] = slot;
+    if (there && low && !k) a.to[seg * a.cap + h0 + __popc(hb & below)] = slot;
+    if (k && !low) a.from[seg * a.cap + m0 + __popc(mb & below)] = slot;
+    h0 += __popc(hb);
+    m0 += __popc(mb);
+  }
+  __threadfence();
+  cl.sync();   // every CTA's lists are written (and nobody reads another's shared memory any more)
+  for (int i = rank * kEvThreads + tid; i < all; i += nc * kEvThreads)
+    src[__ldcg(&a.to[seg * a.cap + i])] = __ldcg(&a.from[seg * a.cap + i]);
+}
+
+// ============================================================================
+// Move: a row's K and V as 16-byte vectors, one per thread, kEvRows rows' loads
+// in flight; in place only rows whose source is another slot.  HBM-bound:
+// 8 hd bytes per copied row.
+// ============================================================================
+constexpr int kEvRows = 4;
+__global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int vec, int rows_cta) {
+  pdl_wait();
+  const flashloop_evict_args& c = a.c;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const long long seg = static_cast<long long>(b) * c.Hkv + g;
+  const int n = a.n_kept[seg];
+  const bool in_place = c.k_out == c.k;
+  if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0) c.lens_out[b] = n;
+  const int32_t* src = a.src + seg * a.cap;
+  const uint16_t* k = c.k + b * c.k_stride[0] + g * c.k_stride[1];
+  const uint16_t* v = c.v + b * c.v_stride[0] + g * c.v_stride[1];
+  uint16_t* ko = c.k_out + b * c.k_out_stride[0] + g * c.k_out_stride[1];
+  uint16_t* vo = c.v_out + b * c.v_out_stride[0] + g * c.v_out_stride[1];
+  const int row0 = blockIdx.x * rows_cta, row1 = min(n, row0 + rows_cta);
+  if (row0 >= row1) return;
+  const int total = (row1 - row0) * 2 * vec;   // vectors of this CTA's rows: K then V of each row
+  for (int e0 = threadIdx.x; e0 < total; e0 += 256 * kEvRows) {
+    uint4 x[kEvRows];
+    int from[kEvRows];
+#pragma unroll
+    for (int u = 0; u < kEvRows; ++u) {
+      const int e = e0 + u * 256;
+      from[u] = e < total ? src[row0 + e / (2 * vec)] : -1;
+      if (from[u] >= 0 && in_place && from[u] == row0 + e / (2 * vec)) from[u] = -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kEvRows; ++u) {
+      const int e = e0 + u * 256, w = e % (2 * vec);
+      if (from[u] >= 0)
+        x[u] = w < vec ? *reinterpret_cast<const uint4*>(k + from[u] * c.k_stride[2] + w * 8)
+                       : *reinterpret_cast<const uint4*>(v + from[u] * c.v_stride[2] + (w - vec) * 8);
+    }
+#pragma unroll
+    for (int u = 0; u < kEvRows; ++u) {
+      const int e = e0 + u * 256, w = e % (2 * vec);
+      const long long row = row0 + e / (2 * vec);
+      if (from[u] >= 0)
+        *reinterpret_cast<uint4*>(w < vec ? ko + row * c.k_out_stride[2] + w * 8
+                                          : vo + row * c.v_out_stride[2] + (w - vec) * 8) = x[u];
+    }
+  }
+  for (int r = row0 + threadIdx.x; r < row1; r += 256) {
+    const int f = src[r];
+    if (in_place && f == r) continue;
+    c.acc_out[b * c.acc_out_stride[0] + g * c.acc_out_stride[1] + r] = c.acc[b * c.acc_stride[0] + g * c.acc_stride[1] + f];
+    c.pos_out[b * c.pos_out_stride[0] + g * c.pos_out_stride[1] + r] = c.pos[b * c.pos_stride[0] + g * c.pos_stride[1] + f];
+  }
+}
+
+bool evict_shape_ok(int B, int Hkv, int S, int keep) {
+  return B >= 1 && Hkv >= 1 && S >= 0 && keep >= 1 && S <= kEvSlots && B <= 65535 && Hkv <= 65535;
+}
+size_t evict_bytes(int B, int Hkv, int S, int keep) {
+  const size_t seg = static_cast<size_t>(B) * Hkv, cap = std::min(keep, S);
+  return 3 * align256_sz(seg * cap * 4) + align256_sz(seg * 4) + 256;
+}
+
+}  // namespace
+}  // namespace fl
+
+using namespace fl;
+
+extern "C" {
+
+size_t flashloop_evict_scratch_bytes(int B, int Hkv, int S, int keep) {
+  return evict_shape_ok(B, Hkv, S, keep) ? evict_bytes(B, Hkv, S, keep) : 0;
+}
+
+fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t scratch_bytes, fl_stream_t stream) {
+  if (!c) return refuse(FL_ERR_INVALID_ARG, "NULL arguments");
+  if (!evict_shape_ok(c->B, c->Hkv, c->S, c->keep) || c->hd < 8 || c->hd % 8 || c->hd > 1024)
+    return refuse(FL_ERR_INVALID_ARG, "B, Hkv, S (<= 262144), keep (>= 1) or hd (a multiple of 8, <= 1024) out of range");
+  if (c->recent < 0 || c->sinks < 0 || static_cast<long long>(c->recent) + c->sinks > c->keep)
+    return refuse(FL_ERR_INVALID_ARG, "recent and sinks must not be negative, nor more than keep together");
+  if (c->S == 0) return refuse(FL_ERR_INVALID_ARG, "S must be at least 1");
+  const void* p16[4] = {c->k, c->v, c->k_out, c->v_out};
+  for (const void* p : p16)
+    if (!p || !is_aligned(p, 16)) return refuse(FL_ERR_INVALID_ARG, "k, v, k_out and v_out must be non-NULL and 16-byte aligned");
+  const void* p4[6] = {c->acc, c->pos, c->lens, c->acc_out, c->pos_out, c->lens_out};
+  for (const void* p : p4)
+    if (!p || !is_aligned(p, 4)) return refuse(FL_ERR_INVALID_ARG, "acc, pos, lens and their outputs must be non-NULL and 4-byte aligned");
+  const int same = (c->k_out == c->k) + (c->v_out == c->v) + (c->acc_out == c->acc) + (c->pos_out == c->pos) +
+                   (c->lens_out == c->lens);
+  if (same != 0 && same != 5) return refuse(FL_ERR_INVALID_ARG, "either every output is its input (in place) or none is");
+  const int64_t in[3] = {c->B, c->Hkv, c->S}, out[3] = {c->B, c->Hkv, c->keep};
+  for (int i = 0; i < 3; ++i) {
+    if (!stride_ok(c->k_stride[i], in[i], 8) || !stride_ok(c->v_stride[i], in[i], 8) ||
+        !stride_ok(c->k_out_stride[i], out[i], 8) || !stride_ok(c->v_out_stride[i], out[i], 8))
+      return refuse(FL_ERR_INVALID_ARG, "k, v, k_out and v_out strides must be positive multiples of 8");
+    if (same == 5 && in[i] > 1 &&
+        (c->k_stride[i] != c->k_out_stride[i] || c->v_stride[i] != c->v_out_stride[i] ||
+         (i < 2 && (c->acc_stride[i] != c->acc_out_stride[i] || c->pos_stride[i] != c->pos_out_stride[i]))))
+      return refuse(FL_ERR_INVALID_ARG, "in place, the outputs' strides must be the inputs'");
+    if (i < 2 && (!stride_ok(c->acc_stride[i], in[i], 1) || !stride_ok(c->pos_stride[i], in[i], 1) ||
+                  !stride_ok(c->acc_out_stride[i], in[i], 1) || !stride_ok(c->pos_out_stride[i], in[i], 1)))
+      return refuse(FL_ERR_INVALID_ARG, "acc, pos and their outputs' strides must be positive");
+  }
+  const size_t need = evict_bytes(c->B, c->Hkv, c->S, c->keep);
+  if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
+    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (dev < 0 || dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvKeys * 4);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (dev >= 0 && dev < 64) done[dev] = true;
+  }
+  EvictArgs a{};
+  a.c = *c;
+  a.cap = std::min(c->keep, c->S);
+  const size_t seg = static_cast<size_t>(c->B) * c->Hkv, list = align256_sz(seg * a.cap * 4);
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
+  a.src = reinterpret_cast<int32_t*>(ws);
+  a.from = reinterpret_cast<int32_t*>(ws + list);
+  a.to = reinterpret_cast<int32_t*>(ws + 2 * list);
+  a.n_kept = reinterpret_cast<int32_t*>(ws + 3 * list);
+  // CTAs per segment: chunks of about 4096 slots (8 per thread and pass)
+  int nc = 1;
+  while (nc < kEvCluster && c->S > nc * 4096) nc *= 2;
+  a.chunk = ceil_div_i(c->S, nc);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(nc, c->Hkv, c->B);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.chunk) * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = nc;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k_evict_select, a);
+  if (e != cudaSuccess) return cuda_status(e);
+  const int vec = c->hd / 8;
+  const int rows_cta = std::max(1, 256 * kEvRows * 2 / (2 * vec));
+  return cuda_status(launch_k(true, k_evict_move, dim3(ceil_div_i(a.cap, rows_cta), c->Hkv, c->B), dim3(256), 0, s, a,
+                              vec, rows_cta));
+}
+
+}  // extern "C"

@@ -23,6 +23,7 @@
 
 #include "fl_device.cuh"
 #include "fl_internal.h"
+#include "fl_serving.h"
 
 namespace cg = cooperative_groups;
 
@@ -849,6 +850,29 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, uint64_t k, uint64_t r
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2,
+                      int64_t s_row, int64_t s1, int64_t s2, uint32_t box_rows) {
+  EncodeFn fn = get_encode();
+  if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || hd % 64 || rows < 1 || n1 < 1 || n2 < 1 ||
+      box_rows == 0 || box_rows > 256)
+    return false;
+  // the stride of a dimension of one element is never used; give it a valid value
+  if (rows == 1) s_row = hd;
+  if (n1 == 1) s1 = s_row;
+  if (n2 == 1) s2 = s1;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n1),
+                              static_cast<cuuint64_t>(n2)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s_row) * 2, static_cast<cuuint64_t>(s1) * 2,
+                                 static_cast<cuuint64_t>(s2) * 2};
+  const cuuint32_t box[4] = {64, box_rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 

@@ -1,0 +1,829 @@
+// fl_prefix.cu -- attention of a batch that shares a prefix, and the attention
+// weight of key columns.
+//
+// Shared prefix: the batch's queries of one KV head form one matrix, so a tile
+// of the prefix is read once for all of them instead of once per sequence.  The
+// columns -- the prefix, and each sequence's own rows -- are split over CTAs;
+// every split leaves (max, sum, unnormalised output) per row in fp32, and one
+// merge forms the softmax over all of them:
+//   M = max_i m_i,  L = sum_i e^(m_i - M) l_i,  out = sum_i e^(m_i - M) o_i / L.
+#include <algorithm>
+#include <cmath>
+
+#include "fl_mma.cuh"
+#include "fl_serving.h"
+
+namespace fl {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPxTile = 32;                       // keys of one warp's tile
+constexpr int kPxWarps = 4;
+constexpr int kPxRing = kPxWarps * 48 * 1024;     // bytes of the four warps' tile rings
+constexpr int kMaxGroup = 64;                     // query heads per KV head
+constexpr int kMaxTq = 64;
+
+struct PrefixArgs {
+  const uint16_t* q;      // bf16 queries, or
+  const float* q32;       // fp32 queries (hi + lo products)
+  long long q_sb, q_st, q_sh;
+  uint16_t* out;
+  long long o_sb, o_st, o_sh;
+  float* out32;
+  float* lse;
+  const uint16_t *k, *v;  // each sequence's own rows (the merge reads the causal tail itself)
+  long long k_sb, k_sg, k_sr, v_sb, v_sg, v_sr;
+  const int32_t* lens;
+  const int32_t* q_lens;
+  int lens_add;
+  int B, Tq, H, Hkv, G, P, S;
+  float scale2;           // scale * log2(e): the softmax runs in powers of two
+  int rb_p, n_p;          // prefix: row blocks per KV head, column splits
+  int rb_s, n_s;          // own rows: row blocks per (sequence, KV head), column splits
+  int items_p;            // CTAs of the prefix part
+  long long rows;         // B * Tq * H
+  float* part_o;          // [n_p + n_s][rows][hd]
+  float2* part_ml;        // [n_p + n_s][rows]: max (log2 domain), sum
+};
+
+__device__ __forceinline__ int q_len_of(const PrefixArgs& a, int b) {
+  return a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq;
+}
+__device__ __forceinline__ int len_of(const PrefixArgs& a, int b) {
+  return a.S ? min(max(a.lens[b] + a.lens_add, 0), a.S) : 0;
+}
+
+// The valid queries of the batch, packed: query number i of all sequences'
+// first q_lens[b] ones, i in [first, first + count), as slots b * Tq + t (-1 past
+// the last).  Called by one warp; returns how many there are in all.
+__device__ int pack_queries(const PrefixArgs& a, int first, int count, int* slot) {
+  const int lane = threadIdx.x & 31;
+  if (!a.q_lens) {
+    const int total = a.B * a.Tq;
+    for (int i = lane; i < count; i += 32) slot[i] = first + i < total ? first + i : -1;
+    return total;
+  }
+  for (int i = lane; i < count; i += 32) slot[i] = -1;
+  __syncwarp();
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int n = b0 + lane < a.B ? q_len_of(a, b0 + lane) : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int start = base + incl - n - first;
+    for (int t = max(0, -start); t < n && start + t < count; ++t) slot[start + t] = (b0 + lane) * a.Tq + t;
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  __syncwarp();
+  return base;
+}
+
+// byte offset of 16-byte chunk c (8 dims) of row r in a tile of 128-byte swizzled boxes of `rows` rows
+__device__ __forceinline__ uint32_t sw_off(int rows, int r, int c) {
+  return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// ============================================================================
+// One split: up to 16 NM query rows of one KV head over a range of columns of
+// the prefix (rows of every sequence, packed) or of one sequence's own rows.
+// Four warps take alternate 32-key tiles, each from a TMA ring of its own, with
+// its own running (max, sum, output): no barrier between warps until the end.
+// HBM-bound: a tile's 16 KB feed 16 NM rows.  A row sees every column of
+// the range -- a sequence's columns stop at the last one all its queries see;
+// the few that only later queries see are added by the merge -- so what a masked
+// row of V holds never meets a product.  HILO: fp32 queries and probabilities as
+// bf16 hi + lo pairs (about 16 significant bits).
+// ============================================================================
+template <int HD, int NM, bool HILO>
+__global__ void __launch_bounds__(128, 1)
+    k_prefix_split(const __grid_constant__ CUtensorMap kp, const __grid_constant__ CUtensorMap vp,
+                   const __grid_constant__ CUtensorMap ks, const __grid_constant__ CUtensorMap vs, const PrefixArgs a) {
+  constexpr int RB = 16 * NM;                       // query rows
+  constexpr int NB = HD / 64;                       // 128-byte boxes per row
+  constexpr int TILE_BYTES = kPxTile * HD * 2;      // K or V of one tile
+  constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  constexpr int STAGES = kPxRing / kPxWarps / STAGE_BYTES;
+  constexpr int QBYTES = RB * HD * 2;
+  constexpr int NT = HD / 8;                        // 8-dim output tiles
+  constexpr int OLD = HD + 8;                       // padded row of the merge buffer
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qsm = ring + kPxRing;
+  __shared__ __align__(8) uint64_t full[kPxWarps][12];
+  __shared__ int slot_sm[RB + 1];
+  __shared__ long long row_id[RB];
+  __shared__ float sm_m[kPxWarps][RB], sm_l[kPxWarps][RB];
+  __shared__ int n_valid_sm, bad_sm;
+  static_assert(STAGES <= 12, "barriers");
+
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kPxWarps * 12; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
+    fence_mbar_init();
+    bad_sm = 0;
+  }
+  pdl_wait();
+  // ---- which rows, which columns
+  const bool pre = static_cast<int>(blockIdx.x) < a.items_p;
+  int it = pre ? blockIdx.x : blockIdx.x - a.items_p;
+  const int rbs = pre ? a.rb_p : a.rb_s, nsp = pre ? a.n_p : a.n_s;
+  const int rb = it % rbs;
+  it /= rbs;
+  const int sp = it % nsp;
+  it /= nsp;
+  const int g = it % a.Hkv, b = it / a.Hkv;
+  const int r0 = rb * RB;
+  int ncols, nrows;
+  if (pre) {
+    const int first = r0 / a.G, count = (r0 + RB - 1) / a.G - first + 1;
+    if (warp == 0) {
+      const int total = pack_queries(a, first, count, slot_sm);
+      if (lane == 0) n_valid_sm = total;
+    }
+    __syncthreads();
+    nrows = n_valid_sm * a.G;
+    ncols = a.P;
+    if (tid < RB) {
+      const int s = r0 + tid < nrows ? slot_sm[(r0 + tid) / a.G - first] : -1;
+      row_id[tid] = s < 0 ? -1 : static_cast<long long>(s) * a.H + g * a.G + (r0 + tid) % a.G;
+    }
+  } else {
+    const int ql = q_len_of(a, b), len = len_of(a, b);
+    nrows = ql * a.G;
+    ncols = min(max(len - ql + 1, 0), len);
+    if (tid < RB) {
+      const int r = r0 + tid;
+      row_id[tid] = r < nrows ? (static_cast<long long>(b) * a.Tq + r / a.G) * a.H + g * a.G + r % a.G : -1;
+    }
+  }
+  __syncthreads();   // barriers, row_id
+  if (r0 >= nrows) return;
+  const int ntiles = (ncols + kPxTile - 1) / kPxTile;
+  const int tb = static_cast<int>(static_cast<long long>(sp) * ntiles / nsp);
+  const int te = static_cast<int>(static_cast<long long>(sp + 1) * ntiles / nsp);
+  const int mine = te - tb > warp ? (te - tb - warp + kPxWarps - 1) / kPxWarps : 0;   // this warp's tiles
+  const CUtensorMap* km = pre ? &kp : &ks;
+  const CUtensorMap* vm = pre ? &vp : &vs;
+  uint8_t* wring = ring + warp * (kPxRing / kPxWarps);
+  auto issue = [&](int u) {
+    const int y = (tb + warp + u * kPxWarps) * kPxTile;
+    const uint32_t st = smem_u32(wring + (u % STAGES) * STAGE_BYTES), fb = smem_u32(&full[warp][u % STAGES]);
+    mbar_arrive_expect_tx(fb, STAGE_BYTES);
+#pragma unroll
+    for (int bx = 0; bx < NB; ++bx) {
+      tma_load_4d(st + bx * kPxTile * 128, km, fb, bx * 64, y, g, pre ? 0 : b);
+      tma_load_4d(st + TILE_BYTES + bx * kPxTile * 128, vm, fb, bx * 64, y, g, pre ? 0 : b);
+    }
+  };
+  if (lane == 0)
+    for (int u = 0; u < STAGES && u < mine; ++u) issue(u);
+
+  // ---- queries to shared memory (rows past the last: zero)
+  for (int e = tid; e < RB * (HD / 8); e += 128) {
+    const int r = e / (HD / 8), c = e % (HD / 8);
+    const long long id = row_id[r];
+    uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+    if (id >= 0) {
+      const long long s = id / a.H, h = id % a.H;
+      const long long off = (s / a.Tq) * a.q_sb + (s % a.Tq) * a.q_st + h * a.q_sh + c * 8;
+      if (!HILO) {
+        hi = *reinterpret_cast<const uint4*>(a.q + off);
+      } else {
+        const float4 x0 = *reinterpret_cast<const float4*>(a.q32 + off);
+        const float4 x1 = *reinterpret_cast<const float4*>(a.q32 + off + 4);
+        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+        float h8[8], l8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split_bf16(x[i], h8[i], l8[i]);
+        hi = make_uint4(pack_bf16x2(h8[0], h8[1]), pack_bf16x2(h8[2], h8[3]), pack_bf16x2(h8[4], h8[5]),
+                        pack_bf16x2(h8[6], h8[7]));
+        lo = make_uint4(pack_bf16x2(l8[0], l8[1]), pack_bf16x2(l8[2], l8[3]), pack_bf16x2(l8[4], l8[5]),
+                        pack_bf16x2(l8[6], l8[7]));
+      }
+    }
+    *reinterpret_cast<uint4*>(qsm + sw_off(RB, r, c)) = hi;
+    if (HILO) *reinterpret_cast<uint4*>(qsm + QBYTES + sw_off(RB, r, c)) = lo;
+  }
+  __syncthreads();
+
+  float m_run[NM][2], l_run[NM][2], acc[NM][NT][4];
+#pragma unroll
+  for (int i = 0; i < NM; ++i) {
+    m_run[i][0] = m_run[i][1] = -INFINITY;
+    l_run[i][0] = l_run[i][1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+  }
+  const uint32_t qs = smem_u32(qsm);
+  int done = 0;
+  for (; done < mine; ++done) {
+    const int st = done % STAGES;
+    if (!mbar_wait(smem_u32(&full[warp][st]), (done / STAGES) & 1, nullptr)) break;
+    const uint32_t Kt = smem_u32(wring + st * STAGE_BYTES), Vt = Kt + TILE_BYTES;
+    const int nc = min(kPxTile, ncols - (tb + warp + done * kPxWarps) * kPxTile);   // columns of this tile in range
+    if (nc < kPxTile) {
+      // rows past the range (another query's tokens, or never written): their
+      // probabilities are 0, and 0 times what they hold must stay 0
+      for (int e = lane; e < (kPxTile - nc) * (HD / 8); e += 32)
+        *reinterpret_cast<uint4*>(wring + st * STAGE_BYTES + TILE_BYTES +
+                                  sw_off(kPxTile, nc + e / (HD / 8), e % (HD / 8))) = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+    // ---- scores of the tile's 32 keys
+    float s[NM][4][4] = {};
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+      uint32_t kf[2][4];
+#pragma unroll
+      for (int n2 = 0; n2 < 2; ++n2)
+        ldsm_x4(Kt + sw_off(kPxTile, n2 * 16 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), kf[n2]);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+#pragma unroll
+        for (int part = 0; part < (HILO ? 2 : 1); ++part) {
+          uint32_t qf[4];
+          ldsm_x4(qs + part * QBYTES + sw_off(RB, i * 16 + (lane & 15), k * 2 + (lane >> 4)), qf);
+#pragma unroll
+          for (int n2 = 0; n2 < 2; ++n2) {
+            mma_bf16_16816(s[i][n2 * 2], qf, kf[n2][0], kf[n2][1]);
+            mma_bf16_16816(s[i][n2 * 2 + 1], qf, kf[n2][2], kf[n2][3]);
+          }
+        }
+      }
+    }
+    // ---- running softmax: thread holds rows lane/4 (+8), columns 8n + 2(lane%4) + {0, 1}
+    uint32_t pf[NM][2][4], pl[HILO ? NM : 1][2][4];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[i][n][e] * a.scale2;
+          if (nc < kPxTile && n * 8 + 2 * (lane & 3) + (e & 1) >= nc) x = -INFINITY;
+          s[i][n][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      float al[2], ms[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        const float mn = fmaxf(m_run[i][e], mx[e]);
+        ms[e] = mn == -INFINITY ? 0.f : mn;   // nothing finite yet: weights of 0, not NaN
+        al[e] = exp2f(m_run[i][e] - ms[e]);
+        m_run[i][e] = mn;
+        l_run[i][e] *= al[e];
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp2f(s[i][n][e] - ms[e >> 1]);
+          s[i][n][e] = p;
+          l_run[i][e >> 1] += p;
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        acc[i][n][0] *= al[0];
+        acc[i][n][1] *= al[0];
+        acc[i][n][2] *= al[1];
+        acc[i][n][3] *= al[1];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = s[i][2 * k + (j >> 1)][(j & 1) * 2], x1 = s[i][2 * k + (j >> 1)][(j & 1) * 2 + 1];
+          pf[i][k][j] = pack_bf16x2(x0, x1);
+          if (HILO)
+            pl[HILO ? i : 0][k][j] = pack_bf16x2(x0 - bf16_to_f(pf[i][k][j] & 0xFFFF), x1 - bf16_to_f(pf[i][k][j] >> 16));
+        }
+    }
+    // ---- output += P V
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int n2 = 0; n2 < NT / 2; ++n2) {
+        uint32_t vf[4];
+        ldsm_x4_t(Vt + sw_off(kPxTile, k * 16 + (lane & 15), n2 * 2 + (lane >> 4)), vf);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          mma_bf16_16816(acc[i][n2 * 2], pf[i][k], vf[0], vf[1]);
+          mma_bf16_16816(acc[i][n2 * 2 + 1], pf[i][k], vf[2], vf[3]);
+          if (HILO) {
+            mma_bf16_16816(acc[i][n2 * 2], pl[HILO ? i : 0][k], vf[0], vf[1]);
+            mma_bf16_16816(acc[i][n2 * 2 + 1], pl[HILO ? i : 0][k], vf[2], vf[3]);
+          }
+        }
+      }
+    }
+    __syncwarp();   // the slot is free again
+    if (lane == 0 && done + STAGES < mine) issue(done + STAGES);
+  }
+  if (done < mine) {
+    // a tile never arrived: let the copies in flight land (bounded); the result becomes NaN
+    if (lane == 0) {
+      bad_sm = 1;
+      for (int u = done; u < mine && u < done + STAGES; ++u)
+        mbar_wait(smem_u32(&full[warp][u % STAGES]), (u / STAGES) & 1, nullptr);
+    }
+  }
+  // ---- the four warps' parts become one
+#pragma unroll
+  for (int i = 0; i < NM; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = l_run[i][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if ((lane & 3) == 0) {
+        sm_m[warp][i * 16 + e * 8 + (lane >> 2)] = m_run[i][e];
+        sm_l[warp][i * 16 + e * 8 + (lane >> 2)] = l;
+      }
+    }
+  __syncthreads();   // every warp is done with its ring
+  float* om = reinterpret_cast<float*>(ring);   // [warps][RB][OLD]
+#pragma unroll
+  for (int i = 0; i < NM; ++i)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float* d0 = om + (warp * RB + i * 16 + (lane >> 2)) * OLD + n * 8 + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(d0) = make_float2(acc[i][n][0], acc[i][n][1]);
+      *reinterpret_cast<float2*>(d0 + 8 * OLD) = make_float2(acc[i][n][2], acc[i][n][3]);
+    }
+  __syncthreads();
+  const long long split = pre ? sp : a.n_p + sp;
+  for (int e = tid; e < RB * (HD / 4); e += 128) {
+    const int r = e / (HD / 4), d = (e % (HD / 4)) * 4;
+    const long long id = row_id[r];
+    if (id < 0) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kPxWarps; ++w) M = fmaxf(M, sm_m[w][r]);
+    const float ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kPxWarps; ++w) {
+      const float wt = exp2f(sm_m[w][r] - ms);
+      const float4 x = *reinterpret_cast<const float4*>(om + (w * RB + r) * OLD + d);
+      L += wt * sm_l[w][r];
+      o.x += wt * x.x;
+      o.y += wt * x.y;
+      o.z += wt * x.z;
+      o.w += wt * x.w;
+    }
+    if (M > -INFINITY || !(L == 0.f) || bad_sm)
+      *reinterpret_cast<float4*>(a.part_o + (split * a.rows + id) * HD + d) = o;
+    if (d == 0) a.part_ml[split * a.rows + id] = bad_sm ? make_float2(0.f, NAN) : make_float2(M, L);
+  }
+}
+
+// ============================================================================
+// Merge: one CTA per output row.  Groups of HD/4 lanes take every n-th split
+// (a few loads in flight each) and every n-th column of the causal tail -- the
+// columns this query sees and an earlier one of its sequence does not, at most
+// Tq - 1 -- as fp32 dot products; then the groups' (max, sum, output) meet in
+// shared memory.
+// ============================================================================
+template <int HD, bool Q32>
+__global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
+  constexpr int LPG = HD / 4;          // lanes of a group, 4 dims each
+  constexpr int NG = 128 / LPG;        // groups
+  constexpr int MB = 8;                // splits requested together
+  __shared__ float gm[NG], gl[NG];
+  __shared__ float4 go[NG][LPG];
+  pdl_trigger();
+  const long long row = blockIdx.x;
+  const int h = static_cast<int>(row % a.H), t = static_cast<int>(row / a.H % a.Tq);
+  const int b = static_cast<int>(row / a.H / a.Tq);
+  const int grp = threadIdx.x / LPG, gl_lane = threadIdx.x % LPG;
+  pdl_wait();
+  const int ql = q_len_of(a, b);
+  if (t >= ql) return;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float ms, float ls, const float4& x) {   // a part with maximum ms, sum ls, output x
+    if (ms == -INFINITY) {   // nothing there: its output was never written
+      l += ls;               // 0, or NaN
+      return;
+    }
+    const float mn = fmaxf(m, ms);
+    const float w0 = exp2f(m - mn), w1 = exp2f(ms - mn);
+    l = l * w0 + ls * w1;
+    o.x = o.x * w0 + x.x * w1;
+    o.y = o.y * w0 + x.y * w1;
+    o.z = o.z * w0 + x.z * w1;
+    o.w = o.w * w0 + x.w * w1;
+    m = mn;
+  };
+  const int n = a.n_p + a.n_s;
+  for (int i0 = grp; i0 < n; i0 += NG * MB) {
+    float2 ml[MB];
+    float4 x[MB];
+#pragma unroll
+    for (int u = 0; u < MB; ++u) {
+      const int i = i0 + u * NG;
+      ml[u] = i < n ? __ldcg(&a.part_ml[static_cast<long long>(i) * a.rows + row]) : make_float2(-INFINITY, 0.f);
+      x[u] = i < n ? __ldcg(reinterpret_cast<const float4*>(&a.part_o[(static_cast<long long>(i) * a.rows + row) * HD +
+                                                                     gl_lane * 4]))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < MB; ++u)
+      if (i0 + u * NG < n) add(ml[u].x, ml[u].y, x[u]);
+  }
+  const int len = len_of(a, b);
+  const int base = min(max(len - ql + 1, 0), len), lim = min(max(len - ql + t + 1, 0), len);
+  if (lim > base) {
+    const int g = h / a.G;
+    float4 q4;
+    const long long qo = b * a.q_sb + t * a.q_st + h * a.q_sh + gl_lane * 4;
+    if (Q32) {
+      q4 = *reinterpret_cast<const float4*>(a.q32 + qo);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(a.q + qo);
+      q4 = make_float4(bf16_to_f(u.x & 0xFFFF), bf16_to_f(u.x >> 16), bf16_to_f(u.y & 0xFFFF), bf16_to_f(u.y >> 16));
+    }
+    const unsigned mask = LPG == 32 ? 0xffffffffu : (0xffffu << (threadIdx.x & 16));
+    for (int j = base + grp; j < lim; j += NG) {
+      const uint2 ku = *reinterpret_cast<const uint2*>(a.k + b * a.k_sb + g * a.k_sg + j * a.k_sr + gl_lane * 4);
+      const uint2 vu = *reinterpret_cast<const uint2*>(a.v + b * a.v_sb + g * a.v_sg + j * a.v_sr + gl_lane * 4);
+      float s = q4.x * bf16_to_f(ku.x & 0xFFFF) + q4.y * bf16_to_f(ku.x >> 16) + q4.z * bf16_to_f(ku.y & 0xFFFF) +
+                q4.w * bf16_to_f(ku.y >> 16);
+#pragma unroll
+      for (int d = LPG / 2; d > 0; d >>= 1) s += __shfl_xor_sync(mask, s, d);
+      add(s * a.scale2, 1.f, make_float4(bf16_to_f(vu.x & 0xFFFF), bf16_to_f(vu.x >> 16), bf16_to_f(vu.y & 0xFFFF),
+                                         bf16_to_f(vu.y >> 16)));
+    }
+  }
+  if (gl_lane == 0) {
+    gm[grp] = m;
+    gl[grp] = l;
+  }
+  go[grp][gl_lane] = o;
+  __syncthreads();
+  if (threadIdx.x >= LPG) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NG; ++i) M = fmaxf(M, gm[i]);
+  const float ms = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    const float w = exp2f(gm[i] - ms);
+    const float4 x = go[i][gl_lane];
+    L += w * gl[i] + (gm[i] == -INFINITY ? gl[i] : 0.f);
+    r.x += w * x.x;
+    r.y += w * x.y;
+    r.z += w * x.z;
+    r.w += w * x.w;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;   // nothing visible: 0 and -inf
+  r.x *= inv;
+  r.y *= inv;
+  r.z *= inv;
+  r.w *= inv;
+  *reinterpret_cast<uint2*>(a.out + b * a.o_sb + t * a.o_st + h * a.o_sh + gl_lane * 4) =
+      make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
+  if (a.out32) *reinterpret_cast<float4*>(a.out32 + row * HD + gl_lane * 4) = r;
+  if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// ============================================================================
+// Attention weight of key columns: out = acc + sum over rows of
+// 2^(scale2 q.k - lse2).  A CTA owns 128 columns of one (sequence, KV head); its
+// keys are loaded once by TMA and every query row passes over them in blocks of
+// 32, so no sum leaves its thread until the end: no atomics, a fixed order.
+// ============================================================================
+constexpr int kCwCols = 128, kCwRows = 32;
+struct WeightsArgs {
+  const uint16_t* q;
+  long long q_sb, q_st, q_sh;
+  const float* lse;
+  const float* acc;
+  float* out;
+  const int32_t* lens;
+  const int32_t* q_lens;
+  int B, Tq, H, Hkv, G, S;
+  float scale2;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(128) k_column_weights(const __grid_constant__ CUtensorMap km, const WeightsArgs a) {
+  constexpr int NB = HD / 64;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* ksm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qsm = ksm + kCwCols * HD * 2;
+  __shared__ __align__(8) uint64_t full;
+  __shared__ float lse_s[kCwRows];
+  __shared__ int lim_s[kCwRows];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col0 = blockIdx.x * kCwCols, g = blockIdx.y, b = blockIdx.z;
+  const bool causal = a.lens != nullptr;
+  const int ql = a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq;
+  const int len = causal ? min(max(a.lens[b], 0), a.S) : a.S;
+  const size_t base = (static_cast<size_t>(b) * a.Hkv + g) * a.S;
+  const int ncol = min(kCwCols, a.S - col0);
+  const int top = min(col0 + kCwCols, len);   // columns of this CTA that some query sees
+  if (top <= col0 || ql == 0) {
+    if (a.out != a.acc && tid < ncol) a.out[base + col0 + tid] = a.acc[base + col0 + tid];
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(smem_u32(&full), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (tid == 0) {
+    mbar_arrive_expect_tx(smem_u32(&full), kCwCols * HD * 2);
+    for (int bx = 0; bx < NB; ++bx)
+      tma_load_4d(smem_u32(ksm + bx * kCwCols * 128), &km, smem_u32(&full), bx * 64, col0, g, b);
+  }
+  const bool ok = mbar_wait(smem_u32(&full), 0, nullptr);
+  const uint32_t Kt = smem_u32(ksm), Qt = smem_u32(qsm);
+  float sum[4][2] = {};   // columns warp*32 + 8n + 2(lane%4) + {0, 1}
+  // queries see a prefix of the columns that grows with t: those before t_first see none of this CTA's
+  const int t_first = causal ? max(0, col0 - (len - ql)) : 0;
+  for (int r0 = t_first * a.G; r0 < ql * a.G; r0 += kCwRows) {
+    __syncthreads();
+    for (int e = tid; e < kCwRows * (HD / 8); e += 128) {
+      const int r = r0 + e / (HD / 8), c = e % (HD / 8);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < ql * a.G)
+        x = *reinterpret_cast<const uint4*>(a.q + b * a.q_sb + static_cast<long long>(r / a.G) * a.q_st +
+                                            static_cast<long long>(g * a.G + r % a.G) * a.q_sh + c * 8);
+      *reinterpret_cast<uint4*>(qsm + sw_off(kCwRows, r - r0, c)) = x;
+    }
+    if (tid < kCwRows) {
+      const int r = r0 + tid, t = r / a.G;
+      float l = -INFINITY;
+      if (r < ql * a.G) l = a.lse[(static_cast<size_t>(b) * a.Tq + t) * a.H + g * a.G + r % a.G];
+      lse_s[tid] = l * kLog2e;
+      lim_s[tid] = l == -INFINITY ? 0 : (causal ? min(len - ql + t + 1, len) : a.S);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float s[4][4] = {};
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        uint32_t qf[4], kf[4];
+        ldsm_x4(Qt + sw_off(kCwRows, i * 16 + (lane & 15), k * 2 + (lane >> 4)), qf);
+#pragma unroll
+        for (int n2 = 0; n2 < 2; ++n2) {
+          ldsm_x4(Kt + sw_off(kCwCols, warp * 32 + n2 * 16 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)),
+                  kf);
+          mma_bf16_16816(s[n2 * 2], qf, kf[0], kf[1]);
+          mma_bf16_16816(s[n2 * 2 + 1], qf, kf[2], kf[3]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = i * 16 + (lane >> 2) + (e >> 1) * 8;
+        const float l2 = lse_s[r];
+        const int lim = lim_s[r] - (col0 + warp * 32 + 2 * (lane & 3) + (e & 1));
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float p = exp2f(s[n][e] * a.scale2 - l2);
+          sum[n][e & 1] += n * 8 < lim ? p : 0.f;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = sum[n][e];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      const int c = warp * 32 + n * 8 + 2 * (lane & 3) + e;
+      if (lane < 4 && c < ncol) a.out[base + col0 + c] = a.acc[base + col0 + c] + (ok ? v : NAN);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Rows per CTA and column splits of both parts.  About two CTAs per SM in all,
+// none shorter than 256 columns: a shorter split costs more in partial results
+// (hd + 2 floats per row) than its keys and values cost to read.
+struct PrefixPlan {
+  int nm;
+  int rb_p, n_p, rb_s, n_s;
+  size_t rows, bytes;
+};
+PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
+  PrefixPlan p{};
+  const int G = H / Hkv;
+  const long long rows_p = static_cast<long long>(B) * Tq * G, rows_s = static_cast<long long>(Tq) * G;
+  p.nm = (P > 0 && rows_p > 16) || rows_s > 16 ? 2 : 1;
+  const int RB = 16 * p.nm;
+  p.rb_p = ceil_div_i(rows_p, RB);
+  p.rb_s = ceil_div_i(rows_s, RB);
+  const double cols = static_cast<double>(p.rb_p) * Hkv * P + static_cast<double>(p.rb_s) * Hkv * B * S;
+  const double per = std::max(256.0, cols / (2.0 * kNumSM));
+  auto splits = [&](int n) { return n ? std::min(64, std::max(1, static_cast<int>(std::ceil(n / per)))) : 0; };
+  p.n_p = splits(P);
+  p.n_s = splits(S);
+  p.rows = static_cast<size_t>(B) * Tq * H;
+  const size_t n = p.n_p + p.n_s;
+  p.bytes = align256_sz(n * p.rows * hd * 4) + align256_sz(n * p.rows * 8) + 256;
+  return p;
+}
+
+size_t split_smem(int hd, int nm, bool hilo) { return 1024 + kPxRing + static_cast<size_t>(16 * nm) * hd * 2 * (hilo ? 2 : 1); }
+
+template <int HD, int NM, bool HILO>
+cudaError_t run_split(const CUtensorMap* m, const PrefixArgs& a, int grid, bool pdl, cudaStream_t s) {
+  return launch_k(pdl, k_prefix_split<HD, NM, HILO>, dim3(grid), dim3(128), split_smem(HD, NM, HILO), s, m[0], m[1],
+                  m[2], m[3], a);
+}
+template <int HD>
+cudaError_t run_split_hd(int nm, bool hilo, const CUtensorMap* m, const PrefixArgs& a, int grid, bool pdl,
+                         cudaStream_t s) {
+  if (nm == 1)
+    return hilo ? run_split<HD, 1, true>(m, a, grid, pdl, s) : run_split<HD, 1, false>(m, a, grid, pdl, s);
+  return hilo ? run_split<HD, 2, true>(m, a, grid, pdl, s) : run_split<HD, 2, false>(m, a, grid, pdl, s);
+}
+
+size_t weights_smem(int hd) { return 1024 + static_cast<size_t>(kCwCols + kCwRows) * hd * 2; }
+
+}  // namespace
+
+cudaError_t serving_init_attrs() {
+  static bool done[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  auto set = [&](auto* kern, size_t bytes) {
+    cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess) e = r;
+  };
+  set(k_prefix_split<64, 1, false>, split_smem(64, 1, false));
+  set(k_prefix_split<64, 1, true>, split_smem(64, 1, true));
+  set(k_prefix_split<64, 2, false>, split_smem(64, 2, false));
+  set(k_prefix_split<64, 2, true>, split_smem(64, 2, true));
+  set(k_prefix_split<128, 1, false>, split_smem(128, 1, false));
+  set(k_prefix_split<128, 1, true>, split_smem(128, 1, true));
+  set(k_prefix_split<128, 2, false>, split_smem(128, 2, false));
+  set(k_prefix_split<128, 2, true>, split_smem(128, 2, true));
+  set(k_column_weights<64>, weights_smem(64));
+  set(k_column_weights<128>, weights_smem(128));
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
+
+size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
+  return plan_prefix(B, Tq, H, Hkv, hd, P, S).bytes;
+}
+
+cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) {
+  const flashloop_prefix_args& c = L.a;
+  cudaError_t e = serving_init_attrs();
+  if (e != cudaSuccess) return e;
+  const PrefixPlan p = plan_prefix(c.B, c.Tq, c.H, c.Hkv, c.hd, c.P, c.S);
+  PrefixArgs a{};
+  a.q = c.q; a.q32 = L.q32; a.q_sb = c.q_stride[0]; a.q_st = c.q_stride[1]; a.q_sh = c.q_stride[2];
+  a.out = c.out; a.o_sb = c.out_stride[0]; a.o_st = c.out_stride[1]; a.o_sh = c.out_stride[2];
+  a.out32 = L.out32; a.lse = c.lse; a.k = c.k; a.v = c.v;
+  a.k_sb = c.k_stride[0]; a.k_sg = c.k_stride[1]; a.k_sr = c.k_stride[2];
+  a.v_sb = c.v_stride[0]; a.v_sg = c.v_stride[1]; a.v_sr = c.v_stride[2];
+  a.lens = c.lens; a.q_lens = c.q_lens; a.lens_add = L.lens_add;
+  a.B = c.B; a.Tq = c.Tq; a.H = c.H; a.Hkv = c.Hkv; a.G = c.H / c.Hkv; a.P = c.P; a.S = c.S;
+  a.scale2 = c.scale * kLog2e;
+  a.rb_p = p.rb_p; a.n_p = p.n_p; a.rb_s = p.rb_s; a.n_s = p.n_s;
+  a.items_p = p.rb_p * p.n_p * c.Hkv;
+  a.rows = static_cast<long long>(p.rows);
+  a.part_o = static_cast<float*>(scratch);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) +
+                                        align256_sz(static_cast<size_t>(p.n_p + p.n_s) * p.rows * c.hd * 4));
+  CUtensorMap m[4] = {};
+  if (c.P > 0) {
+    if (!encode_tmap_rows(&m[0], c.k_prefix, c.hd, c.P, c.Hkv, 1, c.kp_stride[1], c.kp_stride[0], 0, kPxTile) ||
+        !encode_tmap_rows(&m[1], c.v_prefix, c.hd, c.P, c.Hkv, 1, c.vp_stride[1], c.vp_stride[0], 0, kPxTile))
+      return cudaErrorInvalidValue;
+  }
+  if (c.S > 0) {
+    if (!encode_tmap_rows(&m[2], c.k, c.hd, c.S, c.Hkv, c.B, c.k_stride[2], c.k_stride[1], c.k_stride[0], kPxTile) ||
+        !encode_tmap_rows(&m[3], c.v, c.hd, c.S, c.Hkv, c.B, c.v_stride[2], c.v_stride[1], c.v_stride[0], kPxTile))
+      return cudaErrorInvalidValue;
+  }
+  if (c.P == 0) m[0] = m[2], m[1] = m[3];
+  if (c.S == 0) m[2] = m[0], m[3] = m[1];
+  const long long grid = a.items_p + static_cast<long long>(p.rb_s) * p.n_s * c.Hkv * c.B;
+  bool pdl = L.pdl;
+  if (grid > 0) {
+    e = c.hd == 128 ? run_split_hd<128>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s)
+                    : run_split_hd<64>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s);
+    if (e != cudaSuccess) return e;
+    pdl = true;
+  }
+  const dim3 mg(static_cast<unsigned>(p.rows));
+  if (c.hd == 128)
+    return L.q32 ? launch_k(pdl, k_prefix_merge<128, true>, mg, dim3(128), 0, s, a)
+                 : launch_k(pdl, k_prefix_merge<128, false>, mg, dim3(128), 0, s, a);
+  return L.q32 ? launch_k(pdl, k_prefix_merge<64, true>, mg, dim3(128), 0, s, a)
+               : launch_k(pdl, k_prefix_merge<64, false>, mg, dim3(128), 0, s, a);
+}
+
+}  // namespace fl
+
+using namespace fl;
+
+namespace {
+// Head shapes that the attention operators take.
+bool heads_ok(int B, int Tq, int H, int Hkv, int hd) {
+  return B >= 1 && Tq >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= kMaxGroup && (hd == 64 || hd == 128) &&
+         Hkv <= 65535 && B <= 65535 && static_cast<long long>(B) * Tq * H <= (1LL << 30);
+}
+}  // namespace
+
+extern "C" {
+
+size_t flashloop_prefix_attention_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
+  if (!heads_ok(B, Tq, H, Hkv, hd) || Tq > kMaxTq || P < 0 || S < 0) return 0;
+  return prefix_scratch_bytes(B, Tq, H, Hkv, hd, P, S);
+}
+
+fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scratch, size_t scratch_bytes,
+                                     fl_stream_t stream) {
+  if (!a) return refuse(FL_ERR_INVALID_ARG, "NULL arguments");
+  if (!heads_ok(a->B, a->Tq, a->H, a->Hkv, a->hd) || a->Tq > kMaxTq || a->P < 0 || a->S < 0)
+    return refuse(FL_ERR_INVALID_ARG, "B, Tq (<= 64), H, Hkv (H % Hkv == 0, H / Hkv <= 64), hd (64 or 128), P or S out of range");
+  if (!std::isfinite(a->scale)) return refuse(FL_ERR_INVALID_ARG, "scale must be finite");
+  if (!a->q || !a->out || !is_aligned(a->q, 16) || !is_aligned(a->out, 16) || !is_aligned(a->lse, 4) ||
+      !is_aligned(a->q_lens, 4))
+    return refuse(FL_ERR_INVALID_ARG, "q and out must be non-NULL and 16-byte aligned, lse and q_lens 4-byte aligned");
+  if (a->P > 0 && (!a->k_prefix || !a->v_prefix || !is_aligned(a->k_prefix, 16) || !is_aligned(a->v_prefix, 16)))
+    return refuse(FL_ERR_INVALID_ARG, "k_prefix and v_prefix must be non-NULL and 16-byte aligned when P > 0");
+  if (a->S > 0 && (!a->k || !a->v || !a->lens || !is_aligned(a->k, 16) || !is_aligned(a->v, 16) || !is_aligned(a->lens, 4)))
+    return refuse(FL_ERR_INVALID_ARG, "k, v (16-byte aligned) and lens must be non-NULL when S > 0");
+  const int64_t qd[3] = {a->B, a->Tq, a->H}, kd[3] = {a->B, a->Hkv, a->S}, pd[2] = {a->Hkv, a->P};
+  for (int i = 0; i < 3; ++i) {
+    if (!stride_ok(a->q_stride[i], qd[i], 8) || !stride_ok(a->out_stride[i], qd[i], 8))
+      return refuse(FL_ERR_INVALID_ARG, "q and out strides must be positive multiples of 8");
+    if (a->S > 0 && (!stride_ok(a->k_stride[i], kd[i], 8) || !stride_ok(a->v_stride[i], kd[i], 8)))
+      return refuse(FL_ERR_INVALID_ARG, "k and v strides must be positive multiples of 8");
+    if (i < 2 && a->P > 0 && (!stride_ok(a->kp_stride[i], pd[i], 8) || !stride_ok(a->vp_stride[i], pd[i], 8)))
+      return refuse(FL_ERR_INVALID_ARG, "k_prefix and v_prefix strides must be positive multiples of 8");
+  }
+  const size_t need = prefix_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->P, a->S);
+  if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
+    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+  PrefixLaunch L{};
+  L.a = *a;
+  return cuda_status(launch_prefix(L, scratch, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t flashloop_column_weights_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int S) {
+  if (!heads_ok(B, Tq, H, Hkv, hd) || S < 0) return 0;
+  return 256;
+}
+
+fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratch, size_t scratch_bytes,
+                                   fl_stream_t stream) {
+  if (!a) return refuse(FL_ERR_INVALID_ARG, "NULL arguments");
+  if (!heads_ok(a->B, a->Tq, a->H, a->Hkv, a->hd) || a->S < 0)
+    return refuse(FL_ERR_INVALID_ARG, "B, Tq, H, Hkv (H % Hkv == 0, H / Hkv <= 64), hd (64 or 128) or S out of range");
+  if (!std::isfinite(a->scale)) return refuse(FL_ERR_INVALID_ARG, "scale must be finite");
+  if (a->S == 0) return FL_OK;
+  if (!a->q || !a->k || !a->lse || !a->acc || !a->out || !is_aligned(a->q, 16) || !is_aligned(a->k, 16) ||
+      !is_aligned(a->lse, 4) || !is_aligned(a->acc, 4) || !is_aligned(a->out, 4) || !is_aligned(a->lens, 4) ||
+      !is_aligned(a->q_lens, 4))
+    return refuse(FL_ERR_INVALID_ARG, "q and k must be 16-byte aligned, lse, acc, out, lens and q_lens 4-byte aligned");
+  const int64_t qd[3] = {a->B, a->Tq, a->H}, kd[3] = {a->B, a->Hkv, a->S};
+  for (int i = 0; i < 3; ++i)
+    if (!stride_ok(a->q_stride[i], qd[i], 8) || !stride_ok(a->k_stride[i], kd[i], 8))
+      return refuse(FL_ERR_INVALID_ARG, "q and k strides must be positive multiples of 8");
+  const size_t need = flashloop_column_weights_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->S);
+  if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
+    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+  cudaError_t e = serving_init_attrs();
+  if (e != cudaSuccess) return cuda_status(e);
+  WeightsArgs w{};
+  w.q = a->q; w.q_sb = a->q_stride[0]; w.q_st = a->q_stride[1]; w.q_sh = a->q_stride[2];
+  w.lse = a->lse; w.acc = a->acc; w.out = a->out; w.lens = a->lens; w.q_lens = a->lens ? a->q_lens : nullptr;
+  w.B = a->B; w.Tq = a->Tq; w.H = a->H; w.Hkv = a->Hkv; w.G = a->H / a->Hkv; w.S = a->S;
+  w.scale2 = a->scale * kLog2e;
+  CUtensorMap km;
+  if (!encode_tmap_rows(&km, a->k, a->hd, a->S, a->Hkv, a->B, a->k_stride[2], a->k_stride[1], a->k_stride[0], kCwCols))
+    return refuse(FL_ERR_INVALID_ARG, "tensor map encoding failed");
+  const dim3 grid(ceil_div_i(a->S, kCwCols), a->Hkv, a->B);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(a->hd == 128 ? launch_k(false, k_column_weights<128>, grid, dim3(128), weights_smem(128), s, km, w)
+                                  : launch_k(false, k_column_weights<64>, grid, dim3(128), weights_smem(64), s, km, w));
+}
+
+}  // extern "C"

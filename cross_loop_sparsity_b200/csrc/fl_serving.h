@@ -1,0 +1,48 @@
+// fl_serving.h -- what the serving operators' translation units share: argument
+// checks, the tensor maps of strided caches, and the prefix attention's launch
+// (also made by a context's decode step).
+#pragma once
+#include <string>
+
+#include "flashloop.h"
+#include "fl_internal.h"
+
+namespace fl {
+
+inline int ceil_div_i(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+inline size_t align256_sz(size_t v) { return (v + 255) & ~size_t(255); }
+inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Failures leave their reason where flashloop_last_cuda_error(NULL) reports it.
+inline fl_status refuse(fl_status st, const std::string& why) {
+  set_last_error(why);
+  return st;
+}
+inline fl_status cuda_status(cudaError_t e) {
+  return e == cudaSuccess ? FL_OK : refuse(FL_ERR_CUDA, cudaGetErrorString(e));
+}
+
+// A stride is usable when its dimension has one element or it is a positive multiple of `unit`.
+inline bool stride_ok(int64_t stride, int64_t dim, int64_t unit) {
+  return dim <= 1 || (stride > 0 && stride % unit == 0 && stride < (int64_t(1) << 38));
+}
+
+// Tensor map over bf16 rows [n2][n1][rows][hd] with element strides, 128-byte
+// swizzle, box 64 dims x box_rows rows.
+bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2,
+                      int64_t s_row, int64_t s1, int64_t s2, uint32_t box_rows);
+
+// The prefix attention as launched: the C arguments, or a context's decode step
+// (fp32 queries, an fp32 copy of the output, lengths offset by lens_add).
+struct PrefixLaunch {
+  flashloop_prefix_args a;
+  const float* q32;     // fp32 queries [B][Tq][H][hd] by q_stride (a.q unused), or nullptr
+  float* out32;         // fp32 copy of the output rows [B*Tq*H][hd], or nullptr
+  int lens_add;         // added to lens[b] before it is clamped
+  bool pdl;             // the first launch may overlap its predecessor
+};
+size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S);
+cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s);
+cudaError_t serving_init_attrs();   // opt the kernels in to their shared memory (per device)
+
+}  // namespace fl

@@ -57,6 +57,39 @@ class Weights(ctypes.Structure):
         ("prelude", Layers), ("coda", Layers), ("loop_embed", ctypes.c_void_p)]
 
 
+_I2 = ctypes.c_int64 * 2
+_I3 = ctypes.c_int64 * 3
+
+
+def _fields(names, kind):
+    return [(n, kind) for n in names.split()]
+
+
+class PrefixArgs(ctypes.Structure):
+    _fields_ = (_fields("q k_prefix v_prefix k v out lse lens q_lens", ctypes.c_void_p)
+                + _fields("B Tq H Hkv hd P S", ctypes.c_int) + [("scale", ctypes.c_float)]
+                + _fields("q_stride out_stride", _I3) + _fields("kp_stride vp_stride", _I2)
+                + _fields("k_stride v_stride", _I3))
+
+
+class WeightsArgs(ctypes.Structure):
+    _fields_ = (_fields("q k lse acc out lens q_lens", ctypes.c_void_p) + _fields("B Tq H Hkv hd S", ctypes.c_int)
+                + [("scale", ctypes.c_float)] + _fields("q_stride k_stride", _I3))
+
+
+class EvictArgs(ctypes.Structure):
+    _fields_ = (_fields("k v acc pos lens k_out v_out acc_out pos_out lens_out", ctypes.c_void_p)
+                + _fields("B Hkv S hd keep recent sinks", ctypes.c_int) + _fields("k_stride v_stride", _I3)
+                + _fields("acc_stride pos_stride", _I2) + _fields("k_out_stride v_out_stride", _I3)
+                + _fields("acc_out_stride pos_out_stride", _I2))
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = (_fields("logits draft_logits draft u n_draft tokens n_accepted", ctypes.c_void_p)
+                + _fields("B D V", ctypes.c_int) + [("temperature", ctypes.c_float)]
+                + _fields("logits_stride draft_logits_stride", _I2))
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SIG = {
@@ -92,6 +125,14 @@ _SIG = {
     "fl_test_gemm_scratch_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "fl_test_gemm": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, ctypes.c_size_t, _P]),
     "fl_gemm_skinny_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "flashloop_prefix_attention_scratch_bytes": (ctypes.c_size_t, [_I] * 7),
+    "flashloop_prefix_attention": (_I, [ctypes.POINTER(PrefixArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_column_weights_scratch_bytes": (ctypes.c_size_t, [_I] * 6),
+    "flashloop_column_weights": (_I, [ctypes.POINTER(WeightsArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_evict_scratch_bytes": (ctypes.c_size_t, [_I] * 4),
+    "flashloop_evict": (_I, [ctypes.POINTER(EvictArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_verify_draft_scratch_bytes": (ctypes.c_size_t, [_I] * 3),
+    "flashloop_verify_draft": (_I, [ctypes.POINTER(VerifyArgs), _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -459,3 +500,189 @@ def gemm_noalloc(A, B, out=None, stream=None):
     _check(lib().fl_gemm_skinny_noalloc(_ptr(A), _ptr(B), _ptr(D), m, n, k, _stream_ptr(stream)),
            "fl_gemm_skinny_noalloc")
     return D
+
+
+# ---------------------------------------------------------------------------- serving operators
+# Tensors stay where they are and are taken with their strides.  Work goes to
+# ``stream``, or to torch's current stream of the tensors' device, so the calls
+# may be captured with ``torch.cuda.graph``.  ``scratch`` (a uint8 cuda tensor of
+# the *_scratch_bytes figure, 256-byte aligned as torch allocates) is allocated
+# per call unless given; a decode loop keeps one.
+def _need(ok: bool, what: str, why: str):
+    if not ok:
+        raise FlashLoopError(1, what, why)
+
+
+def _take(what: str, name: str, t, dtype, shape, device, contiguous=False):
+    """Check one tensor argument and return its pointer (None stays None)."""
+    if t is None:
+        return None
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), what,
+          f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
+    _need(t.is_cuda and t.device == device, what, f"{name} must be on {device}")
+    if contiguous:
+        _need(t.is_contiguous(), what, f"{name} must be contiguous")
+    else:
+        _need(t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1, what, f"{name}'s last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _run(what: str, fn, args, nbytes: int, scratch, stream, device):
+    import torch
+    _need(nbytes > 0, what, "a size is out of range")
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream(device) if stream is None else stream
+        if scratch is None:
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if stream is not None:
+                scratch.record_stream(stream)   # the allocator must not reuse it under the call
+        _need(scratch.is_cuda and scratch.device == device and scratch.is_contiguous(), what,
+              f"scratch must be contiguous and on {device}")
+        _check(fn(ctypes.byref(args), scratch.data_ptr(), scratch.numel() * scratch.element_size(), s.cuda_stream), what)
+
+
+def prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S) -> int:
+    return int(lib().flashloop_prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S))
+
+
+def prefix_attention(q, k_prefix, v_prefix, k, v, lens, q_lens=None, scale=None, out=None, lse=None, scratch=None,
+                     stream=None):
+    """Attention of B sequences that share a prefix (``flashloop_prefix_attention``).
+
+    q: bf16 [B, Tq, H, hd], the last ``q_lens[b]`` (default Tq) tokens of each sequence; k_prefix,
+    v_prefix: bf16 [Hkv, P, hd], common to all, or None; k, v: bf16 [B, Hkv, S, hd], each
+    sequence's own rows after the prefix, ``lens[b]`` of them valid (the queries' own
+    included), or None.  scale defaults to hd ** -0.5.  Returns (out bf16 like q, lse fp32
+    [B, Tq, H]); rows t >= q_lens[b] of both keep what the given buffers hold (new
+    buffers: 0 and -inf)."""
+    import torch
+    what = "flashloop_prefix_attention"
+    _need(q.dim() == 4, what, "q must be [B, Tq, H, hd]")
+    B, Tq, H, hd = q.shape
+    dev, bf = q.device, torch.bfloat16
+    own, pre = k if k is not None else v, k_prefix if k_prefix is not None else v_prefix
+    _need(own is None or own.dim() == 4, what, "k and v must be [B, Hkv, S, hd]")
+    _need(pre is None or pre.dim() == 3, what, "k_prefix and v_prefix must be [Hkv, P, hd]")
+    _need(own is not None or pre is not None, what, "neither a prefix nor rows of the sequences' own")
+    Hkv = own.shape[1] if own is not None else pre.shape[0]
+    S, P = own.shape[2] if own is not None else 0, pre.shape[1] if pre is not None else 0
+    if out is None:
+        out = torch.zeros((B, Tq, H, hd), dtype=bf, device=dev) if q_lens is not None else torch.empty(
+            (B, Tq, H, hd), dtype=bf, device=dev)
+    if lse is None:
+        lse = torch.full((B, Tq, H), -float("inf"), device=dev)
+    a = PrefixArgs(_take(what, "q", q, bf, (B, Tq, H, hd), dev),
+                   _take(what, "k_prefix", k_prefix, bf, (Hkv, P, hd), dev),
+                   _take(what, "v_prefix", v_prefix, bf, (Hkv, P, hd), dev),
+                   _take(what, "k", k, bf, (B, Hkv, S, hd), dev), _take(what, "v", v, bf, (B, Hkv, S, hd), dev),
+                   _take(what, "out", out, bf, (B, Tq, H, hd), dev),
+                   _take(what, "lse", lse, torch.float32, (B, Tq, H), dev, True),
+                   _take(what, "lens", lens, torch.int32, (B,), dev, True),
+                   _take(what, "q_lens", q_lens, torch.int32, (B,), dev, True),
+                   B, Tq, H, Hkv, hd, P, S, hd ** -0.5 if scale is None else scale,
+                   _I3(*q.stride()[:3]), _I3(*out.stride()[:3]),
+                   _I2(*k_prefix.stride()[:2]) if k_prefix is not None else _I2(),
+                   _I2(*v_prefix.stride()[:2]) if v_prefix is not None else _I2(),
+                   _I3(*k.stride()[:3]) if k is not None else _I3(), _I3(*v.stride()[:3]) if v is not None else _I3())
+    _run(what, lib().flashloop_prefix_attention, a, prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S), scratch,
+         stream, dev)
+    return out, lse
+
+
+def column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S) -> int:
+    return int(lib().flashloop_column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S))
+
+
+def column_weights(q, k, lse, acc, lens=None, q_lens=None, scale=None, out=None, scratch=None, stream=None):
+    """acc plus the attention weight of every key column (``flashloop_column_weights``).
+
+    q: bf16 [B, Tq, H, hd]; k: bf16 [B, Hkv, S, hd]; lse: fp32 [B, Tq, H], as
+    ``prefix_attention`` returns it; acc: fp32 [B, Hkv, S].  lens (with q_lens): causal, as there;
+    None: every query sees every column.  ``out=acc`` adds in place.  The columns of a
+    shared prefix are one sequence of B * Tq queries:
+    ``column_weights(q.view(1, B * Tq, H, hd), k_prefix[None], lse.view(1, B * Tq, H), acc_prefix[None])``;
+    queries whose lse is -inf add nothing."""
+    import torch
+    what = "flashloop_column_weights"
+    _need(q.dim() == 4 and k.dim() == 4, what, "q must be [B, Tq, H, hd] and k [B, Hkv, S, hd]")
+    B, Tq, H, hd = q.shape
+    Hkv, S, dev, f32 = k.shape[1], k.shape[2], q.device, torch.float32
+    _need(q_lens is None or lens is not None, what, "q_lens goes with lens")
+    if out is None:
+        out = torch.empty((B, Hkv, S), device=dev)
+    a = WeightsArgs(_take(what, "q", q, torch.bfloat16, (B, Tq, H, hd), dev),
+                    _take(what, "k", k, torch.bfloat16, (B, Hkv, S, hd), dev),
+                    _take(what, "lse", lse, f32, (B, Tq, H), dev, True),
+                    _take(what, "acc", acc, f32, (B, Hkv, S), dev, True),
+                    _take(what, "out", out, f32, (B, Hkv, S), dev, True),
+                    _take(what, "lens", lens, torch.int32, (B,), dev, True),
+                    _take(what, "q_lens", q_lens, torch.int32, (B,), dev, True),
+                    B, Tq, H, Hkv, hd, S, hd ** -0.5 if scale is None else scale, _I3(*q.stride()[:3]),
+                    _I3(*k.stride()[:3]))
+    _run(what, lib().flashloop_column_weights, a, column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S), scratch, stream,
+         dev)
+    return out
+
+
+def evict_scratch_bytes(B, Hkv, S, keep) -> int:
+    return int(lib().flashloop_evict_scratch_bytes(B, Hkv, S, keep))
+
+
+def evict(k, v, acc, pos, lens, keep: int, recent: int = 0, sinks: int = 0, out=None, scratch=None, stream=None):
+    """Keep the ``keep`` columns of most accumulated weight of every (sequence, KV head) (``flashloop_evict``).
+
+    k, v: [B, Hkv, S, hd] of a 2-byte type; acc: fp32, pos: int32 [B, Hkv, S]; lens: int32 [B].  The
+    ``recent`` newest tokens (by pos) and those at pos < ``sinks`` are always kept.  In place,
+    or into out = (k, v, acc, pos, lens) with ``keep`` slots per head.  Returns those five."""
+    import torch
+    what = "flashloop_evict"
+    _need(k.dim() == 4 and k.element_size() == 2, what, "k must be [B, Hkv, S, hd] of a 2-byte type")
+    B, Hkv, S, hd = k.shape
+    dev, f32, i32 = k.device, torch.float32, torch.int32
+    n = S if out is None else keep
+    ko, vo, ao, po, lo = (k, v, acc, pos, lens) if out is None else out
+    a = EvictArgs(_take(what, "k", k, k.dtype, (B, Hkv, S, hd), dev), _take(what, "v", v, k.dtype, (B, Hkv, S, hd), dev),
+                  _take(what, "acc", acc, f32, (B, Hkv, S), dev), _take(what, "pos", pos, i32, (B, Hkv, S), dev),
+                  _take(what, "lens", lens, i32, (B,), dev, True),
+                  _take(what, "out k", ko, k.dtype, (B, Hkv, n, hd), dev),
+                  _take(what, "out v", vo, k.dtype, (B, Hkv, n, hd), dev),
+                  _take(what, "out acc", ao, f32, (B, Hkv, n), dev), _take(what, "out pos", po, i32, (B, Hkv, n), dev),
+                  _take(what, "out lens", lo, i32, (B,), dev, True), B, Hkv, S, hd, keep, recent, sinks,
+                  _I3(*k.stride()[:3]), _I3(*v.stride()[:3]), _I2(*acc.stride()[:2]), _I2(*pos.stride()[:2]),
+                  _I3(*ko.stride()[:3]), _I3(*vo.stride()[:3]), _I2(*ao.stride()[:2]), _I2(*po.stride()[:2]))
+    _run(what, lib().flashloop_evict, a, evict_scratch_bytes(B, Hkv, S, keep), scratch, stream, dev)
+    return ko, vo, ao, po, lo
+
+
+def verify_draft_scratch_bytes(B, D, V) -> int:
+    return int(lib().flashloop_verify_draft_scratch_bytes(B, D, V))
+
+
+def verify_draft(logits, draft_logits, draft, u, n_draft=None, temperature: float = 1.0, tokens=None, n_accepted=None,
+                 scratch=None, stream=None):
+    """Verify drafted tokens and sample the next one (``flashloop_verify_draft``).
+
+    logits: fp32 [B, D + 1, V], the target's at every drafted position and after the last;
+    draft_logits: fp32 [B, D, V], or None (a draft without probabilities); draft: int32 [B, D]; u: fp32
+    [B, D + 1] uniform in [0, 1), the last column for the sampled token (None when greedy);
+    n_draft: int32 [B], or None for D; temperature 0: greedy.  Returns (tokens int32
+    [B, D + 1], padded with -1; n_accepted int32 [B])."""
+    import torch
+    what = "flashloop_verify_draft"
+    _need(logits.dim() == 3 and logits.shape[1] >= 1, what, "logits must be [B, D + 1, V]")
+    B, D, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+    dev, f32, i32 = logits.device, torch.float32, torch.int32
+    if tokens is None:
+        tokens = torch.empty((B, D + 1), dtype=i32, device=dev)
+    if n_accepted is None:
+        n_accepted = torch.empty((B,), dtype=i32, device=dev)
+    a = VerifyArgs(_take(what, "logits", logits, f32, (B, D + 1, V), dev),
+                   _take(what, "draft_logits", draft_logits, f32, (B, D, V), dev) if D else None,
+                   _take(what, "draft", draft, i32, (B, D), dev, True) if D else None,
+                   _take(what, "u", u, f32, (B, D + 1), dev, True),
+                   _take(what, "n_draft", n_draft, i32, (B,), dev, True),
+                   _take(what, "tokens", tokens, i32, (B, D + 1), dev, True),
+                   _take(what, "n_accepted", n_accepted, i32, (B,), dev, True), B, D, V, temperature,
+                   _I2(*logits.stride()[:2]), _I2(*draft_logits.stride()[:2]) if D and draft_logits is not None else _I2())
+    _run(what, lib().flashloop_verify_draft, a, verify_draft_scratch_bytes(B, D, V), scratch, stream, dev)
+    return tokens, n_accepted

@@ -347,6 +347,152 @@ fl_status fl_test_gemm(const uint16_t* A, const uint16_t* B, float* D, int m, in
 fl_status fl_gemm_skinny_noalloc(const uint16_t* A, const uint16_t* B, float* D, int m, int n, int k,
                                  fl_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Serving operators on caller buffers (device pointers): what a decode loop  */
+/* does around the step for many samples of one prompt.  The paper has no    */
+/* counterpart; the definitions are below.  Common rules:                    */
+/*  - strides are in elements; the innermost dimension is contiguous and      */
+/*    every other stride of a dimension longer than one is a positive         */
+/*    multiple of 8; pointers are 16-byte aligned where not said otherwise.   */
+/*  - lengths in device memory (lens, q_lens, n_draft) are clamped to the     */
+/*    range the shapes allow, so a bad value never reaches outside a buffer.  */
+/*  - scratch (256-byte aligned, at least the *_scratch_bytes figure) carries  */
+/*    nothing between calls and needs no initialisation; calls that may run   */
+/*    at the same time need one each.  The buffers belong to the current      */
+/*    device.  Every call may be captured into a CUDA graph.                  */
+/*  - outputs may not overlap inputs or each other except where stated.       */
+/*  - a refused call launches nothing; its reason is                          */
+/*    flashloop_last_cuda_error(NULL).                                        */
+/* ------------------------------------------------------------------------ */
+
+/* Attention of a batch whose sequences share a prefix.  Query (b, t, h) reads,
+ * with KV head g = h / (H / Hkv), the P rows of the shared prefix and rows
+ * j <= lens[b] - q_lens[b] + t (j < lens[b]) of its sequence's own cache: its
+ * queries are the last q_lens[b] tokens of that cache, causally masked.
+ *   out = softmax(scale * q . [Kprefix, K]) [Vprefix, V],  lse = log sum exp
+ * bf16 inputs and output, fp32 sums, P rounded to bf16 in front of the product
+ * with V.  A query that sees nothing gets out = 0 and lse = -inf.  Rows t >=
+ * q_lens[b] of out and lse are left as they were.  K / V rows past a query's
+ * last visible one are never used, whatever they hold.
+ *   q, out [B][Tq][H][hd]; k_prefix, v_prefix [Hkv][P][hd]; k, v [B][Hkv][S][hd]
+ *   lse fp32 [B][Tq][H] contiguous, or NULL; lens int32 [B]; q_lens int32 [B], or NULL for Tq.
+ * Limits: hd 64 or 128, H / Hkv <= 64, 1 <= Tq <= 64, P >= 0, S >= 0 (k_prefix and
+ * v_prefix, or k, v and lens, may be NULL where P, or S, is 0). */
+typedef struct {
+  const uint16_t* q;
+  const uint16_t* k_prefix;
+  const uint16_t* v_prefix;
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* out;
+  float* lse;
+  const int32_t* lens;
+  const int32_t* q_lens;
+  int B, Tq, H, Hkv, hd, P, S;
+  float scale;
+  int64_t q_stride[3];   /* of b, t, h */
+  int64_t out_stride[3]; /* of b, t, h */
+  int64_t kp_stride[2];  /* of g, row; likewise vp_stride */
+  int64_t vp_stride[2];
+  int64_t k_stride[3];   /* of b, g, row; likewise v_stride */
+  int64_t v_stride[3];
+} flashloop_prefix_args;
+size_t flashloop_prefix_attention_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S);
+fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scratch, size_t scratch_bytes,
+                                     fl_stream_t stream);
+
+/* Attention weight of every key column, added to a running sum:
+ *   out[b][g][j] = acc[b][g][j] + sum over queries (t, h in group g) that see j of
+ *                  exp(scale * q[b][t][h] . k[b][g][j] - lse[b][t][h])
+ * in fp32.  lens NULL: every query sees every column; otherwise query t < q_lens[b]
+ * sees j <= lens[b] - q_lens[b] + t, j < lens[b], as in flashloop_prefix_attention, whose lse it takes.
+ * A query whose lse is -inf adds nothing.  Columns that no query sees keep acc's
+ * value.  (A shared prefix is one sequence, B = 1, of B * Tq queries, lens NULL.)
+ *   q bf16 [B][Tq][H][hd]; k bf16 [B][Hkv][S][hd]; lse fp32 [B][Tq][H], acc and out
+ *   fp32 [B][Hkv][S], contiguous; out may be acc.
+ * Limits: hd 64 or 128, H / Hkv <= 64, Tq >= 1, S >= 0. */
+typedef struct {
+  const uint16_t* q;
+  const uint16_t* k;
+  const float* lse;
+  const float* acc;
+  float* out;
+  const int32_t* lens;
+  const int32_t* q_lens;
+  int B, Tq, H, Hkv, hd, S;
+  float scale;
+  int64_t q_stride[3]; /* of b, t, h */
+  int64_t k_stride[3]; /* of b, g, row */
+} flashloop_weights_args;
+size_t flashloop_column_weights_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int S);
+fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratch, size_t scratch_bytes,
+                                   fl_stream_t stream);
+
+/* Evict the columns of least accumulated weight from a cache.  Per (sequence b,
+ * KV head g) with n = lens[b] > keep columns, the `keep` columns kept are the
+ * first in this order: protected ones (pos < sinks, or pos > the largest pos
+ * among the n columns - recent), then by acc descending -- compared as IEEE bit patterns
+ * (uint32), like the other selections; acc holds sums of weights, never
+ * negative -- then by slot ascending.  A kept column in a slot < keep stays there; the slots < keep
+ * freed by the others take the kept columns from slots >= keep, both in ascending
+ * slot order: what moves is as little as can be, and pos says which token a slot
+ * holds.  n <= keep keeps everything.  lens_out[b] = min(lens[b], keep).
+ *   k, v [B][Hkv][S][hd] (any 2-byte type; hd a multiple of 8, <= 1024); acc fp32 and pos int32 [B][Hkv][S];
+ *   lens int32 [B]; *_out alike with `keep` slots, or the inputs' own pointers: then the cache is
+ *   compacted in place, with the inputs' strides.  Slots from lens_out[b] on are left as they were.
+ * acc and pos (and their outputs) have contiguous rows, 4-byte aligned, with strides of b and g.
+ * Limits: keep >= 1, recent >= 0, sinks >= 0, recent + sinks <= keep; all outputs in place, or none. */
+typedef struct {
+  const uint16_t* k;
+  const uint16_t* v;
+  const float* acc;
+  const int32_t* pos;
+  const int32_t* lens;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  float* acc_out;
+  int32_t* pos_out;
+  int32_t* lens_out;
+  int B, Hkv, S, hd, keep, recent, sinks;
+  int64_t k_stride[3], v_stride[3];         /* of b, g, row */
+  int64_t acc_stride[2], pos_stride[2];     /* of b, g */
+  int64_t k_out_stride[3], v_out_stride[3];
+  int64_t acc_out_stride[2], pos_out_stride[2];
+} flashloop_evict_args;
+size_t flashloop_evict_scratch_bytes(int B, int Hkv, int S, int keep);
+fl_status flashloop_evict(const flashloop_evict_args* a, void* scratch, size_t scratch_bytes, fl_stream_t stream);
+
+/* Verify drafted tokens against the target model, from given random numbers.
+ * With p_i = softmax(logits[b][i] / temperature), q_i = softmax(draft_logits[b][i] /
+ * temperature), x_i = draft[b][i] and n = n_draft[b]: draft i < n is accepted
+ * while u[b][i] * q_i(x_i) < p_i(x_i); with m the number accepted, tokens[b] =
+ * x_0 .. x_{m-1}, y, -1 .. -1, n_accepted[b] = m, and y the smallest index whose
+ * running sum exceeds u[b][D] times the total of max(p_m - q_m, 0) (of p_m when m = n).
+ * Sums that decide are formed in 64 bits.  draft_logits NULL: a draft without
+ * probabilities (q_i one at x_i).  temperature 0: draft i is accepted while it is
+ * the argmax of logits[b][i] (ties to the lowest index; NaN ignored), y the argmax
+ * of row m; u and draft_logits are not read.  A draft token outside [0, V) is rejected.  y = -1 when the
+ * row's distribution is not finite or empty (NaN, +inf, or no finite logit).
+ *   logits fp32 [B][D+1][V], draft_logits fp32 [B][D][V]: rows contiguous, 4-byte aligned, strides of b and i;
+ *   draft int32 [B][D]; u fp32 [B][D+1] in [0, 1); n_draft int32 [B] or NULL for D;
+ *   tokens int32 [B][D+1]; n_accepted int32 [B], all contiguous.
+ * Limits: 0 <= D <= 64 (D = 0 samples one token), 1 <= V, temperature >= 0 and finite. */
+typedef struct {
+  const float* logits;
+  const float* draft_logits;
+  const int32_t* draft;
+  const float* u;
+  const int32_t* n_draft;
+  int32_t* tokens;
+  int32_t* n_accepted;
+  int B, D, V;
+  float temperature;
+  int64_t logits_stride[2], draft_logits_stride[2]; /* of b, i */
+} flashloop_verify_args;
+size_t flashloop_verify_draft_scratch_bytes(int B, int D, int V);
+fl_status flashloop_verify_draft(const flashloop_verify_args* a, void* scratch, size_t scratch_bytes,
+                                 fl_stream_t stream);
+
 /* Runtime options of a context. */
 typedef enum {
   FL_OPT_USE_GRAPH = 1, /* 1 (default): capture decode steps into CUDA graphs; 0: launch directly */
