@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -126,13 +127,13 @@ _SIG = {
     "fl_test_gemm": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, ctypes.c_size_t, _P]),
     "fl_gemm_skinny_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _P]),
     "flashloop_prefix_attention_scratch_bytes": (ctypes.c_size_t, [_I] * 7),
-    "flashloop_prefix_attention": (_I, [ctypes.POINTER(PrefixArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_prefix_attention": (_I, [_P, _P, ctypes.c_size_t, _P]),
     "flashloop_column_weights_scratch_bytes": (ctypes.c_size_t, [_I] * 6),
-    "flashloop_column_weights": (_I, [ctypes.POINTER(WeightsArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_column_weights": (_I, [_P, _P, ctypes.c_size_t, _P]),
     "flashloop_evict_scratch_bytes": (ctypes.c_size_t, [_I] * 4),
-    "flashloop_evict": (_I, [ctypes.POINTER(EvictArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_evict": (_I, [_P, _P, ctypes.c_size_t, _P]),
     "flashloop_verify_draft_scratch_bytes": (ctypes.c_size_t, [_I] * 3),
-    "flashloop_verify_draft": (_I, [ctypes.POINTER(VerifyArgs), _P, ctypes.c_size_t, _P]),
+    "flashloop_verify_draft": (_I, [_P, _P, ctypes.c_size_t, _P]),
 }
 
 _lib = None
@@ -508,37 +509,71 @@ def gemm_noalloc(A, B, out=None, stream=None):
 # may be captured with ``torch.cuda.graph``.  ``scratch`` (a uint8 cuda tensor of
 # the *_scratch_bytes figure, 256-byte aligned as torch allocates) is allocated
 # per call unless given; a decode loop keeps one.
+#
+# A call's argument block is its pointers followed by sizes and strides.  The
+# second part depends on shapes, strides and types alone: it is checked and built
+# once for each of those and kept, so a repeated call only looks it up and adds
+# the pointers (a few microseconds of a call that may itself take as few).
+_blocks: dict = {}
+_MAX_BLOCKS = 4096
+
+
 def _need(ok: bool, what: str, why: str):
     if not ok:
         raise FlashLoopError(1, what, why)
 
 
-def _take(what: str, name: str, t, dtype, shape, device, contiguous=False):
-    """Check one tensor argument and return its pointer (None stays None)."""
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _check_tensor(what: str, name: str, t, dtype, shape, device: int, contiguous=False):
     if t is None:
-        return None
+        return
     _need(t.dtype == dtype and tuple(t.shape) == tuple(shape), what,
           f"{name} must be {dtype} {list(shape)}, not {t.dtype} {list(t.shape)}")
-    _need(t.is_cuda and t.device == device, what, f"{name} must be on {device}")
+    _need(t.is_cuda and t.get_device() == device, what, f"{name} must be on cuda device {device}")
     if contiguous:
         _need(t.is_contiguous(), what, f"{name} must be contiguous")
     else:
-        _need(t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1, what, f"{name}'s last dimension must be contiguous")
-    return t.data_ptr()
+        _need(t.shape[-1] <= 1 or t.stride(-1) == 1, what, f"{name}'s last dimension must be contiguous")
 
 
-def _run(what: str, fn, args, nbytes: int, scratch, stream, device):
+def _block(key, make):
+    """The (bytes after the pointers, scratch bytes) of an argument block, made on first use."""
+    got = _blocks.get(key)
+    if got is None:
+        args, n_ptr, nbytes = make()
+        _need(nbytes > 0, key[0], "a size is out of range")
+        if len(_blocks) >= _MAX_BLOCKS:
+            _blocks.clear()
+        got = _blocks[key] = (bytes(args)[8 * n_ptr:], nbytes)
+    return got
+
+
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _run(what: str, fn, ptrs: bytes, block, scratch, stream, device: int):
     import torch
-    _need(nbytes > 0, what, "a size is out of range")
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        if scratch is None:
-            scratch = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            if stream is not None:
-                scratch.record_stream(stream)   # the allocator must not reuse it under the call
-        _need(scratch.is_cuda and scratch.device == device and scratch.is_contiguous(), what,
-              f"scratch must be contiguous and on {device}")
-        _check(fn(ctypes.byref(args), scratch.data_ptr(), scratch.numel() * scratch.element_size(), s.cuda_stream), what)
+    tail, nbytes = block
+    if torch._C._cuda_getDevice() != device:
+        with torch.cuda.device(device):
+            return _run(what, fn, ptrs, block, scratch, stream, device)
+    if scratch is None:
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+        if stream is not None:
+            scratch.record_stream(stream)   # the allocator must not reuse it under the call
+    elif scratch.get_device() != device or not scratch.is_contiguous():
+        raise FlashLoopError(1, what, f"scratch must be contiguous and on cuda device {device}")
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    st = fn(ptrs + tail, scratch.data_ptr(), scratch.nbytes, s)
+    if st != FL_OK:
+        _check(st, what)
+
+
+_ptrs7, _ptrs9, _ptrs10 = (struct.Struct(f"={n}Q").pack for n in (7, 9, 10))
 
 
 def prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S) -> int:
@@ -558,34 +593,42 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, lens, q_lens=None, scale=None,
     import torch
     what = "flashloop_prefix_attention"
     _need(q.dim() == 4, what, "q must be [B, Tq, H, hd]")
-    B, Tq, H, hd = q.shape
-    dev, bf = q.device, torch.bfloat16
-    own, pre = k if k is not None else v, k_prefix if k_prefix is not None else v_prefix
-    _need(own is None or own.dim() == 4, what, "k and v must be [B, Hkv, S, hd]")
-    _need(pre is None or pre.dim() == 3, what, "k_prefix and v_prefix must be [Hkv, P, hd]")
-    _need(own is not None or pre is not None, what, "neither a prefix nor rows of the sequences' own")
-    Hkv = own.shape[1] if own is not None else pre.shape[0]
-    S, P = own.shape[2] if own is not None else 0, pre.shape[1] if pre is not None else 0
     if out is None:
-        out = torch.zeros((B, Tq, H, hd), dtype=bf, device=dev) if q_lens is not None else torch.empty(
-            (B, Tq, H, hd), dtype=bf, device=dev)
+        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device) if q_lens is not None else torch.empty(
+            q.shape, dtype=torch.bfloat16, device=q.device)
     if lse is None:
-        lse = torch.full((B, Tq, H), -float("inf"), device=dev)
-    a = PrefixArgs(_take(what, "q", q, bf, (B, Tq, H, hd), dev),
-                   _take(what, "k_prefix", k_prefix, bf, (Hkv, P, hd), dev),
-                   _take(what, "v_prefix", v_prefix, bf, (Hkv, P, hd), dev),
-                   _take(what, "k", k, bf, (B, Hkv, S, hd), dev), _take(what, "v", v, bf, (B, Hkv, S, hd), dev),
-                   _take(what, "out", out, bf, (B, Tq, H, hd), dev),
-                   _take(what, "lse", lse, torch.float32, (B, Tq, H), dev, True),
-                   _take(what, "lens", lens, torch.int32, (B,), dev, True),
-                   _take(what, "q_lens", q_lens, torch.int32, (B,), dev, True),
-                   B, Tq, H, Hkv, hd, P, S, hd ** -0.5 if scale is None else scale,
-                   _I3(*q.stride()[:3]), _I3(*out.stride()[:3]),
-                   _I2(*k_prefix.stride()[:2]) if k_prefix is not None else _I2(),
-                   _I2(*v_prefix.stride()[:2]) if v_prefix is not None else _I2(),
-                   _I3(*k.stride()[:3]) if k is not None else _I3(), _I3(*v.stride()[:3]) if v is not None else _I3())
-    _run(what, lib().flashloop_prefix_attention, a, prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S), scratch,
-         stream, dev)
+        lse = torch.full(q.shape[:3], -float("inf"), device=q.device)
+    dev = q.get_device()
+
+    def make():
+        B, Tq, H, hd = q.shape
+        own, pre = k if k is not None else v, k_prefix if k_prefix is not None else v_prefix
+        _need(own is None or own.dim() == 4, what, "k and v must be [B, Hkv, S, hd]")
+        _need(pre is None or pre.dim() == 3, what, "k_prefix and v_prefix must be [Hkv, P, hd]")
+        _need(own is not None or pre is not None, what, "neither a prefix nor rows of the sequences' own")
+        Hkv = own.shape[1] if own is not None else pre.shape[0]
+        S, P = own.shape[2] if own is not None else 0, pre.shape[1] if pre is not None else 0
+        bf = torch.bfloat16
+        for name, t, dt, shape, contiguous in (
+                ("q", q, bf, (B, Tq, H, hd), False), ("out", out, bf, (B, Tq, H, hd), False),
+                ("k_prefix", k_prefix, bf, (Hkv, P, hd), False), ("v_prefix", v_prefix, bf, (Hkv, P, hd), False),
+                ("k", k, bf, (B, Hkv, S, hd), False), ("v", v, bf, (B, Hkv, S, hd), False),
+                ("lse", lse, torch.float32, (B, Tq, H), True), ("lens", lens, torch.int32, (B,), True),
+                ("q_lens", q_lens, torch.int32, (B,), True)):
+            _check_tensor(what, name, t, dt, shape, dev, contiguous)
+        a = PrefixArgs(*[None] * 9, B, Tq, H, Hkv, hd, P, S, hd ** -0.5 if scale is None else scale,
+                       _I3(*q.stride()[:3]), _I3(*out.stride()[:3]),
+                       _I2(*k_prefix.stride()[:2]) if k_prefix is not None else _I2(),
+                       _I2(*v_prefix.stride()[:2]) if v_prefix is not None else _I2(),
+                       _I3(*k.stride()[:3]) if k is not None else _I3(),
+                       _I3(*v.stride()[:3]) if v is not None else _I3())
+        return a, 9, prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S)
+
+    block = _block((what, scale, _sig(q), _sig(k_prefix), _sig(v_prefix), _sig(k), _sig(v), _sig(out), _sig(lse),
+                    _sig(lens), _sig(q_lens)), make)
+    _run(what, lib().flashloop_prefix_attention,
+         _ptrs9(q.data_ptr(), _addr(k_prefix), _addr(v_prefix), _addr(k), _addr(v), out.data_ptr(), lse.data_ptr(),
+                _addr(lens), _addr(q_lens)), block, scratch, stream, dev)
     return out, lse
 
 
@@ -604,23 +647,30 @@ def column_weights(q, k, lse, acc, lens=None, q_lens=None, scale=None, out=None,
     queries whose lse is -inf add nothing."""
     import torch
     what = "flashloop_column_weights"
-    _need(q.dim() == 4 and k.dim() == 4, what, "q must be [B, Tq, H, hd] and k [B, Hkv, S, hd]")
-    B, Tq, H, hd = q.shape
-    Hkv, S, dev, f32 = k.shape[1], k.shape[2], q.device, torch.float32
-    _need(q_lens is None or lens is not None, what, "q_lens goes with lens")
     if out is None:
-        out = torch.empty((B, Hkv, S), device=dev)
-    a = WeightsArgs(_take(what, "q", q, torch.bfloat16, (B, Tq, H, hd), dev),
-                    _take(what, "k", k, torch.bfloat16, (B, Hkv, S, hd), dev),
-                    _take(what, "lse", lse, f32, (B, Tq, H), dev, True),
-                    _take(what, "acc", acc, f32, (B, Hkv, S), dev, True),
-                    _take(what, "out", out, f32, (B, Hkv, S), dev, True),
-                    _take(what, "lens", lens, torch.int32, (B,), dev, True),
-                    _take(what, "q_lens", q_lens, torch.int32, (B,), dev, True),
-                    B, Tq, H, Hkv, hd, S, hd ** -0.5 if scale is None else scale, _I3(*q.stride()[:3]),
-                    _I3(*k.stride()[:3]))
-    _run(what, lib().flashloop_column_weights, a, column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S), scratch, stream,
-         dev)
+        out = torch.empty(acc.shape, device=acc.device)
+    dev = q.get_device()
+
+    def make():
+        _need(q.dim() == 4 and k.dim() == 4, what, "q must be [B, Tq, H, hd] and k [B, Hkv, S, hd]")
+        _need(q_lens is None or lens is not None, what, "q_lens goes with lens")
+        B, Tq, H, hd = q.shape
+        Hkv, S = k.shape[1], k.shape[2]
+        bf, f32 = torch.bfloat16, torch.float32
+        for name, t, dt, shape, contiguous in (
+                ("q", q, bf, (B, Tq, H, hd), False), ("k", k, bf, (B, Hkv, S, hd), False),
+                ("lse", lse, f32, (B, Tq, H), True), ("acc", acc, f32, (B, Hkv, S), True),
+                ("out", out, f32, (B, Hkv, S), True), ("lens", lens, torch.int32, (B,), True),
+                ("q_lens", q_lens, torch.int32, (B,), True)):
+            _check_tensor(what, name, t, dt, shape, dev, contiguous)
+        a = WeightsArgs(*[None] * 7, B, Tq, H, Hkv, hd, S, hd ** -0.5 if scale is None else scale,
+                        _I3(*q.stride()[:3]), _I3(*k.stride()[:3]))
+        return a, 7, column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S)
+
+    block = _block((what, scale, _sig(q), _sig(k), _sig(lse), _sig(acc), _sig(out), _sig(lens), _sig(q_lens)), make)
+    _run(what, lib().flashloop_column_weights,
+         _ptrs7(q.data_ptr(), k.data_ptr(), lse.data_ptr(), acc.data_ptr(), out.data_ptr(), _addr(lens),
+                _addr(q_lens)), block, scratch, stream, dev)
     return out
 
 
@@ -636,21 +686,31 @@ def evict(k, v, acc, pos, lens, keep: int, recent: int = 0, sinks: int = 0, out=
     or into out = (k, v, acc, pos, lens) with ``keep`` slots per head.  Returns those five."""
     import torch
     what = "flashloop_evict"
-    _need(k.dim() == 4 and k.element_size() == 2, what, "k must be [B, Hkv, S, hd] of a 2-byte type")
-    B, Hkv, S, hd = k.shape
-    dev, f32, i32 = k.device, torch.float32, torch.int32
-    n = S if out is None else keep
     ko, vo, ao, po, lo = (k, v, acc, pos, lens) if out is None else out
-    a = EvictArgs(_take(what, "k", k, k.dtype, (B, Hkv, S, hd), dev), _take(what, "v", v, k.dtype, (B, Hkv, S, hd), dev),
-                  _take(what, "acc", acc, f32, (B, Hkv, S), dev), _take(what, "pos", pos, i32, (B, Hkv, S), dev),
-                  _take(what, "lens", lens, i32, (B,), dev, True),
-                  _take(what, "out k", ko, k.dtype, (B, Hkv, n, hd), dev),
-                  _take(what, "out v", vo, k.dtype, (B, Hkv, n, hd), dev),
-                  _take(what, "out acc", ao, f32, (B, Hkv, n), dev), _take(what, "out pos", po, i32, (B, Hkv, n), dev),
-                  _take(what, "out lens", lo, i32, (B,), dev, True), B, Hkv, S, hd, keep, recent, sinks,
-                  _I3(*k.stride()[:3]), _I3(*v.stride()[:3]), _I2(*acc.stride()[:2]), _I2(*pos.stride()[:2]),
-                  _I3(*ko.stride()[:3]), _I3(*vo.stride()[:3]), _I2(*ao.stride()[:2]), _I2(*po.stride()[:2]))
-    _run(what, lib().flashloop_evict, a, evict_scratch_bytes(B, Hkv, S, keep), scratch, stream, dev)
+    dev = k.get_device()
+
+    def make():
+        _need(k.dim() == 4 and k.element_size() == 2, what, "k must be [B, Hkv, S, hd] of a 2-byte type")
+        B, Hkv, S, hd = k.shape
+        f32, i32 = torch.float32, torch.int32
+        n = S if out is None else keep
+        for name, t, dt, shape, contiguous in (
+                ("k", k, k.dtype, (B, Hkv, S, hd), False), ("v", v, k.dtype, (B, Hkv, S, hd), False),
+                ("acc", acc, f32, (B, Hkv, S), False), ("pos", pos, i32, (B, Hkv, S), False),
+                ("lens", lens, i32, (B,), True), ("out k", ko, k.dtype, (B, Hkv, n, hd), False),
+                ("out v", vo, k.dtype, (B, Hkv, n, hd), False), ("out acc", ao, f32, (B, Hkv, n), False),
+                ("out pos", po, i32, (B, Hkv, n), False), ("out lens", lo, i32, (B,), True)):
+            _check_tensor(what, name, t, dt, shape, dev, contiguous)
+        a = EvictArgs(*[None] * 10, B, Hkv, S, hd, keep, recent, sinks, _I3(*k.stride()[:3]), _I3(*v.stride()[:3]),
+                      _I2(*acc.stride()[:2]), _I2(*pos.stride()[:2]), _I3(*ko.stride()[:3]), _I3(*vo.stride()[:3]),
+                      _I2(*ao.stride()[:2]), _I2(*po.stride()[:2]))
+        return a, 10, evict_scratch_bytes(B, Hkv, S, keep)
+
+    block = _block((what, keep, recent, sinks, out is None, _sig(k), _sig(v), _sig(acc), _sig(pos), _sig(lens), _sig(ko),
+                    _sig(vo), _sig(ao), _sig(po), _sig(lo)), make)
+    _run(what, lib().flashloop_evict,
+         _ptrs10(k.data_ptr(), v.data_ptr(), acc.data_ptr(), pos.data_ptr(), lens.data_ptr(), ko.data_ptr(),
+                 vo.data_ptr(), ao.data_ptr(), po.data_ptr(), lo.data_ptr()), block, scratch, stream, dev)
     return ko, vo, ao, po, lo
 
 
@@ -670,19 +730,30 @@ def verify_draft(logits, draft_logits, draft, u, n_draft=None, temperature: floa
     import torch
     what = "flashloop_verify_draft"
     _need(logits.dim() == 3 and logits.shape[1] >= 1, what, "logits must be [B, D + 1, V]")
-    B, D, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
-    dev, f32, i32 = logits.device, torch.float32, torch.int32
     if tokens is None:
-        tokens = torch.empty((B, D + 1), dtype=i32, device=dev)
+        tokens = torch.empty(logits.shape[:2], dtype=torch.int32, device=logits.device)
     if n_accepted is None:
-        n_accepted = torch.empty((B,), dtype=i32, device=dev)
-    a = VerifyArgs(_take(what, "logits", logits, f32, (B, D + 1, V), dev),
-                   _take(what, "draft_logits", draft_logits, f32, (B, D, V), dev) if D else None,
-                   _take(what, "draft", draft, i32, (B, D), dev, True) if D else None,
-                   _take(what, "u", u, f32, (B, D + 1), dev, True),
-                   _take(what, "n_draft", n_draft, i32, (B,), dev, True),
-                   _take(what, "tokens", tokens, i32, (B, D + 1), dev, True),
-                   _take(what, "n_accepted", n_accepted, i32, (B,), dev, True), B, D, V, temperature,
-                   _I2(*logits.stride()[:2]), _I2(*draft_logits.stride()[:2]) if D and draft_logits is not None else _I2())
-    _run(what, lib().flashloop_verify_draft, a, verify_draft_scratch_bytes(B, D, V), scratch, stream, dev)
+        n_accepted = torch.empty(logits.shape[:1], dtype=torch.int32, device=logits.device)
+    if logits.shape[1] == 1:   # nothing drafted: one token is sampled
+        draft = draft_logits = None
+    dev = logits.get_device()
+
+    def make():
+        B, D, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+        f32, i32 = torch.float32, torch.int32
+        for name, t, dt, shape, contiguous in (
+                ("logits", logits, f32, (B, D + 1, V), False), ("draft_logits", draft_logits, f32, (B, D, V), False),
+                ("draft", draft, i32, (B, D), True), ("u", u, f32, (B, D + 1), True),
+                ("n_draft", n_draft, i32, (B,), True), ("tokens", tokens, i32, (B, D + 1), True),
+                ("n_accepted", n_accepted, i32, (B,), True)):
+            _check_tensor(what, name, t, dt, shape, dev, contiguous)
+        a = VerifyArgs(*[None] * 7, B, D, V, temperature, _I2(*logits.stride()[:2]),
+                       _I2(*draft_logits.stride()[:2]) if draft_logits is not None else _I2())
+        return a, 7, verify_draft_scratch_bytes(B, D, V)
+
+    block = _block((what, temperature, _sig(logits), _sig(draft_logits), _sig(draft), _sig(u), _sig(n_draft),
+                    _sig(tokens), _sig(n_accepted)), make)
+    _run(what, lib().flashloop_verify_draft,
+         _ptrs7(logits.data_ptr(), _addr(draft_logits), _addr(draft), _addr(u), _addr(n_draft), tokens.data_ptr(),
+                n_accepted.data_ptr()), block, scratch, stream, dev)
     return tokens, n_accepted
