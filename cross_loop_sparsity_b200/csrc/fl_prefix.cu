@@ -44,6 +44,26 @@ struct PrefixArgs {
   long long rows;         // B * Tq * H
   float* part_o;          // [n_p + n_s][rows][hd]
   float2* part_ml;        // [n_p + n_s][rows]: max (log2 domain), sum
+  int tc_ctas;            // > 0: the prefix part runs on k_prefix_tc with at most this many CTAs (n_p = items_p = 0)
+  float* tc_o;            // [tc_ctas + Hkv * row blocks][kTcRows][hd]
+  float2* tc_ml;          // [tc_ctas + Hkv * row blocks][kTcRows]
+};
+
+// How k_prefix_tc divides the prefix: row blocks of kTcRows packed query rows, 128-key tiles; the
+// (row block, KV head, tile) units in this order, evenly over the CTAs, so a CTA's
+// range covers few (row block, head) pairs.  CTA c's part of pair p is partial c + p.
+constexpr int kTcRows = 256, kTcTile = 128, kTcMinTiles = 2;
+struct TcPlan {
+  int nblk, ntiles, ctas;
+  long long units;
+  __device__ TcPlan(const PrefixArgs& a, int queries) {
+    nblk = (queries * a.G + kTcRows - 1) / kTcRows;
+    ntiles = (a.P + kTcTile - 1) / kTcTile;
+    units = static_cast<long long>(nblk) * a.Hkv * ntiles;
+    ctas = static_cast<int>(min(static_cast<long long>(a.tc_ctas), max(1LL, units / kTcMinTiles)));
+  }
+  __device__ long long begin(int c) const { return c * units / ctas; }
+  __device__ int cta_of(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
 };
 
 __device__ __forceinline__ int q_len_of(const PrefixArgs& a, int b) {
@@ -87,6 +107,13 @@ __device__ __forceinline__ uint32_t sw_off(int rows, int r, int c) {
   return static_cast<uint32_t>((c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// two fp32 to packed bf16 (low half: the first), one conversion
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // ============================================================================
 // One split: up to 16 NM query rows of one KV head over a range of columns of
 // the prefix (rows of every sequence, packed) or of one sequence's own rows.
@@ -127,7 +154,10 @@ __global__ void __launch_bounds__(128, 1)
     fence_mbar_init();
     bad_sm = 0;
   }
-  pdl_wait();
+  // Behind k_prefix_tc (which started after everything this call reads was
+  // written, and shares nothing with this kernel) the wait moves to the end: the
+  // two overlap, and the merge, which waits for this kernel, finds both complete.
+  if (!a.tc_ctas) pdl_wait();
   // ---- which rows, which columns
   const bool pre = static_cast<int>(blockIdx.x) < a.items_p;
   int it = pre ? blockIdx.x : blockIdx.x - a.items_p;
@@ -162,7 +192,10 @@ __global__ void __launch_bounds__(128, 1)
     }
   }
   __syncthreads();   // barriers, row_id
-  if (r0 >= nrows) return;
+  if (r0 >= nrows) {
+    if (a.tc_ctas) pdl_wait();
+    return;
+  }
   const int ntiles = (ncols + kPxTile - 1) / kPxTile;
   const int tb = static_cast<int>(static_cast<long long>(sp) * ntiles / nsp);
   const int te = static_cast<int>(static_cast<long long>(sp + 1) * ntiles / nsp);
@@ -384,6 +417,388 @@ __global__ void __launch_bounds__(128, 1)
       *reinterpret_cast<float4*>(a.part_o + (split * a.rows + id) * HD + d) = o;
     if (d == 0) a.part_ml[split * a.rows + id] = bad_sm ? make_float2(0.f, NAN) : make_float2(M, L);
   }
+  if (a.tc_ctas) pdl_wait();
+}
+
+// ============================================================================
+// The prefix on the 5th-generation tensor cores, when the batch has more query
+// rows per KV head than two warp tiles: 256 rows share every K and V tile, so
+// the kernel is bound by the tensor pipe (4 * 256 FLOP per byte) for full row
+// blocks and by HBM for a few.  Two softmax warpgroups, one MMA thread, one TMA
+// thread.  A job is one 128-row x 128-key product: S = Q K^T into the job's half
+// of TMEM, softmax on S by its warpgroup (a thread owns a row), P as bf16 over S, O +=
+// P V with P read from TMEM.  Jobs alternate between the two halves, so one half's
+// products run under the other's softmax.  With more than 128 rows the halves
+// are two row tiles of the same keys; with fewer they are the same rows over
+// alternate key tiles, joined at the end.
+//   Running maximum: O is rescaled only when a row's maximum has grown by more
+// than 8 (log2 domain) -- until then the old one stays, the probabilities are at
+// most 2^8, and bf16's relative precision is the same there.
+//   P enters the second product rounded to bf16 (as in the prefill attention);
+// the sums use the fp32 values.
+// ============================================================================
+template <int HD>
+struct TcSmem {
+  static constexpr int kBox = 128 * 128;                 // 128 rows of 64 dims
+  static constexpr int kTileBytes = (HD / 64) * kBox;    // 128 rows
+  static constexpr int kKSlots = HD == 128 ? 3 : 6, kVSlots = HD == 128 ? 2 : 4;
+  static constexpr int kBytes = (2 + kKSlots + kVSlots) * kTileBytes;
+};
+constexpr int kTcThreads = 320;
+
+template <int HD>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_prefix_tc(const __grid_constant__ CUtensorMap kp, const __grid_constant__ CUtensorMap vp, const PrefixArgs a) {
+  using C = TcSmem<HD>;
+  constexpr int NB = HD / 64, KS = C::kKSlots, VS = C::kVSlots;
+  constexpr int OLD = HD + 4;                            // padded row of the join buffer
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* qsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ksm = qsm + 2 * C::kTileBytes;
+  uint8_t* vsm = ksm + KS * C::kTileBytes;
+  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_ready[2], o_done[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int row_id[kTcRows];
+  int* slot_sm = reinterpret_cast<int*>(qsm);            // while the query tiles are not there yet
+  float2* join_ml = reinterpret_cast<float2*>(ksm + 128 * OLD * 4);
+  __shared__ int total_sm;
+  __shared__ volatile int bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid == 0) {
+    for (int i = 0; i < KS; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 1);
+      mbar_init(smem_u32(&k_empty[i]), 1);
+    }
+    for (int i = 0; i < VS; ++i) {
+      mbar_init(smem_u32(&v_full[i]), 1);
+      mbar_init(smem_u32(&v_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&p_ready[i]), 128);
+      mbar_init(smem_u32(&o_done[i]), 1);
+    }
+    fence_mbar_init();
+    bad = 0;
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const int total = pack_queries(a, 0, 0, slot_sm);
+    if (lane == 0) total_sm = total;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = tmem_slot;
+  const int queries = total_sm, nrows = queries * a.G;
+  // a negative scale: negated queries and its magnitude, so that the largest score is the largest product
+  const float scale2 = fabsf(a.scale2);
+  const uint32_t flip = a.scale2 < 0.f ? 0x80008000u : 0u;
+  // counts of the barriers' phases, running over the CTA's segments
+  int nk = 0, nv = 0;            // tiles loaded (TMA thread) or consumed (MMA thread)
+  int ns[2] = {0, 0};            // jobs per half (MMA thread), or [0]: this warpgroup's jobs
+  const TcPlan plan(a, queries);
+  long long u = 0, u_end = 0;
+  if (queries > 0 && static_cast<int>(blockIdx.x) < plan.ctas) {
+    u = plan.begin(blockIdx.x);
+    u_end = plan.begin(blockIdx.x + 1);
+  }
+  while (u < u_end && !bad) {
+    const int pair = static_cast<int>(u / plan.ntiles), t0 = static_cast<int>(u % plan.ntiles);
+    const int nt = static_cast<int>(min(static_cast<long long>(plan.ntiles - t0), u_end - u));
+    const int g = pair % a.Hkv, r0 = pair / a.Hkv * kTcRows;
+    const int rows = min(kTcRows, nrows - r0);
+    const bool two = rows > 128;               // the halves are two row tiles
+    const int jobs = two ? 2 * nt : nt;        // job n: half n & 1, tile t0 + (two ? n / 2 : n)
+    auto load_k = [&](int i) {                 // (TMA thread)
+      const uint32_t bar = smem_u32(&k_full[nk % KS]), dst = smem_u32(ksm + (nk % KS) * C::kTileBytes);
+      mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+      for (int bx = 0; bx < NB; ++bx) tma_load_4d(dst + bx * C::kBox, &kp, bar, bx * 64, (t0 + i) * kTcTile, g, 0);
+      ++nk;
+    };
+    auto load_v = [&](int i) {
+      const uint32_t bar = smem_u32(&v_full[nv % VS]), dst = smem_u32(vsm + (nv % VS) * C::kTileBytes);
+      mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+      for (int bx = 0; bx < NB; ++bx) tma_load_4d(dst + bx * C::kBox, &vp, bar, bx * 64, (t0 + i) * kTcTile, g, 0);
+      ++nv;
+    };
+    // ---- the segment's queries (every thread); the K and V rings fill meanwhile
+    int k_at = 0, v_at = 0;                    // next tile to load (TMA thread): K_0 K_1 V_0 K_2 V_1 ...
+    bool stop = false;
+    if (tid == 9 * 32) {
+      // the first tiles of a segment: their slots' last readers finished with the previous segment
+      while (k_at < nt && k_at < KS) {
+        stop = nk >= KS && !mbar_wait(smem_u32(&k_empty[nk % KS]), ((nk / KS) - 1) & 1, nullptr);
+        if (stop) break;
+        load_k(k_at++);
+      }
+      while (!stop && v_at < nt && v_at < VS) {
+        stop = nv >= VS && !mbar_wait(smem_u32(&v_empty[nv % VS]), ((nv / VS) - 1) & 1, nullptr);
+        if (stop) break;
+        load_v(v_at++);
+      }
+    }
+    if (warp == 0) {
+      const int first = r0 / a.G, count = (r0 + rows - 1) / a.G - first + 1;
+      pack_queries(a, first, count, slot_sm);
+    }
+    __syncthreads();
+    if (tid < kTcRows) {
+      const int r = r0 + tid;
+      row_id[tid] = tid < rows ? slot_sm[r / a.G - r0 / a.G] * a.H + g * a.G + r % a.G : -1;   // (at most 2^30 rows)
+    }
+    __syncthreads();
+    for (int e = tid; e < (two ? 256 : 128) * (HD / 8); e += kTcThreads) {
+      const int r = e / (HD / 8), c = e % (HD / 8);
+      const int id = row_id[r];
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (id >= 0) {
+        const int s = id / a.H, h = id % a.H;
+        x = *reinterpret_cast<const uint4*>(a.q + (s / a.Tq) * a.q_sb + (s % a.Tq) * a.q_st + h * a.q_sh + c * 8);
+      }
+      x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
+      *reinterpret_cast<uint4*>(qsm + (r >> 7) * C::kTileBytes + sw_off(128, r & 127, c)) = x;
+    }
+    fence_proxy_async();
+    __syncthreads();
+
+    if (warp < 8) {
+      // ================= softmax warpgroup of one half =================
+      const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + q * 128, to = tmem + lanes + 256 + q * HD;
+      const int mine = (jobs + 1 - q) / 2;     // this half's jobs
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int phase) {   // the warp's threads agree: what follows is warp-wide
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, nullptr)) != 0;
+      };
+      for (int j = 0; j < mine; ++j, ++ns[0]) {
+        if (!wait(&s_full[q], ns[0])) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // Columns 0-63 of S are read twice, once for the maximum and once for the
+        // probabilities: all 128 in registers would spill.  P goes over columns 64-127.
+        uint32_t lo[64], hi[64];
+        tmem_ld32(ts, lo);
+        tmem_ld32(ts + 32, lo + 32);
+        tc_wait_ld();
+        const int ncol = a.P - (t0 + (two ? j : 2 * j + q)) * kTcTile;   // valid columns of this tile
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto top = [&](const uint32_t* r, int first) {
+          if (ncol >= kTcTile) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(r[c]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], first + c < ncol ? __uint_as_float(r[c]) : -INFINITY);
+          }
+        };
+        top(lo, 0);
+        tmem_ld32(ts + 64, hi);
+        tmem_ld32(ts + 96, hi + 32);
+        tc_wait_ld();
+        top(hi, 64);
+        tmem_ld32(ts, lo);
+        tmem_ld32(ts + 32, lo + 32);
+        const float mrow = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float mn = mrow == -INFINITY ? -INFINITY : mrow * scale2;
+        const bool grow = mn > m + 8.f || (m == -INFINITY && mn > m);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m_new = grow ? mn : m;
+          if (j > 0) {
+            const float al = m == m_new ? 1.f : ex2_approx(m - m_new);
+            if (!wait(&o_done[q], ns[0] - 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            l *= al;
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              tmem_ld16(to + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= al;
+              tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          m = m_new;
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        auto probs = [&](const uint32_t* r, int first) {   // 32 columns
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float p0 = ex2_approx(fmaf(__uint_as_float(r[e]), scale2, -ms));
+            float p1 = ex2_approx(fmaf(__uint_as_float(r[e + 1]), scale2, -ms));
+            if (ncol < kTcTile) {
+              if (first + e >= ncol) p0 = 0.f;
+              if (first + e + 1 >= ncol) p1 = 0.f;
+            }
+            sum[(e >> 1) & 3] += p0 + p1;
+            pk[e >> 1] = pack2(p0, p1);
+          }
+          tmem_st16(ts + 64 + first / 2, pk);
+        };
+        probs(hi, 64);
+        probs(hi + 32, 96);
+        tc_wait_ld();
+        probs(lo, 0);
+        probs(lo + 32, 32);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&p_ready[q]));
+      }
+      if (ok && mine > 0 && !wait(&o_done[q], ns[0] - 1)) ok = false;
+      if (!ok) bad = 1;
+      tc_fence_after();
+      // ---- this segment's part of the rows: (max, sum) and the unnormalised output
+      const long long part = blockIdx.x + pair;
+      if (!two) asm volatile("bar.sync 1, 256;" ::: "memory");   // both softmax warpgroups: every product is done
+      if (!two && q == 1) join_ml[row] = make_float2(mine > 0 ? m : -INFINITY, l);
+      float* jo = reinterpret_cast<float*>(ksm) + row * OLD;   // the rings are idle: every load was consumed
+      if (!two && q == 1 && mine > 0 && ok) {
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(to + c * 32, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(jo + c * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (!two) asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (two || q == 0) {
+        const bool have = (two ? q * 128 : 0) + row < rows;
+        float w0 = 1.f, w1 = 0.f, M = m, L = l;
+        if (!two) {
+          const float2 x = join_ml[row];
+          M = fmaxf(m, x.x);
+          const float ms = M == -INFINITY ? 0.f : M;
+          w0 = ex2_approx(m - ms);
+          w1 = ex2_approx(x.x - ms);
+          L = l * w0 + x.y * w1;
+        }
+        const long long at = part * kTcRows + (two ? q * 128 : 0) + row;
+        if (have) a.tc_ml[at] = bad ? make_float2(0.f, NAN) : make_float2(M, L);
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(to + c * 32, o);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            if (!have) break;
+            float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
+                                   __uint_as_float(o[e + 3]));
+            if (!two) {
+              const float4 y = jobs > 1 ? *reinterpret_cast<const float4*>(jo + c * 32 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+              x.x = x.x * w0 + y.x * w1;
+              x.y = x.y * w0 + y.y * w1;
+              x.z = x.z * w0 + y.z * w1;
+              x.w = x.w * w0 + y.w * w1;
+            }
+            *reinterpret_cast<float4*>(a.tc_o + at * HD + c * 32 + e) = x;
+          }
+          __syncwarp();
+        }
+      }
+      fence_proxy_async();   // the join buffer becomes a ring again
+      tc_fence_before();
+    } else if (tid == 8 * 32) {
+      // ================= MMA thread =================
+      constexpr uint32_t id_s = umma_idesc_bf16(128, 128), id_o = umma_idesc_bf16(128, HD) | kIdescBMn;
+      const int k0 = nk, v0 = nv, s0 = ns[0], s1 = ns[1];   // counts at the segment's start
+      auto tile_of = [&](int n) { return two ? n >> 1 : n; };
+      auto do_qk = [&](int n) -> bool {
+        const int q = n & 1, i = tile_of(n), kt = k0 + i, st = kt % KS;
+        if (!mbar_wait(smem_u32(&k_full[st]), (kt / KS) & 1, nullptr)) return false;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(qsm + (two ? q : 0) * C::kTileBytes), kb = smem_u32(ksm + st * C::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          tc_mma_bf16(tmem + q * 128, umma_desc_sw128(qa + (k >> 2) * C::kBox + (k & 3) * 32),
+                      umma_desc_sw128(kb + (k >> 2) * C::kBox + (k & 3) * 32), id_s, k > 0);
+        tc_commit(smem_u32(&s_full[q]));
+        if (!two || q == 1) tc_commit(smem_u32(&k_empty[st]));
+        return true;
+      };
+      bool ok = true;
+      for (int n = 0; n < 2 && n < jobs; ++n) ok = ok && do_qk(n);
+      for (int n = 0; ok && n < jobs; ++n) {
+        const int q = n & 1, i = tile_of(n), vt = v0 + i, st = vt % VS, j = n >> 1;
+        if (!mbar_wait(smem_u32(&p_ready[q]), ((q ? s1 : s0) + j) & 1, nullptr) ||
+            !mbar_wait(smem_u32(&v_full[st]), (vt / VS) & 1, nullptr)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t vb = smem_u32(vsm + st * C::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < kTcTile / 16; ++k)
+          tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + 64 + k * 8,
+                         umma_desc_sw128_mn(vb + k * 2048, C::kBox), id_o, j > 0 || k > 0);
+        tc_commit(smem_u32(&o_done[q]));
+        if (!two || q == 1) tc_commit(smem_u32(&v_empty[st]));
+        if (n + 2 < jobs) ok = do_qk(n + 2);
+      }
+      nk += nt;
+      nv += nt;
+      ns[0] += (jobs + 1) / 2;
+      ns[1] += jobs / 2;
+      if (!ok) bad = 1;
+    } else if (tid == 9 * 32) {
+      // ================= TMA thread =================
+      if (stop) bad = 1;
+      while ((k_at < nt || v_at < nt) && !bad) {
+        // V_i in front of K_{i+2}, as the products need them
+        const bool vk = v_at < nt && (k_at >= nt || v_at <= k_at - 2);
+        if (vk) {
+          if (nv >= VS && !mbar_wait(smem_u32(&v_empty[nv % VS]), ((nv / VS) - 1) & 1, nullptr)) {
+            bad = 1;
+            break;
+          }
+          load_v(v_at++);
+        } else {
+          if (nk >= KS && !mbar_wait(smem_u32(&k_empty[nk % KS]), ((nk / KS) - 1) & 1, nullptr)) {
+            bad = 1;
+            break;
+          }
+          load_k(k_at++);
+        }
+      }
+      if (bad) {   // let every copy in flight land (bounded) before the block can end
+        for (int i = max(0, nk - KS); i < nk; ++i) mbar_wait(smem_u32(&k_full[i % KS]), (i / KS) & 1, nullptr);
+        for (int i = max(0, nv - VS); i < nv; ++i) mbar_wait(smem_u32(&v_full[i % VS]), (i / VS) & 1, nullptr);
+      }
+    }
+    __syncthreads();
+    tc_fence_after();
+    u += nt;
+  }
+  if (bad)   // a wait ran out: every part of this CTA becomes NaN, never a silently wrong sum
+    for (long long w = plan.begin(blockIdx.x); w < u_end; w += plan.ntiles - w % plan.ntiles)
+      if (tid < kTcRows) a.tc_ml[(blockIdx.x + w / plan.ntiles) * kTcRows + tid] = make_float2(0.f, NAN);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 // ============================================================================
@@ -400,6 +815,7 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   constexpr int MB = 8;                // splits requested together
   __shared__ float gm[NG], gl[NG];
   __shared__ float4 go[NG][LPG];
+  __shared__ int cnt[2][4];
   pdl_trigger();
   const long long row = blockIdx.x;
   const int h = static_cast<int>(row % a.H), t = static_cast<int>(row / a.H % a.Tq);
@@ -424,21 +840,50 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
     o.w = o.w * w0 + x.w * w1;
     m = mn;
   };
-  const int n = a.n_p + a.n_s;
-  for (int i0 = grp; i0 < n; i0 += NG * MB) {
-    float2 ml[MB];
-    float4 x[MB];
+  // n partials of this row, `step` rows apart from row `at`
+  auto add_parts = [&](const float* po, const float2* pml, long long at, long long step, int n) {
+    for (int i0 = grp; i0 < n; i0 += NG * MB) {
+      float2 ml[MB];
+      float4 x[MB];
 #pragma unroll
-    for (int u = 0; u < MB; ++u) {
-      const int i = i0 + u * NG;
-      ml[u] = i < n ? __ldcg(&a.part_ml[static_cast<long long>(i) * a.rows + row]) : make_float2(-INFINITY, 0.f);
-      x[u] = i < n ? __ldcg(reinterpret_cast<const float4*>(&a.part_o[(static_cast<long long>(i) * a.rows + row) * HD +
-                                                                     gl_lane * 4]))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int u = 0; u < MB; ++u) {
+        const int i = i0 + u * NG;
+        ml[u] = i < n ? __ldcg(&pml[at + i * step]) : make_float2(-INFINITY, 0.f);
+        x[u] = i < n ? __ldcg(reinterpret_cast<const float4*>(&po[(at + i * step) * HD + gl_lane * 4]))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < MB; ++u)
+        if (i0 + u * NG < n) add(ml[u].x, ml[u].y, x[u]);
     }
-#pragma unroll
-    for (int u = 0; u < MB; ++u)
-      if (i0 + u * NG < n) add(ml[u].x, ml[u].y, x[u]);
+  };
+  add_parts(a.part_o, a.part_ml, row, a.rows, a.n_p + a.n_s);
+  if (a.tc_ctas > 0) {
+    // this query's number among the valid ones, and all of them
+    int before = b * a.Tq, all = a.B * a.Tq;
+    if (a.q_lens) {
+      before = all = 0;
+      for (int i = threadIdx.x; i < a.B; i += 128) {
+        const int x = q_len_of(a, i);
+        all += x;
+        if (i < b) before += x;
+      }
+      before = __reduce_add_sync(0xffffffffu, before);
+      all = __reduce_add_sync(0xffffffffu, all);
+      if ((threadIdx.x & 31) == 0) {
+        cnt[0][threadIdx.x >> 5] = before;
+        cnt[1][threadIdx.x >> 5] = all;
+      }
+      __syncthreads();
+      before = cnt[0][0] + cnt[0][1] + cnt[0][2] + cnt[0][3];
+      all = cnt[1][0] + cnt[1][1] + cnt[1][2] + cnt[1][3];
+    }
+    const TcPlan plan(a, all);
+    const int r = (before + t) * a.G + h % a.G;
+    const int pair = r / kTcRows * a.Hkv + h / a.G;
+    const int c0 = plan.cta_of(static_cast<long long>(pair) * plan.ntiles);
+    const int c1 = plan.cta_of(static_cast<long long>(pair + 1) * plan.ntiles - 1);
+    add_parts(a.tc_o, a.tc_ml, static_cast<long long>(c0 + pair) * kTcRows + r % kTcRows, kTcRows, c1 - c0 + 1);
   }
   const int len = len_of(a, b);
   const int base = min(max(len - ql + 1, 0), len), lim = min(max(len - ql + t + 1, 0), len);
@@ -619,12 +1064,21 @@ __global__ void __launch_bounds__(128) k_column_weights(const __grid_constant__ 
 struct PrefixPlan {
   int nm;
   int rb_p, n_p, rb_s, n_s;
-  size_t rows, bytes;
+  int tc_ctas;         // > 0: the prefix on the 5th-generation tensor cores
+  size_t rows, tc_parts;
+  size_t off_ml, off_tc_o, off_tc_ml, bytes;
 };
-PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
+constexpr int kTcMinRows = 33;   // query rows per KV head (two warp tiles hold 32)
+PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool fp32_queries) {
   PrefixPlan p{};
   const int G = H / Hkv;
   const long long rows_p = static_cast<long long>(B) * Tq * G, rows_s = static_cast<long long>(Tq) * G;
+  if (!fp32_queries && P >= kTcTile && rows_p >= kTcMinRows) {
+    const long long pairs = static_cast<long long>(Hkv) * ceil_div_i(rows_p, kTcRows);
+    p.tc_ctas = static_cast<int>(std::min<long long>(kNumSM, std::max(1LL, pairs * ceil_div_i(P, kTcTile) / kTcMinTiles)));
+    p.tc_parts = static_cast<size_t>(p.tc_ctas + pairs);
+    P = 0;   // nothing of it is left for the warp tiles
+  }
   p.nm = (P > 0 && rows_p > 16) || rows_s > 16 ? 2 : 1;
   const int RB = 16 * p.nm;
   p.rb_p = ceil_div_i(rows_p, RB);
@@ -636,7 +1090,10 @@ PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
   p.n_s = splits(S);
   p.rows = static_cast<size_t>(B) * Tq * H;
   const size_t n = p.n_p + p.n_s;
-  p.bytes = align256_sz(n * p.rows * hd * 4) + align256_sz(n * p.rows * 8) + 256;
+  p.off_ml = align256_sz(n * p.rows * hd * 4);
+  p.off_tc_o = p.off_ml + align256_sz(n * p.rows * 8);
+  p.off_tc_ml = p.off_tc_o + align256_sz(p.tc_parts * kTcRows * hd * 4);
+  p.bytes = p.off_tc_ml + align256_sz(p.tc_parts * kTcRows * 8) + 256;
   return p;
 }
 
@@ -679,21 +1136,23 @@ cudaError_t serving_init_attrs() {
   set(k_prefix_split<128, 1, true>, split_smem(128, 1, true));
   set(k_prefix_split<128, 2, false>, split_smem(128, 2, false));
   set(k_prefix_split<128, 2, true>, split_smem(128, 2, true));
+  set(k_prefix_tc<64>, 1024 + TcSmem<64>::kBytes);
+  set(k_prefix_tc<128>, 1024 + TcSmem<128>::kBytes);
   set(k_column_weights<64>, weights_smem(64));
   set(k_column_weights<128>, weights_smem(128));
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
 }
 
-size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
-  return plan_prefix(B, Tq, H, Hkv, hd, P, S).bytes;
+size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool fp32_queries) {
+  return plan_prefix(B, Tq, H, Hkv, hd, P, S, fp32_queries).bytes;
 }
 
 cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) {
   const flashloop_prefix_args& c = L.a;
   cudaError_t e = serving_init_attrs();
   if (e != cudaSuccess) return e;
-  const PrefixPlan p = plan_prefix(c.B, c.Tq, c.H, c.Hkv, c.hd, c.P, c.S);
+  const PrefixPlan p = plan_prefix(c.B, c.Tq, c.H, c.Hkv, c.hd, c.P, c.S, L.q32 != nullptr);
   PrefixArgs a{};
   a.q = c.q; a.q32 = L.q32; a.q_sb = c.q_stride[0]; a.q_st = c.q_stride[1]; a.q_sh = c.q_stride[2];
   a.out = c.out; a.o_sb = c.out_stride[0]; a.o_st = c.out_stride[1]; a.o_sh = c.out_stride[2];
@@ -706,13 +1165,17 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
   a.rb_p = p.rb_p; a.n_p = p.n_p; a.rb_s = p.rb_s; a.n_s = p.n_s;
   a.items_p = p.rb_p * p.n_p * c.Hkv;
   a.rows = static_cast<long long>(p.rows);
-  a.part_o = static_cast<float*>(scratch);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(scratch) +
-                                        align256_sz(static_cast<size_t>(p.n_p + p.n_s) * p.rows * c.hd * 4));
+  uint8_t* ws = static_cast<uint8_t*>(scratch);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.off_ml);
+  a.tc_ctas = p.tc_ctas;
+  a.tc_o = reinterpret_cast<float*>(ws + p.off_tc_o);
+  a.tc_ml = reinterpret_cast<float2*>(ws + p.off_tc_ml);
   CUtensorMap m[4] = {};
+  const uint32_t box = p.tc_ctas ? kTcTile : kPxTile;
   if (c.P > 0) {
-    if (!encode_tmap_rows(&m[0], c.k_prefix, c.hd, c.P, c.Hkv, 1, c.kp_stride[1], c.kp_stride[0], 0, kPxTile) ||
-        !encode_tmap_rows(&m[1], c.v_prefix, c.hd, c.P, c.Hkv, 1, c.vp_stride[1], c.vp_stride[0], 0, kPxTile))
+    if (!encode_tmap_rows(&m[0], c.k_prefix, c.hd, c.P, c.Hkv, 1, c.kp_stride[1], c.kp_stride[0], 0, box) ||
+        !encode_tmap_rows(&m[1], c.v_prefix, c.hd, c.P, c.Hkv, 1, c.vp_stride[1], c.vp_stride[0], 0, box))
       return cudaErrorInvalidValue;
   }
   if (c.S > 0) {
@@ -724,6 +1187,13 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
   if (c.S == 0) m[2] = m[0], m[3] = m[1];
   const long long grid = a.items_p + static_cast<long long>(p.rb_s) * p.n_s * c.Hkv * c.B;
   bool pdl = L.pdl;
+  if (p.tc_ctas) {
+    const int smem = 1024 + (c.hd == 128 ? TcSmem<128>::kBytes : TcSmem<64>::kBytes);
+    e = c.hd == 128 ? launch_k(pdl, k_prefix_tc<128>, dim3(p.tc_ctas), dim3(kTcThreads), smem, s, m[0], m[1], a)
+                    : launch_k(pdl, k_prefix_tc<64>, dim3(p.tc_ctas), dim3(kTcThreads), smem, s, m[0], m[1], a);
+    if (e != cudaSuccess) return e;
+    pdl = true;
+  }
   if (grid > 0) {
     e = c.hd == 128 ? run_split_hd<128>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s)
                     : run_split_hd<64>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s);
@@ -754,7 +1224,7 @@ extern "C" {
 
 size_t flashloop_prefix_attention_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
   if (!heads_ok(B, Tq, H, Hkv, hd) || Tq > kMaxTq || P < 0 || S < 0) return 0;
-  return prefix_scratch_bytes(B, Tq, H, Hkv, hd, P, S);
+  return prefix_scratch_bytes(B, Tq, H, Hkv, hd, P, S, false);
 }
 
 fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scratch, size_t scratch_bytes,
@@ -779,7 +1249,7 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
     if (i < 2 && a->P > 0 && (!stride_ok(a->kp_stride[i], pd[i], 8) || !stride_ok(a->vp_stride[i], pd[i], 8)))
       return refuse(FL_ERR_INVALID_ARG, "k_prefix and v_prefix strides must be positive multiples of 8");
   }
-  const size_t need = prefix_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->P, a->S);
+  const size_t need = prefix_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->P, a->S, false);
   if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
     return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
   PrefixLaunch L{};

@@ -41,7 +41,7 @@ struct PrefixLaunch {
   int lens_add;         // added to lens[b] before it is clamped
   bool pdl;             // the first launch may overlap its predecessor
 };
-size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S);
+size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool fp32_queries);
 cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s);
 cudaError_t serving_init_attrs();   // opt the kernels in to their shared memory (per device)
 

@@ -73,6 +73,12 @@ ATT = [
     (40, 8, 8, 2, 128, 400, 20, list(range(8, 20)) * 3 + [20] * 4, [1 + i % 8 for i in range(40)]),
     (2, 1, 2, 2, 128, 20011, 3000, [3000, 1501], None),
     (70, 2, 4, 1, 128, 2049, 5, [5] * 70, [2, 0] * 35),
+    (40, 1, 1, 1, 128, 128, 0, None, None),
+    (12, 3, 4, 1, 64, 129, 4, [4, 3, 2] * 4, [3, 1, 2] * 4),
+    (65, 1, 6, 2, 128, 1407, 2, [2] * 65, None),
+    (33, 4, 4, 2, 128, 5000, 6, [6, 5, 4] * 11, [4, 3, 2] * 11),
+    (64, 8, 2, 1, 64, 3333, 9, [9] * 64, [i % 9 for i in range(64)]),
+    (9, 4, 8, 2, 128, 300, 4, [4] * 9, [0] * 9),
 ]
 
 
