@@ -18,7 +18,7 @@ namespace cg = cooperative_groups;
 namespace fl {
 namespace {
 
-constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
+constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32;
 constexpr int kEvCluster = 8;             // CTAs of one (sequence, KV head) at most
 constexpr int kEvKeys = 32768;            // keys one CTA holds in shared memory (128 KB)
 constexpr int kEvSlots = kEvCluster * kEvKeys;
@@ -32,6 +32,19 @@ struct EvictArgs {
   int32_t* to;          // [B * Hkv][cap] freed slots < keep, ascending
   int32_t* n_kept;      // [B * Hkv]
 };
+
+// Exclusive prefix sums of the warps' counts, in place, and their total (one warp; 32 warps).
+__device__ __forceinline__ void scan_warps(int* v, int* total) {
+  const int lane = threadIdx.x & 31, x = v[lane];
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  v[lane] = incl - x;
+  if (lane == 31) *total = incl;
+}
 
 // ============================================================================
 // Selection: a cluster of 1-8 CTAs per (sequence, KV head), each with a contiguous
@@ -67,7 +80,7 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
   const int32_t* pos = c.pos + b * c.pos_stride[0] + g * c.pos_stride[1] + lo;
   // ---- the newest token
   if (tid == 0) newest_sm = INT_MIN;
-  for (int i = tid; i < 512; i += kEvThreads) (&hist[0][0])[i] = 0;
+  if (tid < 512) (&hist[0][0])[tid] = 0;
   __syncthreads();
   int newest = INT_MIN;
   for (int i = tid; i < m; i += kEvThreads) newest = max(newest, pos[i]);
@@ -88,13 +101,9 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
     const int shift = 24 - 8 * d;
     int* h = hist[d & 1];
     __syncthreads();
-    for (int i0 = warp * 32; i0 < m; i0 += kEvThreads) {
-      const uint32_t u = i0 + lane < m ? keys[i0 + lane] : 0u;
-      const bool in = i0 + lane < m && (u & mask) == prefix;
-      const int bin = in ? static_cast<int>((u >> shift) & 0xFF) : 256;
-      // weights of one magnitude share their leading digits: one atomic per distinct digit of the warp
-      const unsigned same = __match_any_sync(0xffffffffu, bin);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&h[bin], __popc(same));
+    for (int i = tid; i < m; i += kEvThreads) {
+      const uint32_t u = keys[i];
+      if ((u & mask) == prefix) atomicAdd(&h[(u >> shift) & 0xFF], 1);
     }
     cl.sync();
     if (tid < 256) {
@@ -140,15 +149,7 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
   for (int i0 = w0; i0 < w1; i0 += 32) eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && keys[i0 + lane] == prefix));
   if (lane == 0) warp_a[warp] = eq;
   __syncthreads();
-  if (tid == 0) {
-    int s = 0;
-    for (int w = 0; w < kEvWarps; ++w) {
-      const int x = warp_a[w];
-      warp_a[w] = s;
-      s += x;
-    }
-    cta_eq = s;
-  }
+  if (warp == 0) scan_warps(warp_a, &cta_eq);
   cl.sync();
   int eq_seen = warp_a[warp];
   for (int r = 0; r < rank; ++r) eq_seen += *cl.map_shared_rank(&cta_eq, r);
@@ -173,17 +174,9 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
     warp_b[warp] = moves;
   }
   __syncthreads();
-  if (tid == 0) {
-    int s = 0, t = 0;
-    for (int w = 0; w < kEvWarps; ++w) {
-      const int x = warp_a[w], y = warp_b[w];
-      warp_a[w] = s;
-      warp_b[w] = t;
-      s += x;
-      t += y;
-    }
-    cta_hole = s;
-    cta_move = t;
+  if (warp == 0) {
+    scan_warps(warp_a, &cta_hole);
+    scan_warps(warp_b, &cta_move);
   }
   cl.sync();
   int h0 = warp_a[warp], m0 = warp_b[warp], all = 0;
@@ -213,50 +206,52 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
 }
 
 // ============================================================================
-// Move: a row's K and V as 16-byte vectors, one per thread, kEvRows rows' loads
-// in flight; in place only rows whose source is another slot.  HBM-bound:
-// 8 hd bytes per copied row.
+// Move: a row's K and V as 16-byte vectors, kEvVecs of them per thread in flight
+// at once; in place only rows whose source is another slot.  HBM-bound: 8 hd
+// bytes per copied row.  W: vectors of a K or V row as a constant (head_dim 64, 128; 0: any).
 // ============================================================================
-constexpr int kEvRows = 4;
-__global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int vec, int rows_cta) {
+constexpr int kEvVecs = 8;
+template <int W>
+__global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int vec_any, int rows_cta) {
   pdl_wait();
   const flashloop_evict_args& c = a.c;
+  const int vec = W ? W : vec_any;
   const int g = blockIdx.y, b = blockIdx.z;
   const long long seg = static_cast<long long>(b) * c.Hkv + g;
   const int n = a.n_kept[seg];
   const bool in_place = c.k_out == c.k;
   if (blockIdx.x == 0 && g == 0 && threadIdx.x == 0) c.lens_out[b] = n;
   const int32_t* src = a.src + seg * a.cap;
+  const int row0 = blockIdx.x * rows_cta, row1 = min(n, row0 + rows_cta);
+  if (row0 >= row1) return;
   const uint16_t* k = c.k + b * c.k_stride[0] + g * c.k_stride[1];
   const uint16_t* v = c.v + b * c.v_stride[0] + g * c.v_stride[1];
   uint16_t* ko = c.k_out + b * c.k_out_stride[0] + g * c.k_out_stride[1];
   uint16_t* vo = c.v_out + b * c.v_out_stride[0] + g * c.v_out_stride[1];
-  const int row0 = blockIdx.x * rows_cta, row1 = min(n, row0 + rows_cta);
-  if (row0 >= row1) return;
   const int total = (row1 - row0) * 2 * vec;   // vectors of this CTA's rows: K then V of each row
-  for (int e0 = threadIdx.x; e0 < total; e0 += 256 * kEvRows) {
-    uint4 x[kEvRows];
-    int from[kEvRows];
+  for (int e0 = threadIdx.x; e0 < total; e0 += 256 * kEvVecs) {
+    uint4 x[kEvVecs];
+    int from[kEvVecs];
 #pragma unroll
-    for (int u = 0; u < kEvRows; ++u) {
+    for (int u = 0; u < kEvVecs; ++u) {
       const int e = e0 + u * 256;
       from[u] = e < total ? src[row0 + e / (2 * vec)] : -1;
-      if (from[u] >= 0 && in_place && from[u] == row0 + e / (2 * vec)) from[u] = -1;
+      if (in_place && from[u] == row0 + e / (2 * vec)) from[u] = -1;
     }
 #pragma unroll
-    for (int u = 0; u < kEvRows; ++u) {
-      const int e = e0 + u * 256, w = e % (2 * vec);
+    for (int u = 0; u < kEvVecs; ++u) {
+      const int w = (e0 + u * 256) % (2 * vec);
       if (from[u] >= 0)
-        x[u] = w < vec ? *reinterpret_cast<const uint4*>(k + from[u] * c.k_stride[2] + w * 8)
-                       : *reinterpret_cast<const uint4*>(v + from[u] * c.v_stride[2] + (w - vec) * 8);
+        x[u] = __ldcs(reinterpret_cast<const uint4*>(w < vec ? k + from[u] * c.k_stride[2] + w * 8
+                                                             : v + from[u] * c.v_stride[2] + (w - vec) * 8));
     }
 #pragma unroll
-    for (int u = 0; u < kEvRows; ++u) {
+    for (int u = 0; u < kEvVecs; ++u) {
       const int e = e0 + u * 256, w = e % (2 * vec);
       const long long row = row0 + e / (2 * vec);
       if (from[u] >= 0)
-        *reinterpret_cast<uint4*>(w < vec ? ko + row * c.k_out_stride[2] + w * 8
-                                          : vo + row * c.v_out_stride[2] + (w - vec) * 8) = x[u];
+        __stcs(reinterpret_cast<uint4*>(w < vec ? ko + row * c.k_out_stride[2] + w * 8
+                                                : vo + row * c.v_out_stride[2] + (w - vec) * 8), x[u]);
     }
   }
   for (int r = row0 + threadIdx.x; r < row1; r += 256) {
@@ -336,9 +331,9 @@ fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t s
   a.from = reinterpret_cast<int32_t*>(ws + list);
   a.to = reinterpret_cast<int32_t*>(ws + 2 * list);
   a.n_kept = reinterpret_cast<int32_t*>(ws + 3 * list);
-  // CTAs per segment: chunks of about 4096 slots (8 per thread and pass)
+  // CTAs per segment: chunks of at most 8192 slots (8 per thread and pass) while the cluster allows
   int nc = 1;
-  while (nc < kEvCluster && c->S > nc * 4096) nc *= 2;
+  while (nc < kEvCluster && c->S > nc * 8192) nc *= 2;
   a.chunk = ceil_div_i(c->S, nc);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchConfig_t cfg = {};
@@ -356,9 +351,11 @@ fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t s
   e = cudaLaunchKernelEx(&cfg, k_evict_select, a);
   if (e != cudaSuccess) return cuda_status(e);
   const int vec = c->hd / 8;
-  const int rows_cta = std::max(1, 256 * kEvRows * 2 / (2 * vec));
-  return cuda_status(launch_k(true, k_evict_move, dim3(ceil_div_i(a.cap, rows_cta), c->Hkv, c->B), dim3(256), 0, s, a,
-                              vec, rows_cta));
+  const int rows_cta = std::max(1, 256 * kEvVecs / (2 * vec));   // one round of every thread's vectors
+  const dim3 grid(ceil_div_i(a.cap, rows_cta), c->Hkv, c->B);
+  if (vec == 16) return cuda_status(launch_k(true, k_evict_move<16>, grid, dim3(256), 0, s, a, vec, rows_cta));
+  if (vec == 8) return cuda_status(launch_k(true, k_evict_move<8>, grid, dim3(256), 0, s, a, vec, rows_cta));
+  return cuda_status(launch_k(true, k_evict_move<0>, grid, dim3(256), 0, s, a, vec, rows_cta));
 }
 
 }  // extern "C"

@@ -1,29 +1,24 @@
 // fl_verify.cu -- verification of drafted tokens against the target's
 // probabilities, from given random numbers.
 //
-// Two launches.  The first reads every row of logits once and leaves, per chunk, the
-// maximum, where it is, and the sum of exponentials relative to it.  The second
-// (a cluster per sequence) decides the accepted drafts and samples the last
-// token from the one row that decides it, whose sums it forms again in 64 bits:
-// a token is the index where a running sum crosses u times its total, and with
-// V tokens between 0 and 1 that index is only well defined when the sum is
-// known far better than 1 / V.
+// Three launches (two when greedy).  The first reads every row of logits once and leaves, per
+// chunk, the maximum, where it is, and the sum of exponentials relative to it.  The second
+// decides the accepted drafts and forms again, in 64 bits, the sums of the one row that
+// decides the last token; the third finds the token.  64 bits because a token
+// is the index where a running sum crosses u times its total: with V tokens between 0 and
+// 1 that index is only well defined when the sum is known far better than 1 / V.
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <cooperative_groups.h>
 
 #include "fl_device.cuh"
 #include "fl_serving.h"
-
-namespace cg = cooperative_groups;
 
 namespace fl {
 namespace {
 
 constexpr int kVfThreads = 256;
 constexpr int kVfChunk = 32 * kVfThreads - 4;   // logits per CTA of the first launch: 32 per thread, 4 spare for alignment
-constexpr int kVfCluster = 8;
 constexpr int kMaxDraft = 64;
 
 struct RowPart {   // one chunk of one row
@@ -35,7 +30,12 @@ struct VerifyArgs {
   int n_chunks;
   double scale2;   // log2(e) / temperature
   RowPart* part;   // [B][2D + 1][n_chunks]: target rows, then draft rows
+  struct Deciding* deciding;   // [B]
+  struct Sums* sums;           // [B][n_sub] of the deciding row's token ranges
+  int n_sub, sub_len;
 };
+constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+constexpr int kSumMaxCtas = kSumThreads / kSumWarps;   // CTAs of one sequence: n_sub <= kSumThreads
 
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int b) {
   return a.c.n_draft ? min(max(a.c.n_draft[b], 0), a.c.D) : a.c.D;
@@ -121,40 +121,322 @@ __global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) 
   }
 }
 
-// ============================================================================
-// One cluster per sequence.  Every CTA decides the accepted drafts from the
-// first launch's sums (32-bit, good to about 1e-6); a decision closer to its
-// border than 1e-4 is taken again from 64-bit sums of that row.  Then each CTA
-// has a contiguous range of the deciding row's tokens, each warp a contiguous
-// part of it: their sums, scanned over warps and CTAs, give the warp that holds
-// the crossing, which walks its part once more.
-// ============================================================================
-struct Near {
-  int at;    // first draft not surely accepted (n: all are)
-  int sure;  // it is surely rejected
+// 2^y for y <= 0 to 2e-15: y = k / 32 + r, |r| <= 1/64, and 2^r = sum (r ln 2)^n / n! to n = 5 (the
+// next term is below 2.3e-15); table[i] = 2^(i/32).  0 below 2^-1020; NaN stays NaN.
+__device__ __forceinline__ double exp2_neg(double y, const double* table) {
+  if (!(y > -1020.0)) return y == y ? 0.0 : y;
+  const double t = fma(y, 32.0, 6755399441055744.0);        // + 1.5 * 2^52: k = rint(32 y) in the low word
+  const int k = __double2loint(t);
+  const double r = fma(t - 6755399441055744.0, -0.03125, y);
+  constexpr double kLn2 = 0.693147180559945309417;
+  constexpr double c1 = kLn2, c2 = kLn2 * kLn2 / 2, c3 = c2 * kLn2 / 3, c4 = c3 * kLn2 / 4, c5 = c4 * kLn2 / 5;
+  const double p = fma(fma(fma(fma(fma(c5, r, c4), r, c3), r, c2), r, c1), r, 1.0);
+  const double f = table[k & 31];
+  return p * __hiloint2double(__double2hiint(f) + ((k >> 5) << 20), __double2loint(f));
+}
+
+// The deciding row of a sequence, from 32-bit sums: target row `row`, draft row
+// `row` when with_draft, their maxima, ratio = the draft's total over the target's.
+struct Deciding {
+  int row;          // drafts accepted in front of it
+  int near;         // whether draft `row` is rejected is too near to say from 32-bit sums
+  int with_draft;   // the weights are max(p - q, 0)
+  int x_out;        // a token left out (the rejected one of a draft without probabilities), or -1
+  double mp, mq, ratio;
 };
 
-__global__ void __launch_bounds__(kVfThreads) k_verify_pick(const VerifyArgs a) {
-  cg::cluster_group cl = cg::this_cluster();
-  constexpr int NW = kVfThreads / 32;
-  __shared__ int verdict[kMaxDraft];      // 0 rejected, 1 accepted, 2 too near to say
-  __shared__ double wsum[2][NW];
-  __shared__ double cta_sum[2][2];        // [buffer][row kind]
-  __shared__ float row_max[2];
+// Sum and maximum of a row from the first launch (one warp).
+__device__ __forceinline__ void row_norm(const VerifyArgs& a, int b, int r, float& m, double& z) {
+  const int lane = threadIdx.x & 31;
+  const RowPart* part = a.part + (static_cast<size_t>(b) * (2 * a.c.D + 1) + r) * a.n_chunks;
+  m = -INFINITY;
+  z = 0.0;
+  for (int k0 = 0; k0 < a.n_chunks; k0 += 32) {
+    RowPart p{-INFINITY, 0.f, 0, 0};
+    if (k0 + lane < a.n_chunks) p = part[k0 + lane];
+    const float mn = fmaxf(m, warp_max(p.m));
+    if (mn > m) z *= static_cast<double>(exp2f(static_cast<float>((m - mn) * a.scale2)));
+    z += p.m == -INFINITY ? p.s : p.s * exp2f(static_cast<float>((p.m - mn) * a.scale2));   // (no finite logit: 0, or NaN)
+    m = mn;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+}
+
+// Verdicts of drafts [first, n) from the 32-bit sums: 0 rejected, 1 accepted, 2
+// too near to say (closer than 1e-4 of p; the sums and exponentials are good to about 1e-6).  Whole block.
+__device__ void judge(const VerifyArgs& a, int b, int first, int n, int* verdict) {
   const flashloop_verify_args& c = a.c;
-  const int nc = cl.num_blocks(), rank = cl.block_rank();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  for (int i = first + warp; i < n; i += nw) {
+    const int x = c.draft[static_cast<size_t>(b) * c.D + i];
+    const bool in = x >= 0 && x < c.V;
+    const double xp = in ? row_of(a, b, i)[x] : 0.0;
+    const double xq = in && c.draft_logits ? row_of(a, b, c.D + 1 + i)[x] : 0.0;
+    const double u = c.u[static_cast<size_t>(b) * (c.D + 1) + i];
+    float m, mq = 0.f;
+    double z, zq = 1.0;
+    row_norm(a, b, i, m, z);
+    if (c.draft_logits) row_norm(a, b, c.D + 1 + i, mq, zq);
+    if (lane == 0) {
+      const double p = in ? exp2((xp - m) * a.scale2) / z : 0.0;
+      const double q = c.draft_logits ? exp2((xq - mq) * a.scale2) / zq : 1.0;
+      verdict[i] = in && fabs(u * q - p) <= 1e-4 * p ? 2 : (in && u * q < p ? 1 : 0);
+    }
+  }
+  __syncthreads();
+}
+
+// The deciding row when drafts [0, row) are accepted (warp 0 fills *d; then a block barrier).
+__device__ void describe(const VerifyArgs& a, int b, int row, int n, int near, Deciding* d) {
+  const flashloop_verify_args& c = a.c;
+  if (threadIdx.x < 32) {
+    const bool residual = row < n, with_draft = residual && c.draft_logits;
+    float mp, mq = 0.f;
+    double zp, zq = 0.0;
+    row_norm(a, b, row, mp, zp);
+    if (with_draft) row_norm(a, b, c.D + 1 + row, mq, zq);
+    if (threadIdx.x == 0)
+      *d = Deciding{row, near, with_draft, residual && !with_draft ? c.draft[static_cast<size_t>(b) * c.D + row] : -1,
+                    mp, mq, zq / zp};
+  }
+  __syncthreads();
+}
+
+// 64-bit sums over tokens [j0, j1) of the deciding row (one warp; every lane returns them): p and q,
+// all exponentials; ap and aq, those of tokens whose weight is positive.  The weight of token j is
+//   max(e_p / Z_p - e_q / Z_q, 0) = max(ratio e_p - e_q, 0) / Z_q,  ratio = Z_q / Z_p,
+// so a range's weight is ratio * ap - aq, and the exact ratio need not be known
+// before the pass: which tokens are positive is decided with the 32-bit one, and a
+// token it gets wrong weighs less than 1e-6 of its probability.
+struct Sums {
+  double p, q, ap, aq;
+};
+__device__ Sums range_sums(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
+  constexpr int U = 8;   // tokens of a lane in flight
+  const int lane = threadIdx.x & 31;
+  const float* xp = row_of(a, b, d.row);
+  const float* xq = d.with_draft ? row_of(a, b, a.c.D + 1 + d.row) : xp;
+  Sums s{0.0, 0.0, 0.0, 0.0};
+  for (int j = j0 + lane; j < j1; j += 32 * U) {
+    float fp[U], fq[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      fp[u] = j + u * 32 < j1 ? xp[j + u * 32] : -INFINITY;
+      fq[u] = j + u * 32 < j1 && d.with_draft ? xq[j + u * 32] : -INFINITY;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j + u * 32 >= j1) break;
+      const double ep = exp2_neg((fp[u] - d.mp) * a.scale2, table);
+      s.p += ep;
+      if (d.with_draft) {
+        const double eq = exp2_neg((fq[u] - d.mq) * a.scale2, table);
+        s.q += eq;
+        if (d.ratio * ep > eq) {
+          s.ap += ep;
+          s.aq += eq;
+        }
+      } else if (j + u * 32 != d.x_out) {
+        s.ap += ep;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.p += __shfl_xor_sync(0xffffffffu, s.p, o);
+    s.q += __shfl_xor_sync(0xffffffffu, s.q, o);
+    s.ap += __shfl_xor_sync(0xffffffffu, s.ap, o);
+    s.aq += __shfl_xor_sync(0xffffffffu, s.aq, o);
+  }
+  return s;
+}
+
+// ============================================================================
+// Second launch: every CTA finds its sequence's deciding row from the first
+// launch's sums, then each of its warps forms the 64-bit sums of a contiguous
+// range of that row's tokens, two exponentials a token, once.  Bound by the 64-bit pipe
+// (about 13 operations per exponential) for many sequences, by the latency of
+// finding the row for few.
+// ============================================================================
+__global__ void __launch_bounds__(kSumThreads) k_verify_sums(const VerifyArgs a) {
+  __shared__ double table[32];
+  __shared__ int verdict[kMaxDraft];
+  __shared__ Deciding d;
+  pdl_trigger();
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) table[threadIdx.x] = exp2(threadIdx.x * 0.03125);
+  const int n = drafts_of(a, b);
   pdl_wait();
-  const int n = drafts_of(a, b), V = c.V, D = c.D;
+  judge(a, b, 0, n, verdict);
+  int row = 0;
+  while (row < n && verdict[row] == 1) ++row;
+  describe(a, b, row, n, row < n && verdict[row] == 2, &d);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.deciding[b] = d;
+  const int sub = blockIdx.x * kSumWarps + warp;
+  const int j0 = min(a.c.V, sub * a.sub_len), j1 = min(a.c.V, j0 + a.sub_len);
+  const Sums s = range_sums(a, b, d, j0, j1, table);
+  if (lane == 0) a.sums[static_cast<size_t>(b) * a.n_sub + sub] = s;
+}
+
+// ============================================================================
+// Third launch, one CTA per sequence: totals of the ranges' sums, the range that holds
+// the crossing, and the crossing token in it.  A near decision is settled by the
+// 64-bit totals of its row; when it turns out accepted, this CTA goes on to the next rows by
+// itself (about one call in ten thousand per draft).
+// ============================================================================
+__device__ double block_sum_f64(double v, double* buf /*[8]*/) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSumWarps; ++w) t += buf[w];
+  return t;
+}
+// exclusive prefix sum over the block's threads, in thread order
+__device__ double block_scan_f64(double v, double* buf /*[8]*/) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) buf[warp] = incl;
+  __syncthreads();
+  double base = 0.0;
+  for (int w = 0; w < warp; ++w) base += buf[w];
+  const double excl = __shfl_up_sync(0xffffffffu, incl, 1);
+  return base + (lane ? excl : 0.0);
+}
+
+__global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a) {
+  __shared__ double table[32], buf[kSumWarps];
+  __shared__ int verdict[kMaxDraft];
+  __shared__ Deciding d;
+  __shared__ int cross, last;
+  __shared__ double cross_start;
+  const flashloop_verify_args& c = a.c;
+  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < 32) table[tid] = exp2(tid * 0.03125);
+  const int n = drafts_of(a, b), D = c.D;
+  const int32_t* draft = c.draft + static_cast<size_t>(b) * D;
+  int32_t* tokens = c.tokens + static_cast<size_t>(b) * (D + 1);
+  Sums* sums = a.sums + static_cast<size_t>(b) * a.n_sub;
+  pdl_wait();
+  if (tid == 0) d = a.deciding[b];
+  __syncthreads();
+  Sums s{0.0, 0.0, 0.0, 0.0};   // n_sub <= threads: one range each
+  double zp, zq;
+  auto totals = [&]() {
+    if (tid < a.n_sub) s = sums[tid];
+    zp = block_sum_f64(s.p, buf);
+    zq = block_sum_f64(s.q, buf);
+  };
+  totals();
+  while (d.near) {
+    const int x = draft[d.row];   // (in range: a token outside is never near)
+    const double p = exp2_neg((row_of(a, b, d.row)[x] - d.mp) * a.scale2, table) / zp;
+    const double q = c.draft_logits ? exp2_neg((row_of(a, b, D + 1 + d.row)[x] - d.mq) * a.scale2, table) / zq : 1.0;
+    if (!(static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + d.row]) * q < p)) break;   // rejected after all
+    int row = d.row + 1;
+    judge(a, b, row, n, verdict);
+    while (row < n && verdict[row] == 1) ++row;
+    describe(a, b, row, n, row < n && verdict[row] == 2, &d);
+    for (int sub = warp; sub < a.n_sub; sub += kSumWarps) {
+      const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
+      const Sums t = range_sums(a, b, d, j0, j1, table);
+      if (lane == 0) sums[sub] = t;
+    }
+    __syncthreads();
+    totals();
+  }
+  const int acc = d.row;
+  const bool with_draft = d.with_draft;
+  const double ratio = with_draft ? zq / zp : 1.0;
+  const double w = ratio * s.ap - s.aq, mine = w > 0.0 ? w : (w == w ? 0.0 : w);
+  const double before = block_scan_f64(mine, buf);
+  const double total = block_sum_f64(mine, buf);
+  const bool fine = isfinite(total) && total > 0.0 && isfinite(zp) && (!with_draft || (isfinite(zq) && zq > 0.0));
+  for (int i = tid; i <= D; i += kSumThreads)
+    if (i != acc || !fine) tokens[i] = i < acc ? draft[i] : -1;
+  if (tid == 0) {
+    c.n_accepted[b] = acc;
+    cross = INT_MAX;
+    last = -1;
+  }
+  if (!fine) return;
+  __syncthreads();
+  const double target = static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + D]) * total;
+  // the first range whose end is past the target (the last with any weight, should rounding leave none)
+  if (mine > 0.0) {
+    atomicMax(&last, tid);
+    if (target < before + mine) atomicMin(&cross, tid);
+  }
+  __syncthreads();
+  const int sub = cross != INT_MAX ? cross : last;
+  if (tid == sub) cross_start = before;
+  __syncthreads();
+  const double start = cross_start;
+  const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
+  const int per = (j1 - j0 + kSumThreads - 1) / kSumThreads;
+  const int t0 = min(j1, j0 + tid * per), t1 = min(j1, t0 + per);
+  const float* xp = row_of(a, b, acc);
+  const float* xq = with_draft ? row_of(a, b, D + 1 + acc) : nullptr;
+  auto weight = [&](int j) {
+    const double ep = exp2_neg((xp[j] - d.mp) * a.scale2, table);
+    if (with_draft) return fmax(ratio * ep - exp2_neg((xq[j] - d.mq) * a.scale2, table), 0.0);
+    return j == d.x_out ? 0.0 : ep;
+  };
+  double mass = 0.0;
+  for (int j = t0; j < t1; ++j) mass += weight(j);
+  const double at = start + block_scan_f64(mass, buf);
+  __syncthreads();
+  if (tid == 0) {
+    cross = INT_MAX;
+    last = -1;
+  }
+  __syncthreads();
+  if (mass > 0.0) {
+    atomicMax(&last, tid);
+    if (target < at + mass) atomicMin(&cross, tid);
+  }
+  __syncthreads();
+  if (tid != (cross != INT_MAX ? cross : last)) return;
+  double run = at;
+  int y = t0;
+  for (int j = t0; j < t1; ++j) {
+    const double x = weight(j);
+    run += x;
+    if (x > 0.0) {
+      y = j;
+      if (run > target) break;
+    }
+  }
+  tokens[acc] = y;
+}
+
+// ============================================================================
+// Greedy: one CTA per sequence; the first launch left every chunk's maximum.
+// ============================================================================
+__global__ void __launch_bounds__(256) k_verify_greedy(const VerifyArgs a) {
+  __shared__ int best[kMaxDraft + 1];
+  const flashloop_verify_args& c = a.c;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  const int n = drafts_of(a, b), D = c.D;
   const int32_t* draft = c.draft + static_cast<size_t>(b) * D;
   int32_t* tokens = c.tokens + static_cast<size_t>(b) * (D + 1);
   const RowPart* part = a.part + static_cast<size_t>(b) * (2 * D + 1) * a.n_chunks;
-  auto best_of = [&](int r, float& m, int& at) {   // (one warp)
-    m = -INFINITY;
-    at = INT_MAX;
+  pdl_wait();
+  for (int i = warp; i <= n; i += 8) {
+    float m = -INFINITY;
+    int at = INT_MAX;
     for (int k = lane; k < a.n_chunks; k += 32) {
-      const RowPart p = part[static_cast<size_t>(r) * a.n_chunks + k];
+      const RowPart p = part[static_cast<size_t>(i) * a.n_chunks + k];
       if (p.m > m || at == INT_MAX) {
         m = p.m;
         at = p.at;
@@ -162,205 +444,23 @@ __global__ void __launch_bounds__(kVfThreads) k_verify_pick(const VerifyArgs a) 
     }
     const float mm = warp_max(m);
     at = __reduce_min_sync(0xffffffffu, m == mm ? at : INT_MAX);
-    m = mm;
-  };
-  if (c.temperature == 0.f) {
-    if (rank != 0) return;
-    for (int i = warp; i <= n; i += NW) {
-      float m;
-      int at;
-      best_of(i, m, at);
-      if (lane == 0 && i < n) verdict[i] = draft[i] == at ? 1 : 0;
-    }
-    __syncthreads();
-    int acc = 0;
-    while (acc < n && verdict[acc] == 1) ++acc;
-    if (warp == 0) {
-      float m;
-      int at;
-      best_of(acc, m, at);
-      for (int i = lane; i <= D; i += 32) tokens[i] = i < acc ? draft[i] : i == acc ? at : -1;
-      if (lane == 0) c.n_accepted[b] = acc;
-    }
-    return;
-  }
-  // sum and maximum of a row from the first launch (one warp)
-  auto norm_of = [&](int r, float& m, double& z) {
-    m = -INFINITY;
-    for (int k = lane; k < a.n_chunks; k += 32) m = fmaxf(m, part[static_cast<size_t>(r) * a.n_chunks + k].m);
-    m = warp_max(m);
-    z = 0.0;
-    for (int k = lane; k < a.n_chunks; k += 32) {
-      const RowPart p = part[static_cast<size_t>(r) * a.n_chunks + k];
-      if (p.m == -INFINITY)
-        z += p.s;   // 0, or NaN
-      else
-        z += p.s * exp2(static_cast<double>(p.m - m) * a.scale2);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-  };
-  for (int i = warp; i < n; i += NW) {
-    const int x = draft[i];
-    float m;
-    double z;
-    norm_of(i, m, z);
-    double p = 0.0, q = 1.0;
-    const bool in = x >= 0 && x < V;
-    if (in) p = exp2(static_cast<double>(row_of(a, b, i)[x] - m) * a.scale2) / z;
-    if (c.draft_logits && in) {
-      norm_of(D + 1 + i, m, z);
-      q = exp2(static_cast<double>(row_of(a, b, D + 1 + i)[x] - m) * a.scale2) / z;
-    }
-    const double uq = static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + i]) * q;
-    if (lane == 0) verdict[i] = in && fabs(uq - p) <= 1e-4 * p ? 2 : (in && uq < p ? 1 : 0);
+    if (lane == 0) best[i] = at;
   }
   __syncthreads();
-  // this CTA's tokens, and this warp's
-  const int per = ((V + nc - 1) / nc + 31) & ~31;
-  const int c0 = min(V, rank * per), c1 = min(V, c0 + per);
-  const int pw = ((c1 - c0 + NW - 1) / NW + 31) & ~31;
-  const int w0 = min(c1, c0 + warp * pw), w1 = min(c1, w0 + pw);
-  int buf = 0;
-  // 64-bit sums of 2^((x - m) scale2) of target row i and draft row i over the cluster
-  auto exact_sums = [&](int i, bool with_draft, float& mp, float& mq, double& zp, double& zq) {
-    if (warp < 2) {
-      float m = 0.f;
-      double z;
-      if (warp == 0 || with_draft) norm_of(warp == 0 ? i : D + 1 + i, m, z);
-      if (lane == 0) row_max[warp] = m;
-    }
-    __syncthreads();
-    mp = row_max[0];
-    mq = row_max[1];
-    const float* xp = row_of(a, b, i);
-    double sp = 0.0, sq = 0.0;
-    for (int j = w0 + lane; j < w1; j += 32) sp += exp2(static_cast<double>(xp[j] - mp) * a.scale2);
-    if (with_draft) {
-      const float* xq = row_of(a, b, D + 1 + i);
-      for (int j = w0 + lane; j < w1; j += 32) sq += exp2(static_cast<double>(xq[j] - mq) * a.scale2);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      sp += __shfl_xor_sync(0xffffffffu, sp, o);
-      sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    }
-    if (lane == 0) {
-      wsum[0][warp] = sp;
-      wsum[1][warp] = sq;
-    }
-    __syncthreads();
-    if (tid < 2) {
-      double t = 0.0;
-      for (int w = 0; w < NW; ++w) t += wsum[tid][w];
-      cta_sum[buf][tid] = t;
-    }
-    cl.sync();
-    zp = zq = 0.0;
-    for (int r = 0; r < nc; ++r) {
-      const double* s = cl.map_shared_rank(&cta_sum[buf][0], r);
-      zp += s[0];
-      zq += s[1];
-    }
-    buf ^= 1;
-  };
   int acc = 0;
-  float mp = 0.f, mq = 0.f;
-  double zp = 0.0, zq = 0.0;
-  bool have = false;   // the exact sums of row acc are at hand
-  while (acc < n && verdict[acc] != 0) {   // (the same in every CTA of the cluster)
-    if (verdict[acc] == 2) {
-      exact_sums(acc, c.draft_logits != nullptr, mp, mq, zp, zq);
-      const int x = draft[acc];
-      const double p = exp2(static_cast<double>(row_of(a, b, acc)[x] - mp) * a.scale2) / zp;
-      const double q = c.draft_logits ? exp2(static_cast<double>(row_of(a, b, D + 1 + acc)[x] - mq) * a.scale2) / zq : 1.0;
-      if (!(static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + acc]) * q < p)) {
-        have = true;
-        break;
-      }
-    }
-    ++acc;
-  }
-  const bool residual = acc < n;
-  const bool with_draft = residual && c.draft_logits != nullptr;
-  if (!have) exact_sums(acc, with_draft, mp, mq, zp, zq);
-  const float* xp = row_of(a, b, acc);
-  const float* xq = with_draft ? row_of(a, b, D + 1 + acc) : nullptr;
-  const int x_out = residual && !with_draft ? draft[acc] : -1;   // a draft without probabilities: its own token is out
-  const double ip = 1.0 / zp, iq = with_draft ? 1.0 / zq : 0.0;
-  auto weight = [&](int j) {
-    double w = exp2(static_cast<double>(xp[j] - mp) * a.scale2) * ip;
-    if (with_draft) w = fmax(w - exp2(static_cast<double>(xq[j] - mq) * a.scale2) * iq, 0.0);
-    return j == x_out ? 0.0 : w;
-  };
-  double s = 0.0;
-  for (int j = w0 + lane; j < w1; j += 32) s += weight(j);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) wsum[0][warp] = s;
-  __syncthreads();
-  if (tid == 0) {
-    double t = 0.0;
-    for (int w = 0; w < NW; ++w) t += wsum[0][w];
-    cta_sum[buf][0] = t;
-  }
-  cl.sync();
-  double total = 0.0, before = 0.0;
-  int last_cta = -1;   // the last CTA with any weight
-  for (int r = 0; r < nc; ++r) {
-    const double t = *cl.map_shared_rank(&cta_sum[buf][0], r);
-    if (r < rank) before += t;
-    total += t;
-    if (t > 0.0) last_cta = r;
-  }
-  cl.sync();   // nobody's shared memory is read from here on
-  const bool fine = isfinite(total) && total > 0.0 && isfinite(zp) && (!with_draft || (isfinite(zq) && zq > 0.0));
-  if (rank == 0) {
-    for (int i = tid; i <= D; i += kVfThreads)
-      if (i != acc || !fine) tokens[i] = i < acc ? draft[i] : -1;
-    if (tid == 0) c.n_accepted[b] = acc;
-  }
-  if (!fine) return;
-  const double target = static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + D]) * total;
-  const double mine = cta_sum[buf][0];
-  // the CTA whose range holds the crossing (the last with any weight, should rounding leave none)
-  if (!(before <= target && (target < before + mine || rank == last_cta)) || mine <= 0.0) return;
-  int last_warp = -1, w_at = -1;
-  double run = before, start = before;
-  for (int w = 0; w < NW; ++w) {
-    if (wsum[0][w] > 0.0) last_warp = w;
-    if (w_at < 0 && target < run + wsum[0][w]) {
-      w_at = w;
-      start = run;
-    }
-    run += wsum[0][w];
-  }
-  if (w_at < 0) {
-    w_at = last_warp;
-    start = before;
-    for (int w = 0; w < w_at; ++w) start += wsum[0][w];
-  }
-  if (warp != w_at) return;
-  int found = INT_MAX, last_pos = -1;
-  for (int j0 = w0; j0 < w1 && found == INT_MAX; j0 += 32) {
-    const double w = j0 + lane < w1 ? weight(j0 + lane) : 0.0;
-    double incl = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned over = __ballot_sync(0xffffffffu, w > 0.0 && start + incl > target);
-    const unsigned any = __ballot_sync(0xffffffffu, w > 0.0);
-    if (any) last_pos = j0 + 31 - __clz(any);
-    if (over) found = j0 + __ffs(over) - 1;
-    start += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  if (lane == 0) tokens[acc] = found != INT_MAX ? found : last_pos;
+  while (acc < n && draft[acc] == best[acc]) ++acc;
+  for (int i = tid; i <= D; i += 256) tokens[i] = i < acc ? draft[i] : i == acc ? best[acc] : -1;
+  if (tid == 0) c.n_accepted[b] = acc;
 }
 
 bool verify_shape_ok(int B, int D, int V) {
   return B >= 1 && B <= 65535 && D >= 0 && D <= kMaxDraft && V >= 1 && V <= (1 << 30);
+}
+// Ranges of the deciding row: about six CTAs per SM over the batch, none with
+// fewer than 1024 tokens (4 a thread), at most one range per thread of the third launch.
+void plan_sums(int B, int V, int& ctas, int& sub_len) {
+  ctas = std::min(std::min(kSumMaxCtas, std::max(1, 6 * kNumSM / B)), std::max(1, V / 1024));
+  sub_len = (ceil_div_i(V, ctas * kSumWarps) + 31) & ~31;
 }
 int verify_chunks(int V) { return ceil_div_i(V, kVfChunk); }
 
@@ -373,7 +473,8 @@ extern "C" {
 
 size_t flashloop_verify_draft_scratch_bytes(int B, int D, int V) {
   if (!verify_shape_ok(B, D, V)) return 0;
-  return align256_sz(static_cast<size_t>(B) * (2 * D + 1) * verify_chunks(V) * sizeof(RowPart)) + 256;
+  return align256_sz(static_cast<size_t>(B) * (2 * D + 1) * verify_chunks(V) * sizeof(RowPart)) +
+         align256_sz(B * sizeof(Deciding)) + align256_sz(static_cast<size_t>(B) * kSumThreads * sizeof(Sums)) + 256;
 }
 
 fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, size_t scratch_bytes,
@@ -403,23 +504,18 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   const int rows = c->D + 1 + (a.c.draft_logits ? c->D : 0);
   cudaError_t e = launch_k(false, k_verify_rows, dim3(a.n_chunks, rows, c->B), dim3(kVfThreads), 0, s, a);
   if (e != cudaSuccess) return cuda_status(e);
-  int nc = 1;   // a CTA per 4096 tokens of a row, at most 8
-  while (nc < kVfCluster && c->V > nc * 4096) nc *= 2;
-  if (c->temperature == 0.f) nc = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(nc, c->B);
-  cfg.blockDim = dim3(kVfThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = nc;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cuda_status(cudaLaunchKernelEx(&cfg, k_verify_pick, a));
+  if (c->temperature == 0.f)
+    return cuda_status(launch_k(true, k_verify_greedy, dim3(c->B), dim3(256), 0, s, a));
+  int ctas;
+  plan_sums(c->B, c->V, ctas, a.sub_len);
+  a.n_sub = ctas * kSumWarps;
+  uint8_t* ws = static_cast<uint8_t*>(scratch) +
+                align256_sz(static_cast<size_t>(c->B) * (2 * c->D + 1) * a.n_chunks * sizeof(RowPart));
+  a.deciding = reinterpret_cast<Deciding*>(ws);
+  a.sums = reinterpret_cast<Sums*>(ws + align256_sz(c->B * sizeof(Deciding)));
+  e = launch_k(true, k_verify_sums, dim3(ctas, c->B), dim3(kSumThreads), 0, s, a);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_k(true, k_verify_pick, dim3(c->B), dim3(kSumThreads), 0, s, a));
 }
 
 }  // extern "C"

@@ -363,6 +363,8 @@ VD = [
     (16, 0, 700, 1.0, None, True),
     (2, 64, 300, 2.0, None, True),
     (32, 4, 50, 1.0, None, True),
+    (2, 2, 300007, 1.0, None, True),
+    (300, 1, 2100, 0.9, None, True),
 ]
 
 
