@@ -18,9 +18,10 @@ namespace cg = cooperative_groups;
 namespace fl {
 namespace {
 
-constexpr int kEvThreads = 1024, kEvWarps = kEvThreads / 32;
-constexpr int kEvCluster = 8;             // CTAs of one (sequence, KV head) at most
-constexpr int kEvKeys = 32768;            // keys one CTA holds in shared memory (128 KB)
+constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
+constexpr int kEvCopies = 8;              // histograms a CTA's lanes share
+constexpr int kEvCluster = 16;            // CTAs of one (sequence, KV head) at most (over 8: non-portable)
+constexpr int kEvKeys = 32 * kEvThreads;  // keys one CTA holds in shared memory (64 KB), a word of 32 slots per thread
 constexpr int kEvSlots = kEvCluster * kEvKeys;
 
 struct EvictArgs {
@@ -33,36 +34,40 @@ struct EvictArgs {
   int32_t* n_kept;      // [B * Hkv]
 };
 
-// Exclusive prefix sums of the warps' counts, in place, and their total (one warp; 32 warps).
+// Exclusive prefix sums of the warps' counts, in place, and their total (one warp; kEvWarps of them).
 __device__ __forceinline__ void scan_warps(int* v, int* total) {
-  const int lane = threadIdx.x & 31, x = v[lane];
+  const int lane = threadIdx.x & 31, x = lane < kEvWarps ? v[lane] : 0;
   int incl = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  v[lane] = incl - x;
+  if (lane < kEvWarps) v[lane] = incl - x;
   if (lane == 31) *total = incl;
 }
 
 // ============================================================================
-// Selection: a cluster of 1-8 CTAs per (sequence, KV head), each with a contiguous
+// Selection: a cluster of 1-16 CTAs per (sequence, KV head), each with a contiguous
 // chunk of slots, its keys in shared memory.  Key: 0xFFFFFFFF when protected, else the
 // weight's bits (at most 0xFFFFFFFE).  Four 8-bit digits, largest first: every
 // CTA histograms the keys that match the digits found so far, and after a
 // cluster barrier reads all CTAs' histograms over distributed shared memory and
-// finds the next digit by itself.  Latency-bound (13 cluster barriers at most);
-// the chunk keeps every pass over the keys short.
+// finds the next digit by itself.  Latency-bound (a round trip to memory, then
+// about ten barriers).
 // ============================================================================
 __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) {
   cg::cluster_group cl = cg::this_cluster();
   extern __shared__ uint32_t keys[];        // [chunk]
-  __shared__ int hist[2][256];              // one per digit parity: a barrier per digit suffices
+  __shared__ int lane_hist[kEvCopies * 257]; // counters of lanes l, l + 8, ..: keys of one magnitude share their
+                                            // leading digits, and adds to one address go one after the other
+  __shared__ int hist[2][256];              // this CTA's, one per digit parity: a cluster barrier per digit suffices
   __shared__ int tot[256];
-  __shared__ int newest_sm, sel_digit, sel_before;
-  __shared__ int warp_a[kEvWarps], warp_b[kEvWarps];
-  __shared__ int cta_eq, cta_hole, cta_move;
+  __shared__ int newest_sm, sel_digit, sel_before, sel_count;
+  __shared__ int warp_a[kEvWarps];
+  __shared__ int cta_eq, cta_both;
+  __shared__ uint32_t kept_w[kEvThreads];   // kept slots, a bit each: word t is thread t's
+  __shared__ int hole_at[kEvThreads], move_at[kEvThreads];
   const flashloop_evict_args& c = a.c;
   const int nc = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,44 +85,66 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
   const int32_t* pos = c.pos + b * c.pos_stride[0] + g * c.pos_stride[1] + lo;
   // ---- the newest token
   if (tid == 0) newest_sm = INT_MIN;
-  if (tid < 512) (&hist[0][0])[tid] = 0;
   __syncthreads();
   int newest = INT_MIN;
-  for (int i = tid; i < m; i += kEvThreads) newest = max(newest, pos[i]);
+#pragma unroll 4
+  for (int i = tid; i < m; i += kEvThreads) {
+    keys[i] = min(__float_as_uint(acc[i]), 0xFFFFFFFEu);
+    newest = max(newest, pos[i]);
+  }
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) atomicMax(&newest_sm, newest);
-  cl.sync();
+  auto sync_all = [&]() {   // the cluster, or its one CTA
+    if (nc > 1) cl.sync();
+    else __syncthreads();
+  };
+  sync_all();
   for (int r = 0; r < nc; ++r) newest = max(newest, *cl.map_shared_rank(&newest_sm, r));
   const long long oldest_safe = static_cast<long long>(newest) - c.recent;   // protected above it
   // ---- keys, and the digits of the keep-th one
+  for (int i = tid; i < kEvCopies * 257; i += kEvThreads) lane_hist[i] = 0;
+#pragma unroll 4
   for (int i = tid; i < m; i += kEvThreads) {
     const int p = pos[i];
-    keys[i] = p < c.sinks || p > oldest_safe ? 0xFFFFFFFFu : min(__float_as_uint(acc[i]), 0xFFFFFFFEu);
+    if (p < c.sinks || p > oldest_safe) keys[i] = 0xFFFFFFFFu;
   }
+  __syncthreads();
   uint32_t prefix = 0, mask = 0;
-  int k_rem = c.keep;
+  int k_rem = c.keep;      // keys still to keep among those that match the digits so far
+  bool ties = true;        // more keys than that match
 #pragma unroll 1
-  for (int d = 0; d < 4; ++d) {
+  for (int d = 0; d < 4 && ties; ++d) {
     const int shift = 24 - 8 * d;
     int* h = hist[d & 1];
-    __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < m; i += kEvThreads) {
       const uint32_t u = keys[i];
-      if ((u & mask) == prefix) atomicAdd(&h[(u >> shift) & 0xFF], 1);
-    }
-    cl.sync();
-    if (tid < 256) {
-      int s = 0;
-      for (int r = 0; r < nc; ++r) s += cl.map_shared_rank(h, r)[tid];
-      tot[tid] = s;
-      hist[(d & 1) ^ 1][tid] = 0;   // the other digit's: every CTA read it before the last barrier but one
+      if ((u & mask) == prefix) atomicAdd(&lane_hist[(lane % kEvCopies) * 257 + ((u >> shift) & 0xFF)], 1);
     }
     __syncthreads();
-    if (warp == 0) {
+    if (tid < 256) {
+      int s = 0;
+#pragma unroll
+      for (int l = 0; l < kEvCopies; ++l) s += lane_hist[l * 257 + tid];
+      h[tid] = s;
+    }
+    if (nc > 1) {
+      cl.sync();
+      if (tid < 256) {
+        int s = 0;
+        for (int r = 0; r < nc; ++r) s += cl.map_shared_rank(h, r)[tid];
+        tot[tid] = s;
+      }
+    }
+    __syncthreads();
+    if (warp != 0) {   // meanwhile: the next digit's counters
+      for (int i = tid - 32; i < kEvCopies * 257; i += kEvThreads - 32) lane_hist[i] = 0;
+    } else {
+      const int* t = nc > 1 ? tot : h;
       int cnt[8], mine = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        cnt[e] = tot[255 - 8 * lane - e];
+        cnt[e] = t[255 - 8 * lane - e];
         mine += cnt[e];
       }
       int incl = mine;
@@ -132,6 +159,7 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
         if (before < k_rem && before + cnt[e] >= k_rem) {
           sel_digit = 255 - 8 * lane - e;
           sel_before = before;
+          sel_count = cnt[e];
         }
         before += cnt[e];
       }
@@ -140,67 +168,78 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
     k_rem -= sel_before;
     prefix |= static_cast<uint32_t>(sel_digit) << shift;
     mask |= 0xFFu << shift;
+    ties = sel_count > k_rem;   // else every key with these digits is kept: the threshold is found
   }
-  // ---- kept: every key above the keep-th, and the k_rem lowest slots equal to it.
-  // Warp w owns a contiguous run of the chunk's slots; counts per warp, then per CTA, give every slot's rank.
-  const int per = (m + kEvWarps - 1) / kEvWarps;
-  const int w0 = min(m, warp * per), w1 = min(m, w0 + per);
-  int eq = 0;
-  for (int i0 = w0; i0 < w1; i0 += 32) eq += __popc(__ballot_sync(0xffffffffu, i0 + lane < w1 && keys[i0 + lane] == prefix));
-  if (lane == 0) warp_a[warp] = eq;
-  __syncthreads();
-  if (warp == 0) scan_warps(warp_a, &cta_eq);
-  cl.sync();
-  int eq_seen = warp_a[warp];
-  for (int r = 0; r < rank; ++r) eq_seen += *cl.map_shared_rank(&cta_eq, r);
+  // ---- kept: every key from the threshold on or, when keys equal to it are left out, those above it
+  // and the k_rem lowest slots equal to it.  32 slots to a word, a word to a thread.
   const unsigned below = (1u << lane) - 1u;
-  auto kept_at = [&](int i0, int& seen) {   // of this lane's slot in [i0, i0 + 32); seen: equal keys before i0
-    const bool there = i0 + lane < w1;
-    const uint32_t u = there ? keys[i0 + lane] : 0u;
-    const unsigned eqb = __ballot_sync(0xffffffffu, there && u == prefix);
-    const bool k = there && (u > prefix || (u == prefix && seen + __popc(eqb & below) < k_rem));
-    seen += __popc(eqb);
-    return k;
-  };
-  int holes = 0, moves = 0, seen = eq_seen;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const bool k = kept_at(i0, seen), low = lo + i0 + lane < c.keep, there = i0 + lane < w1;
-    holes += __popc(__ballot_sync(0xffffffffu, there && low && !k));
-    moves += __popc(__ballot_sync(0xffffffffu, k && !low));
-  }
-  __syncthreads();   // warp_a read
-  if (lane == 0) {
-    warp_a[warp] = holes;
-    warp_b[warp] = moves;
+  const int words = (m + 31) / 32;
+  for (int w = warp; w < words; w += kEvWarps) {
+    const int i = w * 32 + lane;
+    const uint32_t u = i < m ? keys[i] : 0u;
+    const unsigned k = __ballot_sync(0xffffffffu, i < m && (ties ? u > prefix : u >= prefix));
+    const unsigned e = ties ? __ballot_sync(0xffffffffu, i < m && u == prefix) : 0u;
+    if (lane == 0) {
+      kept_w[w] = k;
+      hole_at[w] = static_cast<int>(e);
+    }
   }
   __syncthreads();
-  if (warp == 0) {
-    scan_warps(warp_a, &cta_hole);
-    scan_warps(warp_b, &cta_move);
-  }
-  cl.sync();
-  int h0 = warp_a[warp], m0 = warp_b[warp], all = 0;
-  for (int r = 0; r < nc; ++r) {
-    const int x = *cl.map_shared_rank(&cta_hole, r), y = *cl.map_shared_rank(&cta_move, r);
-    if (r < rank) {
-      h0 += x;
-      m0 += y;
+  auto scan_block = [&](int v, int* warps, int* total) {   // exclusive prefix sum over the threads (two barriers)
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
     }
-    all += x;
+    if (lane == 31) warps[warp] = incl;
+    __syncthreads();
+    if (warp == 0) scan_warps(warps, total);
+    __syncthreads();
+    return warps[warp] + incl - v;
+  };
+  if (ties) {   // (the cluster alike)
+    uint32_t e = tid < words ? static_cast<uint32_t>(hole_at[tid]) : 0u;
+    int seen = scan_block(__popc(e), warp_a, &cta_eq);
+    sync_all();
+    for (int r = 0; r < rank; ++r) seen += *cl.map_shared_rank(&cta_eq, r);
+    for (; e && seen < k_rem; e &= e - 1, ++seen) kept_w[tid] |= e & (0u - e);
+    __syncthreads();
   }
-  seen = eq_seen;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int slot = lo + i0 + lane;
-    const bool k = kept_at(i0, seen), low = slot < c.keep, there = i0 + lane < w1;
-    const unsigned hb = __ballot_sync(0xffffffffu, there && low && !k), mb = __ballot_sync(0xffffffffu, k && !low);
-    if (k && low) src[slot] = slot;
-    if (there && low && !k) a.to[seg * a.cap + h0 + __popc(hb & below)] = slot;
-    if (k && !low) a.from[seg * a.cap + m0 + __popc(mb & below)] = slot;
-    h0 += __popc(hb);
-    m0 += __popc(mb);
+  const uint32_t kw = tid < words ? kept_w[tid] : 0u;
+  const int s0 = tid * 32, n_low = min(32, max(0, c.keep - lo - s0));   // the word's slots below the budget
+  const uint32_t low = n_low >= 32 ? 0xFFFFFFFFu : (1u << n_low) - 1u;
+  const uint32_t there = m - s0 >= 32 ? 0xFFFFFFFFu : (m - s0 > 0 ? (1u << (m - s0)) - 1u : 0u);
+  // holes in the low half, moves in the high one: at most kEvKeys = 2^14 of each in a CTA
+  const uint32_t both = static_cast<uint32_t>(
+      scan_block(__popc(~kw & low & there) | __popc(kw & ~low) << 16, warp_a, &cta_both));
+  int h0 = both & 0xFFFF, m0 = both >> 16;
+  sync_all();
+  int all = 0;
+  for (int r = 0; r < nc; ++r) {
+    const uint32_t x = static_cast<uint32_t>(*cl.map_shared_rank(&cta_both, r));
+    if (r < rank) {
+      h0 += x & 0xFFFF;
+      m0 += x >> 16;
+    }
+    all += x & 0xFFFF;
   }
-  __threadfence();
-  cl.sync();   // every CTA's lists are written (and nobody reads another's shared memory any more)
+  if (tid < words) {
+    hole_at[tid] = h0;
+    move_at[tid] = m0;
+  }
+  __syncthreads();
+  for (int w = warp; w < words; w += kEvWarps) {
+    const int i = w * 32 + lane, slot = lo + i;
+    const uint32_t k = kept_w[w];
+    const bool kept = k >> lane & 1u, is_low = slot < c.keep;
+    const unsigned lowb = __ballot_sync(0xffffffffu, is_low), hb = __ballot_sync(0xffffffffu, i < m && is_low && !kept);
+    if (kept && is_low) src[slot] = slot;
+    if (hb >> lane & 1u) a.to[seg * a.cap + hole_at[w] + __popc(hb & below)] = slot;
+    if (kept && !is_low) a.from[seg * a.cap + move_at[w] + __popc(k & ~lowb & below)] = slot;
+  }
+  if (nc > 1) __threadfence();
+  sync_all();   // every CTA's lists are written (and nobody reads another's shared memory any more)
   for (int i = rank * kEvThreads + tid; i < all; i += nc * kEvThreads)
     src[__ldcg(&a.to[seg * a.cap + i])] = __ldcg(&a.from[seg * a.cap + i]);
 }
@@ -236,7 +275,7 @@ __global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int vec_a
     for (int u = 0; u < kEvVecs; ++u) {
       const int e = e0 + u * 256;
       from[u] = e < total ? src[row0 + e / (2 * vec)] : -1;
-      if (in_place && from[u] == row0 + e / (2 * vec)) from[u] = -1;
+      if (in_place && from[u] == row0 + e / (2 * vec)) from[u] = -1;   // it stays where it is
     }
 #pragma unroll
     for (int u = 0; u < kEvVecs; ++u) {
@@ -319,6 +358,7 @@ fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t s
   if (e != cudaSuccess) return cuda_status(e);
   if (dev < 0 || dev >= 64 || !done[dev]) {
     e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvKeys * 4);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return cuda_status(e);
     if (dev >= 0 && dev < 64) done[dev] = true;
   }
@@ -333,7 +373,7 @@ fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t s
   a.n_kept = reinterpret_cast<int32_t*>(ws + 3 * list);
   // CTAs per segment: chunks of at most 8192 slots (8 per thread and pass) while the cluster allows
   int nc = 1;
-  while (nc < kEvCluster && c->S > nc * 8192) nc *= 2;
+  while ((nc < 8 && c->S > nc * 8192) || c->S > nc * kEvKeys) nc *= 2;
   a.chunk = ceil_div_i(c->S, nc);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchConfig_t cfg = {};

@@ -277,6 +277,7 @@ EV = [
     (1, 1, 70001, 64, [70001], 1, 1, 0, True),
     (1, 1, 33000, 64, [33000], 32999, 5, 5, True),
     (2, 1, 64, 200, [64, 64], 100, 10, 0, False),
+    (1, 1, 262144, 8, [262143], 5000, 10, 1, True),
 ]
 
 
