@@ -853,11 +853,12 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, uint64_t k, uint64_t r
   return r == CUDA_SUCCESS;
 }
 
-bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2,
-                      int64_t s_row, int64_t s1, int64_t s2, uint32_t box_rows) {
+namespace {
+bool encode_tmap_4d(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2, int64_t s_row,
+                    int64_t s1, int64_t s2, uint32_t box_rows, uint32_t box_1) {
   EncodeFn fn = get_encode();
   if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || hd % 64 || rows < 1 || n1 < 1 || n2 < 1 ||
-      box_rows == 0 || box_rows > 256)
+      box_rows == 0 || box_rows > 256 || box_1 == 0 || box_1 > 256)
     return false;
   // the stride of a dimension of one element is never used; give it a valid value
   if (rows == 1) s_row = hd;
@@ -867,13 +868,24 @@ bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, 
                               static_cast<cuuint64_t>(n2)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s_row) * 2, static_cast<cuuint64_t>(s1) * 2,
                                  static_cast<cuuint64_t>(s2) * 2};
-  const cuuint32_t box[4] = {64, box_rows, 1, 1};
+  const cuuint32_t box[4] = {64, box_rows, box_1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r =
       fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2, int64_t s_row,
+                      int64_t s1, int64_t s2, uint32_t box_rows) {
+  return encode_tmap_4d(map, base, hd, rows, n1, n2, s_row, s1, s2, box_rows, 1);
+}
+bool encode_tmap_queries(CUtensorMap* map, const void* base, int hd, int H, int Tq, int B, int64_t s_h, int64_t s_t,
+                         int64_t s_b, uint32_t box_heads, uint32_t box_queries) {
+  return encode_tmap_4d(map, base, hd, H, Tq, B, s_h, s_t, s_b, box_heads, box_queries);
 }
 
 }  // namespace fl

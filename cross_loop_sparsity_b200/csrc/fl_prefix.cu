@@ -945,11 +945,9 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
 
 // ============================================================================
 // Attention weight of key columns: out = acc + sum over rows of
-// 2^(scale2 q.k - lse2).  A CTA owns 128 columns of one (sequence, KV head); its
-// keys are loaded once by TMA and every query row passes over them in blocks of
-// 32, so no sum leaves its thread until the end: no atomics, a fixed order.
+// 2^(scale2 q.k - lse2).  Every sum stays in one thread over all rows of a part, and
+// parts meet in a fixed order: no atomics.
 // ============================================================================
-constexpr int kCwCols = 128, kCwRows = 32;
 struct WeightsArgs {
   const uint16_t* q;
   long long q_sb, q_st, q_sh;
@@ -960,101 +958,315 @@ struct WeightsArgs {
   const int32_t* q_lens;
   int B, Tq, H, Hkv, G, S;
   float scale2;
+  int nt;             // k_weights_tc: queries (of G rows) per row block
+  int n_rs;           // k_weights_tc: row splits
+  float* part;        // [n_rs][B][Hkv][S] when n_rs > 1
+};
+// What the queries of sequence b see: query t columns j < min(j0 + t + 1, len) (every column when not causal).
+struct Seen {
+  int ql, len, j0;
+  bool causal;
+  __device__ Seen(const WeightsArgs& a, int b) {
+    causal = a.lens != nullptr;
+    ql = a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq;
+    len = causal ? min(max(a.lens[b], 0), a.S) : a.S;
+    j0 = causal ? len - ql : len;
+  }
+  __device__ int limit(int t) const { return causal ? min(j0 + t + 1, len) : len; }
 };
 
-template <int HD>
-__global__ void __launch_bounds__(128) k_column_weights(const __grid_constant__ CUtensorMap km, const WeightsArgs a) {
-  constexpr int NB = HD / 64;
+// ---- few rows (decode): 32-key tiles streamed by each warp from a TMA ring of its own, the
+// rows' fragments in registers.  HBM-bound: the keys are read once and nothing else is large.
+// Warps take contiguous runs of the tiles of all (sequence, KV head) pairs.
+constexpr int kWsWarps = 8, kWsStages = 3;
+template <int HD, int NM>
+__global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_constant__ CUtensorMap km, const WeightsArgs a) {
+  constexpr int NB = HD / 64, STAGE = kPxTile * HD * 2;
   extern __shared__ uint8_t sm_raw[];
-  uint8_t* ksm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qsm = ksm + kCwCols * HD * 2;
-  __shared__ __align__(8) uint64_t full;
-  __shared__ float lse_s[kCwRows];
-  __shared__ int lim_s[kCwRows];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[kWsWarps][kWsStages];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int col0 = blockIdx.x * kCwCols, g = blockIdx.y, b = blockIdx.z;
-  const bool causal = a.lens != nullptr;
-  const int ql = a.q_lens ? min(max(a.q_lens[b], 0), a.Tq) : a.Tq;
-  const int len = causal ? min(max(a.lens[b], 0), a.S) : a.S;
-  const size_t base = (static_cast<size_t>(b) * a.Hkv + g) * a.S;
-  const int ncol = min(kCwCols, a.S - col0);
-  const int top = min(col0 + kCwCols, len);   // columns of this CTA that some query sees
-  if (top <= col0 || ql == 0) {
-    if (a.out != a.acc && tid < ncol) a.out[base + col0 + tid] = a.acc[base + col0 + tid];
-    return;
-  }
   if (tid == 0) {
-    mbar_init(smem_u32(&full), 1);
+    for (int i = 0; i < kWsWarps * kWsStages; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
     fence_mbar_init();
   }
   __syncthreads();
-  if (tid == 0) {
-    mbar_arrive_expect_tx(smem_u32(&full), kCwCols * HD * 2);
+  const int tiles = (a.S + kPxTile - 1) / kPxTile;
+  const long long units = static_cast<long long>(a.B) * a.Hkv * tiles;
+  const long long w = static_cast<long long>(blockIdx.x) * kWsWarps + warp, nw = static_cast<long long>(gridDim.x) * kWsWarps;
+  const long long u0 = w * units / nw, u1 = (w + 1) * units / nw;
+  uint8_t* wring = ring + warp * kWsStages * STAGE;
+  auto issue = [&](long long u) {
+    const int st = static_cast<int>((u - u0) % kWsStages), pair = static_cast<int>(u / tiles);
+    const uint32_t dst = smem_u32(wring + st * STAGE), bar = smem_u32(&full[warp][st]);
+    mbar_arrive_expect_tx(bar, STAGE);
+#pragma unroll
     for (int bx = 0; bx < NB; ++bx)
-      tma_load_4d(smem_u32(ksm + bx * kCwCols * 128), &km, smem_u32(&full), bx * 64, col0, g, b);
-  }
-  const bool ok = mbar_wait(smem_u32(&full), 0, nullptr);
-  const uint32_t Kt = smem_u32(ksm), Qt = smem_u32(qsm);
-  float sum[4][2] = {};   // columns warp*32 + 8n + 2(lane%4) + {0, 1}
-  // queries see a prefix of the columns that grows with t: those before t_first see none of this CTA's
-  const int t_first = causal ? max(0, col0 - (len - ql)) : 0;
-  for (int r0 = t_first * a.G; r0 < ql * a.G; r0 += kCwRows) {
-    __syncthreads();
-    for (int e = tid; e < kCwRows * (HD / 8); e += 128) {
-      const int r = r0 + e / (HD / 8), c = e % (HD / 8);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < ql * a.G)
-        x = *reinterpret_cast<const uint4*>(a.q + b * a.q_sb + static_cast<long long>(r / a.G) * a.q_st +
-                                            static_cast<long long>(g * a.G + r % a.G) * a.q_sh + c * 8);
-      *reinterpret_cast<uint4*>(qsm + sw_off(kCwRows, r - r0, c)) = x;
-    }
-    if (tid < kCwRows) {
-      const int r = r0 + tid, t = r / a.G;
-      float l = -INFINITY;
-      if (r < ql * a.G) l = a.lse[(static_cast<size_t>(b) * a.Tq + t) * a.H + g * a.G + r % a.G];
-      lse_s[tid] = l * kLog2e;
-      lim_s[tid] = l == -INFINITY ? 0 : (causal ? min(len - ql + t + 1, len) : a.S);
-    }
-    __syncthreads();
+      tma_load_4d(dst + bx * kPxTile * 128, &km, bar, bx * 64, static_cast<int>(u % tiles) * kPxTile, pair % a.Hkv, pair / a.Hkv);
+  };
+  long long last = u0 - 1;   // the last tile requested (lane 0)
+  if (lane == 0)
+    for (; last + 1 < u1 && last + 1 < u0 + kWsStages; ++last) issue(last + 1);
+  int pair_at = -1;
+  uint32_t qf[NM][HD / 16][4];
+  float lse2[NM][2];
+  int lim[NM][2], lim_max = 0;
+  bool ok = true;
+  for (long long u = u0; u < u1; ++u) {
+    const int pair = static_cast<int>(u / tiles), b = pair / a.Hkv, g = pair % a.Hkv;
+    const int col0 = static_cast<int>(u % tiles) * kPxTile;
+    const long long at = static_cast<long long>(pair) * a.S + col0 + (lane >> 3) * 8 + 2 * (lane & 3) + ((lane >> 2) & 1);
+    const bool inside = at < static_cast<long long>(pair + 1) * a.S;
+    const float old = inside ? a.acc[at] : 0.f;
+    if (pair != pair_at) {
+      // the rows of this (sequence, KV head): row r is query r / G, head g G + r % G
+      pair_at = pair;
+      const Seen see(a, b);
+      lim_max = 0;
 #pragma unroll
+      for (int i = 0; i < NM; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = i * 16 + e * 8 + (lane >> 2), t = r / a.G, h = g * a.G + r % a.G;
+          const bool valid = t < see.ql;
+          const float l = valid ? a.lse[(static_cast<long long>(b) * a.Tq + t) * a.H + h] : -INFINITY;
+          lse2[i][e] = l * kLog2e;
+          lim[i][e] = l == -INFINITY ? 0 : see.limit(t);
+          lim_max = max(lim_max, lim[i][e]);
+          const uint16_t* q = a.q + b * a.q_sb + t * a.q_st + h * a.q_sh + 2 * (lane & 3);
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            qf[i][k][e] = valid ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
+            qf[i][k][2 + e] = valid ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
+          }
+        }
+      lim_max = __reduce_max_sync(0xffffffffu, lim_max);
+    }
+    const int st = static_cast<int>((u - u0) % kWsStages);
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][st]), static_cast<int>((u - u0) / kWsStages) & 1,
+                                                 nullptr));
+    float sum[4][2] = {};   // columns 8n + 2(lane%4) + {0, 1}
+    if (col0 < lim_max) {
+      const uint32_t Kt = smem_u32(wring + st * STAGE);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+        float s[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          uint32_t kf[4];
+#pragma unroll
+          for (int n2 = 0; n2 < 2; ++n2) {
+            ldsm_x4(Kt + sw_off(kPxTile, n2 * 16 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), kf);
+            mma_bf16_16816(s[n2 * 2], qf[i][k], kf[0], kf[1]);
+            mma_bf16_16816(s[n2 * 2 + 1], qf[i][k], kf[2], kf[3]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int left = lim[i][e >> 1] - (col0 + 2 * (lane & 3) + (e & 1));
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const float p = exp2f(fmaf(s[n][e], a.scale2, -lse2[i][e >> 1]));
+            sum[n][e & 1] += n * 8 < left ? p : 0.f;
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && ok && u + kWsStages < u1) {
+      issue(u + kWsStages);
+      last = u + kWsStages;
+    }
+    // over the 8 row groups; then lane l writes column (l >> 3) * 8 + 2 (l & 3) + ((l >> 2) & 1)
+    float mine = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = sum[n][e];
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if ((lane >> 2) == n * 2 + e) mine = v;
+      }
+    if (inside) a.out[at] = old + (ok ? mine : NAN);
+    __syncwarp();
+  }
+  if (!ok && lane == 0)   // a tile never arrived: let the copies in flight land (bounded) before the warp ends
+    for (long long u = max(u0, last + 1 - kWsStages); u <= last; ++u)
+      mbar_wait(smem_u32(&full[warp][(u - u0) % kWsStages]), static_cast<int>((u - u0) / kWsStages) & 1, nullptr);
+}
+
+// ---- many rows: S^T = K Q^T on tcgen05, 128 keys x 128 rows a block, so that a thread
+// owns a key and its sum needs no exchange.  One TMA thread, one MMA thread, two
+// warpgroups that take alternate row blocks (a TMEM buffer each).  Two CTAs per SM.  Bound by
+// the exponentials: 16 a clock and SM against 32 multiply-adds of head_dim 128.
+constexpr int kWtCols = 128, kWtRows = 128, kWtThreads = 320;
+template <int HD>
+__global__ void __launch_bounds__(kWtThreads, 2)
+    k_weights_tc(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap qm, const WeightsArgs a) {
+  constexpr int NB = HD / 64, BOX = 128 * 128, TILE = NB * BOX;
+  extern __shared__ uint8_t sm_raw[];
+  uint8_t* ksm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qsm = ksm + TILE;   // two row blocks
+  __shared__ __align__(8) uint64_t k_full, q_full[2], q_empty[2], d_full[2], d_empty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) float lse_s[2][kWtRows];
+  __shared__ float join[128];
+  __shared__ volatile int bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int col0 = blockIdx.x * kWtCols, g = blockIdx.y % a.Hkv, rs = blockIdx.y / a.Hkv, b = blockIdx.z;
+  const Seen see(a, b);
+  const long long base = (static_cast<long long>(b) * a.Hkv + g) * a.S;
+  float* out = a.n_rs > 1 ? a.part + static_cast<long long>(rs) * a.B * a.Hkv * a.S : a.out;
+  const int ncol = min(kWtCols, a.S - col0);
+  // queries that see any of these columns, from t0 on; this split's blocks of nt of them
+  const int t0 = see.causal ? max(0, col0 - see.j0) : 0;
+  const int all_blocks = col0 < see.len && t0 < see.ql ? (see.ql - t0 + a.nt - 1) / a.nt : 0;
+  const int first = rs * all_blocks / a.n_rs, blocks = (rs + 1) * all_blocks / a.n_rs - first;
+  if (blocks == 0) {
+    if (tid < ncol) {
+      if (a.n_rs > 1) out[base + col0 + tid] = 0.f;
+      else if (a.out != a.acc) out[base + col0 + tid] = a.acc[base + col0 + tid];
+    }
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(smem_u32(&k_full), 1);
     for (int i = 0; i < 2; ++i) {
-      float s[4][4] = {};
+      mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_empty[i]), 1);
+      mbar_init(smem_u32(&d_full[i]), 1);
+      mbar_init(smem_u32(&d_empty[i]), 128);
+    }
+    fence_mbar_init();
+    bad = 0;
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&tmem_slot), 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp < 8) {
+    // ================= a warpgroup: blocks wg, wg + 2, .. =================
+    const int wg = warp >> 2, key = (warp & 3) * 32 + lane, row = tid & 127;
+    const uint32_t td = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 128;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const int j = col0 + key;
+    int phase = 0;
+    bool ok = true;
+    for (int n = wg; n < blocks; n += 2, ++phase) {
+      const int tb = t0 + (first + n) * a.nt;                 // the block's first query
+      const int t = tb + row / a.G, h = g * a.G + row % a.G;
+      float l = -INFINITY;
+      if (row < a.nt * a.G && t < see.ql) l = a.lse[(static_cast<long long>(b) * a.Tq + t) * a.H + h];
+      lse_s[wg][row] = l == -INFINITY ? INFINITY : l * kLog2e;   // +inf: the row adds nothing
+      // rows that add nothing, or columns that the block's first queries do not see: each weight is looked at
+      int edge = l == -INFINITY || (see.causal && see.limit(tb) < min(col0 + kWtCols, see.len));
+      if (wg == 0)
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
+                     "selp.s32 %0, 1, 0, q;\n\t}" : "+r"(edge)::"memory");
+      else
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+                     "selp.s32 %0, 1, 0, q;\n\t}" : "+r"(edge)::"memory");
+      // (after a wait that ran out the loop goes on without waiting, so that the barriers above still meet)
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&d_full[wg]), phase & 1, nullptr));
+      if (!ok) continue;
+      tc_fence_after();
+      // the first row (query) of the block that sees this key
+      const int r_min = see.causal ? max(0, j - see.j0 - tb) * a.G : 0;
 #pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        uint32_t qf[4], kf[4];
-        ldsm_x4(Qt + sw_off(kCwRows, i * 16 + (lane & 15), k * 2 + (lane >> 4)), qf);
+      for (int c = 0; c < kWtRows; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(td + c, r);
+        tc_wait_ld();
+        if (!edge) {
 #pragma unroll
-        for (int n2 = 0; n2 < 2; ++n2) {
-          ldsm_x4(Kt + sw_off(kCwCols, warp * 32 + n2 * 16 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)),
-                  kf);
-          mma_bf16_16816(s[n2 * 2], qf, kf[0], kf[1]);
-          mma_bf16_16816(s[n2 * 2 + 1], qf, kf[2], kf[3]);
+          for (int e = 0; e < 32; e += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(&lse_s[wg][c + e]);
+            sum[0] += ex2_approx(fmaf(__uint_as_float(r[e]), a.scale2, -l4.x));
+            sum[1] += ex2_approx(fmaf(__uint_as_float(r[e + 1]), a.scale2, -l4.y));
+            sum[2] += ex2_approx(fmaf(__uint_as_float(r[e + 2]), a.scale2, -l4.z));
+            sum[3] += ex2_approx(fmaf(__uint_as_float(r[e + 3]), a.scale2, -l4.w));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float l2 = lse_s[wg][c + e];
+            const float p = ex2_approx(fmaf(__uint_as_float(r[e]), a.scale2, -l2));
+            sum[e & 3] += c + e >= r_min && l2 < INFINITY ? p : 0.f;
+          }
         }
       }
+      tc_fence_before();
+      mbar_arrive(smem_u32(&d_empty[wg]));
+    }
+    if (!ok) bad = 1;
+    float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    if (j >= see.len) total = 0.f;   // (a column past the sequence: nobody sees it)
+    if (wg == 1) join[key] = total;
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    if (wg == 0 && key < ncol) {
+      total += join[key];
+      if (bad) total = NAN;
+      out[base + j] = a.n_rs > 1 ? total : a.acc[base + j] + total;
+    }
+  } else if (tid == 8 * 32) {
+    // ================= MMA thread =================
+    constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
+    bool ok = mbar_wait(smem_u32(&k_full), 0, nullptr);
+    for (int n = 0; ok && n < blocks; ++n) {
+      const int st = n & 1, ph = n >> 1;
+      ok = mbar_wait(smem_u32(&q_full[st]), ph & 1, nullptr) && (n < 2 || mbar_wait(smem_u32(&d_empty[st]), (ph - 1) & 1, nullptr));
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = i * 16 + (lane >> 2) + (e >> 1) * 8;
-        const float l2 = lse_s[r];
-        const int lim = lim_s[r] - (col0 + warp * 32 + 2 * (lane & 3) + (e & 1));
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const float p = exp2f(s[n][e] * a.scale2 - l2);
-          sum[n][e & 1] += n * 8 < lim ? p : 0.f;
-        }
-      }
+      for (int k = 0; k < HD / 16; ++k)
+        tc_mma_bf16(tmem + st * 128, umma_desc_sw128(smem_u32(ksm) + (k >> 2) * BOX + (k & 3) * 32),
+                    umma_desc_sw128(smem_u32(qsm) + st * TILE + (k >> 2) * BOX + (k & 3) * 32), idesc, k > 0);
+      tc_commit(smem_u32(&q_empty[st]));
+      tc_commit(smem_u32(&d_full[st]));
+    }
+    if (!ok) bad = 1;
+  } else if (tid == 9 * 32) {
+    // ================= TMA thread =================
+    mbar_arrive_expect_tx(smem_u32(&k_full), TILE);
+    for (int bx = 0; bx < NB; ++bx) tma_load_4d(smem_u32(ksm) + bx * BOX, &km, smem_u32(&k_full), bx * 64, col0, g, b);
+    int n = 0;
+    for (; n < blocks; ++n) {
+      const int st = n & 1;
+      if (n >= 2 && !mbar_wait(smem_u32(&q_empty[st]), ((n >> 1) - 1) & 1, nullptr)) break;
+      mbar_arrive_expect_tx(smem_u32(&q_full[st]), a.nt * a.G * HD * 2);
+      // rows in the order (query, head of the group); queries past the tensor's last read as zero
+      for (int bx = 0; bx < NB; ++bx)
+        tma_load_4d(smem_u32(qsm) + st * TILE + bx * BOX, &qm, smem_u32(&q_full[st]), bx * 64, g * a.G,
+                    t0 + (first + n) * a.nt, b);
+    }
+    if (n < blocks) {   // the products stopped: let the copies in flight land (bounded) before the block can end
+      bad = 1;
+      mbar_wait(smem_u32(&k_full), 0, nullptr);
+      for (int i = max(0, n - 2); i < n; ++i) mbar_wait(smem_u32(&q_full[i & 1]), (i >> 1) & 1, nullptr);
     }
   }
-#pragma unroll
-  for (int n = 0; n < 4; ++n)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float v = sum[n][e];
-      v += __shfl_xor_sync(0xffffffffu, v, 4);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-      v += __shfl_xor_sync(0xffffffffu, v, 16);
-      const int c = warp * 32 + n * 8 + 2 * (lane & 3) + e;
-      if (lane < 4 && c < ncol) a.out[base + col0 + c] = a.acc[base + col0 + c] + (ok ? v : NAN);
-    }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// the row splits' sums, in order, added to acc
+__global__ void __launch_bounds__(256) k_weights_add(const WeightsArgs a, long long n) {
+  pdl_wait();
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = 0.f;
+  for (int r = 0; r < a.n_rs; ++r) s += a.part[r * n + i];
+  a.out[i] = a.acc[i] + s;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1112,7 +1324,31 @@ cudaError_t run_split_hd(int nm, bool hilo, const CUtensorMap* m, const PrefixAr
   return hilo ? run_split<HD, 2, true>(m, a, grid, pdl, s) : run_split<HD, 2, false>(m, a, grid, pdl, s);
 }
 
-size_t weights_smem(int hd) { return 1024 + static_cast<size_t>(kCwCols + kCwRows) * hd * 2; }
+size_t stream_smem(int hd) { return 1024 + static_cast<size_t>(kWsWarps) * kWsStages * kPxTile * hd * 2; }
+size_t weights_tc_smem(int hd) { return 1024 + static_cast<size_t>(kWtCols + 2 * kWtRows) * hd * 2; }
+
+// Column weights on tcgen05 when a (sequence, KV head) has more rows than two warp tiles.
+// Row splits while there are fewer CTAs than two per SM and a split keeps two row blocks.
+constexpr int kStreamRows = 32;
+struct WeightsPlan {
+  bool tc;
+  int nt, n_rs;
+  size_t bytes;
+};
+WeightsPlan plan_weights(int B, int Tq, int H, int Hkv, int S) {
+  WeightsPlan p{};
+  const int G = H / Hkv;
+  p.tc = static_cast<long long>(Tq) * G > kStreamRows;
+  p.n_rs = 1;
+  p.bytes = 256;
+  if (!p.tc) return p;
+  p.nt = std::min(kWtRows / G, 256);
+  const long long ctas = static_cast<long long>(ceil_div_i(S, kWtCols)) * Hkv * B;
+  const int blocks = ceil_div_i(Tq, p.nt);
+  while (ctas * p.n_rs < 2 * kNumSM && blocks >= 4 * p.n_rs && Hkv * p.n_rs * 2 <= 65535) p.n_rs *= 2;
+  if (p.n_rs > 1) p.bytes += static_cast<size_t>(p.n_rs) * B * Hkv * S * 4;
+  return p;
+}
 
 }  // namespace
 
@@ -1138,8 +1374,12 @@ cudaError_t serving_init_attrs() {
   set(k_prefix_split<128, 2, true>, split_smem(128, 2, true));
   set(k_prefix_tc<64>, 1024 + TcSmem<64>::kBytes);
   set(k_prefix_tc<128>, 1024 + TcSmem<128>::kBytes);
-  set(k_column_weights<64>, weights_smem(64));
-  set(k_column_weights<128>, weights_smem(128));
+  set(k_weights_stream<64, 1>, stream_smem(64));
+  set(k_weights_stream<64, 2>, stream_smem(64));
+  set(k_weights_stream<128, 1>, stream_smem(128));
+  set(k_weights_stream<128, 2>, stream_smem(128));
+  set(k_weights_tc<64>, weights_tc_smem(64));
+  set(k_weights_tc<128>, weights_tc_smem(128));
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
 }
@@ -1259,7 +1499,7 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
 
 size_t flashloop_column_weights_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int S) {
   if (!heads_ok(B, Tq, H, Hkv, hd) || S < 0) return 0;
-  return 256;
+  return plan_weights(B, Tq, H, Hkv, S).bytes;
 }
 
 fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratch, size_t scratch_bytes,
@@ -1287,13 +1527,35 @@ fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratc
   w.lse = a->lse; w.acc = a->acc; w.out = a->out; w.lens = a->lens; w.q_lens = a->lens ? a->q_lens : nullptr;
   w.B = a->B; w.Tq = a->Tq; w.H = a->H; w.Hkv = a->Hkv; w.G = a->H / a->Hkv; w.S = a->S;
   w.scale2 = a->scale * kLog2e;
-  CUtensorMap km;
-  if (!encode_tmap_rows(&km, a->k, a->hd, a->S, a->Hkv, a->B, a->k_stride[2], a->k_stride[1], a->k_stride[0], kCwCols))
+  const WeightsPlan p = plan_weights(a->B, a->Tq, a->H, a->Hkv, a->S);
+  CUtensorMap km, qm;
+  if (!encode_tmap_rows(&km, a->k, a->hd, a->S, a->Hkv, a->B, a->k_stride[2], a->k_stride[1], a->k_stride[0],
+                        p.tc ? kWtCols : kPxTile))
     return refuse(FL_ERR_INVALID_ARG, "tensor map encoding failed");
-  const dim3 grid(ceil_div_i(a->S, kCwCols), a->Hkv, a->B);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(a->hd == 128 ? launch_k(false, k_column_weights<128>, grid, dim3(128), weights_smem(128), s, km, w)
-                                  : launch_k(false, k_column_weights<64>, grid, dim3(128), weights_smem(64), s, km, w));
+  if (!p.tc) {
+    const long long units = static_cast<long long>(a->B) * a->Hkv * ceil_div_i(a->S, kPxTile);
+    const dim3 grid(static_cast<unsigned>(std::min<long long>(kNumSM, (units + kWsWarps - 1) / kWsWarps)));
+    const int block = 32 * kWsWarps;
+    const size_t sm = stream_smem(a->hd);
+    if (a->Tq * w.G > 16)
+      return cuda_status(a->hd == 128 ? launch_k(false, k_weights_stream<128, 2>, grid, dim3(block), sm, s, km, w)
+                                      : launch_k(false, k_weights_stream<64, 2>, grid, dim3(block), sm, s, km, w));
+    return cuda_status(a->hd == 128 ? launch_k(false, k_weights_stream<128, 1>, grid, dim3(block), sm, s, km, w)
+                                    : launch_k(false, k_weights_stream<64, 1>, grid, dim3(block), sm, s, km, w));
+  }
+  // the queries as [B][Tq][H][hd] with boxes of nt queries x the group's heads
+  if (!encode_tmap_queries(&qm, a->q, a->hd, a->H, a->Tq, a->B, a->q_stride[2], a->q_stride[1], a->q_stride[0], w.G, p.nt))
+    return refuse(FL_ERR_INVALID_ARG, "tensor map encoding failed");
+  w.nt = p.nt;
+  w.n_rs = p.n_rs;
+  w.part = static_cast<float*>(scratch);
+  const dim3 grid(ceil_div_i(a->S, kWtCols), a->Hkv * p.n_rs, a->B);
+  e = a->hd == 128 ? launch_k(false, k_weights_tc<128>, grid, dim3(kWtThreads), weights_tc_smem(128), s, km, qm, w)
+                   : launch_k(false, k_weights_tc<64>, grid, dim3(kWtThreads), weights_tc_smem(64), s, km, qm, w);
+  if (e != cudaSuccess || p.n_rs == 1) return cuda_status(e);
+  const long long n = static_cast<long long>(a->B) * a->Hkv * a->S;
+  return cuda_status(launch_k(true, k_weights_add, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, w, n));
 }
 
 }  // extern "C"

@@ -32,6 +32,11 @@ inline bool stride_ok(int64_t stride, int64_t dim, int64_t unit) {
 bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2,
                       int64_t s_row, int64_t s1, int64_t s2, uint32_t box_rows);
 
+// Tensor map over bf16 queries [B][Tq][H][hd] with element strides, 128-byte
+// swizzle, box 64 dims x box_heads heads x box_queries queries.
+bool encode_tmap_queries(CUtensorMap* map, const void* base, int hd, int H, int Tq, int B, int64_t s_h, int64_t s_t,
+                         int64_t s_b, uint32_t box_heads, uint32_t box_queries);
+
 // The prefix attention as launched: the C arguments, or a context's decode step
 // (fp32 queries, an fp32 copy of the output, lengths offset by lens_add).
 struct PrefixLaunch {

@@ -206,6 +206,11 @@ CW = [
     (2, 20, 3, 1, 128, 128, [128, 0], [20, 20]),
     (1, 300, 8, 1, 128, 1025, None, None),
     (2, 600, 2, 1, 64, 900, [900, 650], [600, 599]),
+    (1, 40, 5, 1, 128, 33, [33], [40]),
+    (3, 9, 4, 1, 64, 131, [131, 60, 9], [9, 0, 9]),
+    (1, 2, 64, 1, 128, 400, None, None),
+    (1, 700, 3, 1, 64, 260, None, None),
+    (5, 4, 4, 2, 128, 33, [33, 1, 0, 32, 7], [4, 4, 4, 2, 1]),
 ]
 
 
