@@ -49,21 +49,41 @@ struct PrefixArgs {
   float2* tc_ml;          // [tc_ctas + Hkv * row blocks][kTcRows]
 };
 
+// a / b for a, b >= 0: most quotients here fit the 32-bit divider, several times faster than the 64-bit one
+__device__ __forceinline__ long long quick_div(long long a, long long b) {
+  return (static_cast<unsigned long long>(a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                                                         : a / b;
+}
+
 // How k_prefix_tc divides the prefix: row blocks of kTcRows packed query rows, 128-key tiles; the
-// (row block, KV head, tile) units in this order, evenly over the CTAs, so a CTA's
-// range covers few (row block, head) pairs.  CTA c's part of pair p is partial c + p.
+// (row block, KV head, tile) units in this order, evenly over the CTAs by cost, so a CTA's
+// range covers few (row block, head) pairs.  CTA c's part of pair p is partial c + p.  A unit of a
+// block with more than 128 rows is two products of 128 rows; one of a shorter block is one,
+// at 0.7 of the cost (it reads the same keys and values).
 constexpr int kTcRows = 256, kTcTile = 128, kTcMinTiles = 2;
 struct TcPlan {
   int nblk, ntiles, ctas;
-  long long units;
+  long long units, full;     // all units; those of blocks with more than 128 rows, which come first
   __device__ TcPlan(const PrefixArgs& a, int queries) {
-    nblk = (queries * a.G + kTcRows - 1) / kTcRows;
+    const int rows = queries * a.G;
+    nblk = (rows + kTcRows - 1) / kTcRows;
     ntiles = (a.P + kTcTile - 1) / kTcTile;
-    units = static_cast<long long>(nblk) * a.Hkv * ntiles;
-    ctas = static_cast<int>(min(static_cast<long long>(a.tc_ctas), max(1LL, units / kTcMinTiles)));
+    const long long per_block = static_cast<long long>(a.Hkv) * ntiles;
+    units = nblk * per_block;
+    full = rows - (nblk - 1) * kTcRows > 128 ? units : units - per_block;
+    ctas = static_cast<int>(min(static_cast<long long>(a.tc_ctas), max(1LL, quick_div(units, kTcMinTiles))));
   }
-  __device__ long long begin(int c) const { return c * units / ctas; }
-  __device__ int cta_of(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
+  __device__ long long cost(long long u) const { return u <= full ? 10 * u : 10 * full + 7 * (u - full); }
+  __device__ long long begin(int c) const {   // first unit of CTA c: at least two units' cost apart
+    const long long x = quick_div(c * cost(units), ctas);
+    return x <= 10 * full ? quick_div(x + 9, 10) : full + quick_div(x - 10 * full + 6, 7);
+  }
+  __device__ int cta_of(long long u) const {
+    int c = min(ctas - 1, static_cast<int>(quick_div(cost(u) * ctas, cost(units))));
+    while (c > 0 && begin(c) > u) --c;
+    while (c + 1 < ctas && begin(c + 1) <= u) ++c;
+    return c;
+  }
 };
 
 __device__ __forceinline__ int q_len_of(const PrefixArgs& a, int b) {
@@ -458,13 +478,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* vsm = ksm + KS * C::kTileBytes;
   __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_ready[2], o_done[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int row_id[kTcRows];
+  __shared__ uint32_t row_off[kTcRows];   // a query row's place in q, in 16-byte units (~0: no row)
   int* slot_sm = reinterpret_cast<int*>(qsm);            // while the query tiles are not there yet
   float2* join_ml = reinterpret_cast<float2*>(ksm + 128 * OLD * 4);
   __shared__ int total_sm;
   __shared__ volatile int bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  if (tid == 9 * 32) {
+    tma_prefetch_desc(&kp);
+    tma_prefetch_desc(&vp);
+  }
   if (tid == 0) {
     for (int i = 0; i < KS; ++i) {
       mbar_init(smem_u32(&k_full[i]), 1);
@@ -510,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     u_end = plan.begin(blockIdx.x + 1);
   }
   while (u < u_end && !bad) {
-    const int pair = static_cast<int>(u / plan.ntiles), t0 = static_cast<int>(u % plan.ntiles);
+    const int pair = static_cast<int>(quick_div(u, plan.ntiles)), t0 = static_cast<int>(u - static_cast<long long>(pair) * plan.ntiles);
     const int nt = static_cast<int>(min(static_cast<long long>(plan.ntiles - t0), u_end - u));
     const int g = pair % a.Hkv, r0 = pair / a.Hkv * kTcRows;
     const int rows = min(kTcRows, nrows - r0);
@@ -546,29 +570,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         load_v(v_at++);
       }
     }
+    // (warps 0-8: the TMA warp is not waited for, nor does it read the queries)
     if (warp == 0) {
       const int first = r0 / a.G, count = (r0 + rows - 1) / a.G - first + 1;
       pack_queries(a, first, count, slot_sm);
     }
-    __syncthreads();
-    if (tid < kTcRows) {
-      const int r = r0 + tid;
-      row_id[tid] = tid < rows ? slot_sm[r / a.G - r0 / a.G] * a.H + g * a.G + r % a.G : -1;   // (at most 2^30 rows)
-    }
-    __syncthreads();
-    for (int e = tid; e < (two ? 256 : 128) * (HD / 8); e += kTcThreads) {
-      const int r = e / (HD / 8), c = e % (HD / 8);
-      const int id = row_id[r];
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (id >= 0) {
-        const int s = id / a.H, h = id % a.H;
-        x = *reinterpret_cast<const uint4*>(a.q + (s / a.Tq) * a.q_sb + (s % a.Tq) * a.q_st + h * a.q_sh + c * 8);
+    if (warp < 8) {
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int r = r0 + tid, sl = tid < rows ? slot_sm[r / a.G - r0 / a.G] : 0;
+      const long long off = (sl / a.Tq) * a.q_sb + (sl % a.Tq) * a.q_st + (g * a.G + r % a.G) * a.q_sh;
+      row_off[tid] = tid < rows ? static_cast<uint32_t>(off >> 3) : ~0u;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      constexpr int CH = HD / 8;                 // chunks of a row: thread t copies chunk t % CH of every (256 / CH)-th row
+      const int c = tid % CH;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int qr = tid / CH + i * (256 / CH);
+        if (qr < 128 || two) {
+          const uint32_t off16 = row_off[qr];
+          cp_async_16(smem_u32(qsm + (qr >> 7) * C::kTileBytes + sw_off(128, qr & 127, c)),
+                      a.q + (off16 == ~0u ? 0 : static_cast<long long>(off16) * 8 + c * 8), off16 == ~0u ? 0u : 16u);
+        }
       }
-      x.x ^= flip; x.y ^= flip; x.z ^= flip; x.w ^= flip;
-      *reinterpret_cast<uint4*>(qsm + (r >> 7) * C::kTileBytes + sw_off(128, r & 127, c)) = x;
+      cp_async_wait_all();
+      if (flip)
+        for (int i = 0; i < CH; ++i) {           // the chunks this thread copied
+          const int qr = tid / CH + i * (256 / CH);
+          uint4* x = reinterpret_cast<uint4*>(qsm + (qr >> 7) * C::kTileBytes + sw_off(128, qr & 127, c));
+          if (qr < 128 || two) *x = make_uint4(x->x ^ flip, x->y ^ flip, x->z ^ flip, x->w ^ flip);
+        }
+      fence_proxy_async();
     }
-    fence_proxy_async();
-    __syncthreads();
+    if (warp < 9) asm volatile("bar.sync 2, 288;" ::: "memory");   // the MMA warp too
 
     if (warp < 8) {
       // ================= softmax warpgroup of one half =================
@@ -587,30 +620,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
         tc_fence_after();
-        // Columns 0-63 of S are read twice, once for the maximum and once for the
-        // probabilities: all 128 in registers would spill.  P goes over columns 64-127.
-        uint32_t lo[64], hi[64];
-        tmem_ld32(ts, lo);
-        tmem_ld32(ts + 32, lo + 32);
-        tc_wait_ld();
+        // S is read twice, 32 columns at a time, once for the maximum and once for the
+        // probabilities: all 128 in registers would spill.  P (bf16) goes over the columns
+        // already read: those of chunk c to columns 16 c .. 16 c + 15.
         const int ncol = a.P - (t0 + (two ? j : 2 * j + q)) * kTcTile;   // valid columns of this tile
+        uint32_t buf[2][32];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto top = [&](const uint32_t* r, int first) {
+        tmem_ld32(ts, buf[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tc_wait_ld();
+          tmem_ld32(ts + ((c + 1) & 3) * 32, buf[(c + 1) & 1]);   // (after the last: the first again)
+          const uint32_t* r = buf[c & 1];
           if (ncol >= kTcTile) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(r[c]));
+            for (int e = 0; e < 32; e += 2)
+              mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
           } else {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], first + c < ncol ? __uint_as_float(r[c]) : -INFINITY);
+            for (int e = 0; e < 32; ++e)
+              mx[e & 3] = fmaxf(mx[e & 3], c * 32 + e < ncol ? __uint_as_float(r[e]) : -INFINITY);
           }
-        };
-        top(lo, 0);
-        tmem_ld32(ts + 64, hi);
-        tmem_ld32(ts + 96, hi + 32);
-        tc_wait_ld();
-        top(hi, 64);
-        tmem_ld32(ts, lo);
-        tmem_ld32(ts + 32, lo + 32);
+        }
         const float mrow = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const float mn = mrow == -INFINITY ? -INFINITY : mrow * scale2;
         const bool grow = mn > m + 8.f || (m == -INFINITY && mn > m);
@@ -637,28 +668,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           m = m_new;
         }
         const float ms = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        auto probs = [&](const uint32_t* r, int first) {   // 32 columns
+        const uint64_t sc2 = f2_pack(scale2, scale2), ms2 = f2_pack(-ms, -ms);
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tc_wait_ld();
+          if (c < 3) tmem_ld32(ts + (c + 1) * 32, buf[(c + 1) & 1]);
+          const uint32_t* r = buf[c & 1];
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            float p0 = ex2_approx(fmaf(__uint_as_float(r[e]), scale2, -ms));
-            float p1 = ex2_approx(fmaf(__uint_as_float(r[e + 1]), scale2, -ms));
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, ms2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
             if (ncol < kTcTile) {
-              if (first + e >= ncol) p0 = 0.f;
-              if (first + e + 1 >= ncol) p1 = 0.f;
+              if (c * 32 + e >= ncol) p0 = 0.f;
+              if (c * 32 + e + 1 >= ncol) p1 = 0.f;
             }
-            sum[(e >> 1) & 3] += p0 + p1;
+            sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
             pk[e >> 1] = pack2(p0, p1);
           }
-          tmem_st16(ts + 64 + first / 2, pk);
-        };
-        probs(hi, 64);
-        probs(hi + 32, 96);
-        tc_wait_ld();
-        probs(lo, 0);
-        probs(lo + 32, 32);
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st16(ts + c * 16, pk);
+        }
+        {
+          float x, y;
+          f2_unpack(f2_add(sum2[0], sum2[1]), x, y);
+          l += x + y;
+        }
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(smem_u32(&p_ready[q]));
@@ -666,26 +703,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (ok && mine > 0 && !wait(&o_done[q], ns[0] - 1)) ok = false;
       if (!ok) bad = 1;
       tc_fence_after();
-      // ---- this segment's part of the rows: (max, sum) and the unnormalised output
-      const long long part = blockIdx.x + pair;
-      if (!two) asm volatile("bar.sync 1, 256;" ::: "memory");   // both softmax warpgroups: every product is done
-      if (!two && q == 1) join_ml[row] = make_float2(mine > 0 ? m : -INFINITY, l);
-      float* jo = reinterpret_cast<float*>(ksm) + row * OLD;   // the rings are idle: every load was consumed
-      if (!two && q == 1 && mine > 0 && ok) {
+      // ---- this segment's part of the rows: (max, sum) and the unnormalised output, a row at a
+      // time by bulk copies from shared memory (the rings are idle: every product is done)
+      const int at_row = (two ? q * 128 : 0) + row;
+      const bool have = at_row < rows;
+      const long long at = (blockIdx.x + pair) * static_cast<long long>(kTcRows) + at_row;
+      float* so = reinterpret_cast<float*>(ksm) + at_row * OLD;
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // both softmax warpgroups
+      float w0 = 1.f, w1 = 0.f, M = m, L = l;
+      if (!two) {
+        // the halves are the same rows over alternate tiles: the second leaves its sums and output, the first joins
+        if (q == 1) {
+          join_ml[row] = make_float2(mine > 0 ? m : -INFINITY, l);
+          if (mine > 0 && ok) {
+#pragma unroll 1
+            for (int c = 0; c < HD; c += 16) {
+              float o[16];
+              tmem_ld16(to + c, o);
+              tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(to + c * 32, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(jo + c * 32 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(so + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
         }
-      }
-      if (!two) asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (two || q == 0) {
-        const bool have = (two ? q * 128 : 0) + row < rows;
-        float w0 = 1.f, w1 = 0.f, M = m, L = l;
-        if (!two) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (q == 0) {
           const float2 x = join_ml[row];
           M = fmaxf(m, x.x);
           const float ms = M == -INFINITY ? 0.f : M;
@@ -693,67 +735,82 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           w1 = ex2_approx(x.x - ms);
           L = l * w0 + x.y * w1;
         }
-        const long long at = part * kTcRows + (two ? q * 128 : 0) + row;
-        if (have) a.tc_ml[at] = bad ? make_float2(0.f, NAN) : make_float2(M, L);
-#pragma unroll
-        for (int c = 0; c < HD / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(to + c * 32, o);
+      }
+      if (two || q == 0) {
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 64) {
+          uint32_t o[64];
+          tmem_ld32(to + c, o);
+          tmem_ld32(to + c + 32, o + 32);
           tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            if (!have) break;
+          for (int e = 0; e < 64; e += 4) {
             float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                    __uint_as_float(o[e + 3]));
-            if (!two) {
-              const float4 y = jobs > 1 ? *reinterpret_cast<const float4*>(jo + c * 32 + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-              x.x = x.x * w0 + y.x * w1;
-              x.y = x.y * w0 + y.y * w1;
-              x.z = x.z * w0 + y.z * w1;
-              x.w = x.w * w0 + y.w * w1;
+            if (!two && jobs > 1) {
+              const float4 y = *reinterpret_cast<const float4*>(so + c + e);
+              x = make_float4(x.x * w0 + y.x * w1, x.y * w0 + y.y * w1, x.z * w0 + y.z * w1, x.w * w0 + y.w * w1);
             }
-            *reinterpret_cast<float4*>(a.tc_o + at * HD + c * 32 + e) = x;
+            *reinterpret_cast<float4*>(so + c + e) = x;
           }
-          __syncwarp();
         }
+        if (have) {
+          a.tc_ml[at] = bad ? make_float2(0.f, NAN) : make_float2(M, L);
+          fence_proxy_async();
+          bulk_store(a.tc_o + at * HD, smem_u32(so), HD * 4);
+          bulk_commit();
+          bulk_wait_read();
+        }
+        __syncwarp();
       }
       fence_proxy_async();   // the join buffer becomes a ring again
       tc_fence_before();
-    } else if (tid == 8 * 32) {
-      // ================= MMA thread =================
+    } else if (warp == 8) {
+      // ================= MMA warp =================
+      // The whole warp runs the loop and one elected lane issues: the operands are
+      // then warp-uniform, as the instruction wants them.
       constexpr uint32_t id_s = umma_idesc_bf16(128, 128), id_o = umma_idesc_bf16(128, HD) | kIdescBMn;
       const int k0 = nk, v0 = nv, s0 = ns[0], s1 = ns[1];   // counts at the segment's start
       auto tile_of = [&](int n) { return two ? n >> 1 : n; };
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, nullptr)) != 0;
+      };
+      const uint64_t q_desc = umma_desc_sw128(smem_u32(qsm)), k_desc = umma_desc_sw128(smem_u32(ksm));
+      const uint64_t v_desc = umma_desc_sw128_mn(smem_u32(vsm), C::kBox);
       auto do_qk = [&](int n) -> bool {
         const int q = n & 1, i = tile_of(n), kt = k0 + i, st = kt % KS;
-        if (!mbar_wait(smem_u32(&k_full[st]), (kt / KS) & 1, nullptr)) return false;
+        if (!wait(&k_full[st], kt / KS)) return false;
         tc_fence_after();
-        const uint32_t qa = smem_u32(qsm + (two ? q : 0) * C::kTileBytes), kb = smem_u32(ksm + st * C::kTileBytes);
+        const uint64_t da = q_desc + (two ? q : 0) * (C::kTileBytes >> 4), db = k_desc + st * (C::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k)
-          tc_mma_bf16(tmem + q * 128, umma_desc_sw128(qa + (k >> 2) * C::kBox + (k & 3) * 32),
-                      umma_desc_sw128(kb + (k >> 2) * C::kBox + (k & 3) * 32), id_s, k > 0);
-        tc_commit(smem_u32(&s_full[q]));
-        if (!two || q == 1) tc_commit(smem_u32(&k_empty[st]));
+          for (int k = 0; k < HD / 16; ++k)
+            tc_mma_bf16(tmem + q * 128, da + (k >> 2) * (C::kBox >> 4) + (k & 3) * 2,
+                        db + (k >> 2) * (C::kBox >> 4) + (k & 3) * 2, id_s, k > 0);
+          tc_commit(smem_u32(&s_full[q]));
+          if (!two || q == 1) tc_commit(smem_u32(&k_empty[st]));
+        }
+        __syncwarp();
         return true;
       };
       bool ok = true;
       for (int n = 0; n < 2 && n < jobs; ++n) ok = ok && do_qk(n);
       for (int n = 0; ok && n < jobs; ++n) {
         const int q = n & 1, i = tile_of(n), vt = v0 + i, st = vt % VS, j = n >> 1;
-        if (!mbar_wait(smem_u32(&p_ready[q]), ((q ? s1 : s0) + j) & 1, nullptr) ||
-            !mbar_wait(smem_u32(&v_full[st]), (vt / VS) & 1, nullptr)) {
+        if (!wait(&p_ready[q], (q ? s1 : s0) + j) || !wait(&v_full[st], vt / VS)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t vb = smem_u32(vsm + st * C::kTileBytes);
+        const uint64_t db = v_desc + st * (C::kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTcTile / 16; ++k)
-          tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + 64 + k * 8,
-                         umma_desc_sw128_mn(vb + k * 2048, C::kBox), id_o, j > 0 || k > 0);
-        tc_commit(smem_u32(&o_done[q]));
-        if (!two || q == 1) tc_commit(smem_u32(&v_empty[st]));
+          for (int k = 0; k < kTcTile / 16; ++k)
+            tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + k * 8, db + k * (2048 >> 4), id_o, j > 0 || k > 0);
+          tc_commit(smem_u32(&o_done[q]));
+          if (!two || q == 1) tc_commit(smem_u32(&v_empty[st]));
+        }
+        __syncwarp();
         if (n + 2 < jobs) ok = do_qk(n + 2);
       }
       nk += nt;
@@ -793,6 +850,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (bad)   // a wait ran out: every part of this CTA becomes NaN, never a silently wrong sum
     for (long long w = plan.begin(blockIdx.x); w < u_end; w += plan.ntiles - w % plan.ntiles)
       if (tid < kTcRows) a.tc_ml[(blockIdx.x + w / plan.ntiles) * kTcRows + tid] = make_float2(0.f, NAN);
+  bulk_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 8) {
@@ -802,13 +860,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ============================================================================
-// Merge: one CTA per output row.  Groups of HD/4 lanes take every n-th split
-// (a few loads in flight each) and every n-th column of the causal tail -- the
-// columns this query sees and an earlier one of its sequence does not, at most
-// Tq - 1 -- as fp32 dot products; then the groups' (max, sum, output) meet in
-// shared memory.
+// Merge.  A group is HD/4 lanes, 4 dims each.  ALL: the CTA's groups share one
+// output row -- each takes every n-th split (a few loads in flight) and every
+// n-th column of the causal tail, and their (max, sum, output) meet in shared
+// memory; for few rows, where latency counts.  Otherwise a row per group.  The
+// causal tail: columns this query sees and an earlier one of its sequence does
+// not, at most Tq - 1, as fp32 dot products.
 // ============================================================================
-template <int HD, bool Q32>
+template <int HD, bool Q32, bool ALL>
 __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   constexpr int LPG = HD / 4;          // lanes of a group, 4 dims each
   constexpr int NG = 128 / LPG;        // groups
@@ -817,13 +876,15 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   __shared__ float4 go[NG][LPG];
   __shared__ int cnt[2][4];
   pdl_trigger();
-  const long long row = blockIdx.x;
-  const int h = static_cast<int>(row % a.H), t = static_cast<int>(row / a.H % a.Tq);
-  const int b = static_cast<int>(row / a.H / a.Tq);
-  const int grp = threadIdx.x / LPG, gl_lane = threadIdx.x % LPG;
+  const int grp = ALL ? threadIdx.x / LPG : 0, gl_lane = threadIdx.x % LPG;
+  constexpr int GS = ALL ? NG : 1;     // groups that share a row
+  const int row = ALL ? blockIdx.x : min(static_cast<int>(a.rows) - 1, static_cast<int>(blockIdx.x * NG + threadIdx.x / LPG));
+  const bool last = ALL || static_cast<int>(blockIdx.x * NG + threadIdx.x / LPG) < a.rows;   // (a group past the end repeats the last row)
+  const int slot = row / a.H, h = row - slot * a.H, b = slot / a.Tq, t = slot - b * a.Tq;
   pdl_wait();
   const int ql = q_len_of(a, b);
-  if (t >= ql) return;
+  if (ALL && t >= ql) return;
+  const bool valid = last && t < ql;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float ms, float ls, const float4& x) {   // a part with maximum ms, sum ls, output x
@@ -842,52 +903,65 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   };
   // n partials of this row, `step` rows apart from row `at`
   auto add_parts = [&](const float* po, const float2* pml, long long at, long long step, int n) {
-    for (int i0 = grp; i0 < n; i0 += NG * MB) {
+    for (int i0 = grp; i0 < n; i0 += GS * MB) {
       float2 ml[MB];
       float4 x[MB];
 #pragma unroll
       for (int u = 0; u < MB; ++u) {
-        const int i = i0 + u * NG;
+        const int i = i0 + u * GS;
         ml[u] = i < n ? __ldcg(&pml[at + i * step]) : make_float2(-INFINITY, 0.f);
         x[u] = i < n ? __ldcg(reinterpret_cast<const float4*>(&po[(at + i * step) * HD + gl_lane * 4]))
                      : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int u = 0; u < MB; ++u)
-        if (i0 + u * NG < n) add(ml[u].x, ml[u].y, x[u]);
+        if (i0 + u * GS < n) add(ml[u].x, ml[u].y, x[u]);
     }
   };
-  add_parts(a.part_o, a.part_ml, row, a.rows, a.n_p + a.n_s);
+  add_parts(a.part_o, a.part_ml, row, a.rows, valid ? a.n_p + a.n_s : 0);
   if (a.tc_ctas > 0) {
     // this query's number among the valid ones, and all of them
     int before = b * a.Tq, all = a.B * a.Tq;
     if (a.q_lens) {
       before = all = 0;
-      for (int i = threadIdx.x; i < a.B; i += 128) {
-        const int x = q_len_of(a, i);
-        all += x;
-        if (i < b) before += x;
+      if (ALL) {
+        for (int i = threadIdx.x; i < a.B; i += 128) {
+          const int x = q_len_of(a, i);
+          all += x;
+          if (i < b) before += x;
+        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        all = __reduce_add_sync(0xffffffffu, all);
+        if ((threadIdx.x & 31) == 0) {
+          cnt[0][threadIdx.x >> 5] = before;
+          cnt[1][threadIdx.x >> 5] = all;
+        }
+        __syncthreads();
+        before = cnt[0][0] + cnt[0][1] + cnt[0][2] + cnt[0][3];
+        all = cnt[1][0] + cnt[1][1] + cnt[1][2] + cnt[1][3];
+      } else {
+        for (int i = gl_lane; i < a.B; i += LPG) {
+          const int x = q_len_of(a, i);
+          all += x;
+          if (i < b) before += x;
+        }
+#pragma unroll
+        for (int d = LPG / 2; d > 0; d >>= 1) {
+          before += __shfl_xor_sync(0xffffffffu, before, d);
+          all += __shfl_xor_sync(0xffffffffu, all, d);
+        }
       }
-      before = __reduce_add_sync(0xffffffffu, before);
-      all = __reduce_add_sync(0xffffffffu, all);
-      if ((threadIdx.x & 31) == 0) {
-        cnt[0][threadIdx.x >> 5] = before;
-        cnt[1][threadIdx.x >> 5] = all;
-      }
-      __syncthreads();
-      before = cnt[0][0] + cnt[0][1] + cnt[0][2] + cnt[0][3];
-      all = cnt[1][0] + cnt[1][1] + cnt[1][2] + cnt[1][3];
     }
-    const TcPlan plan(a, all);
-    const int r = (before + t) * a.G + h % a.G;
+    const TcPlan plan(a, max(all, 1));
+    const int r = (valid ? before + t : 0) * a.G + h % a.G;
     const int pair = r / kTcRows * a.Hkv + h / a.G;
     const int c0 = plan.cta_of(static_cast<long long>(pair) * plan.ntiles);
     const int c1 = plan.cta_of(static_cast<long long>(pair + 1) * plan.ntiles - 1);
-    add_parts(a.tc_o, a.tc_ml, static_cast<long long>(c0 + pair) * kTcRows + r % kTcRows, kTcRows, c1 - c0 + 1);
+    add_parts(a.tc_o, a.tc_ml, static_cast<long long>(c0 + pair) * kTcRows + r % kTcRows, kTcRows, valid ? c1 - c0 + 1 : 0);
   }
   const int len = len_of(a, b);
   const int base = min(max(len - ql + 1, 0), len), lim = min(max(len - ql + t + 1, 0), len);
-  if (lim > base) {
+  if (valid && lim > base) {
     const int g = h / a.G;
     float4 q4;
     const long long qo = b * a.q_sb + t * a.q_st + h * a.q_sh + gl_lane * 4;
@@ -898,7 +972,7 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
       q4 = make_float4(bf16_to_f(u.x & 0xFFFF), bf16_to_f(u.x >> 16), bf16_to_f(u.y & 0xFFFF), bf16_to_f(u.y >> 16));
     }
     const unsigned mask = LPG == 32 ? 0xffffffffu : (0xffffu << (threadIdx.x & 16));
-    for (int j = base + grp; j < lim; j += NG) {
+    for (int j = base + grp; j < lim; j += GS) {
       const uint2 ku = *reinterpret_cast<const uint2*>(a.k + b * a.k_sb + g * a.k_sg + j * a.k_sr + gl_lane * 4);
       const uint2 vu = *reinterpret_cast<const uint2*>(a.v + b * a.v_sb + g * a.v_sg + j * a.v_sr + gl_lane * 4);
       float s = q4.x * bf16_to_f(ku.x & 0xFFFF) + q4.y * bf16_to_f(ku.x >> 16) + q4.z * bf16_to_f(ku.y & 0xFFFF) +
@@ -909,29 +983,34 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
                                          bf16_to_f(vu.y >> 16)));
     }
   }
-  if (gl_lane == 0) {
-    gm[grp] = m;
-    gl[grp] = l;
-  }
-  go[grp][gl_lane] = o;
-  __syncthreads();
-  if (threadIdx.x >= LPG) return;
-  float M = -INFINITY;
+  float M = m, L = l;
+  float4 r = o;
+  if (ALL) {
+    if (gl_lane == 0) {
+      gm[grp] = m;
+      gl[grp] = l;
+    }
+    go[grp][gl_lane] = o;
+    __syncthreads();
+    if (threadIdx.x >= LPG) return;
+    M = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < NG; ++i) M = fmaxf(M, gm[i]);
-  const float ms = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < NG; ++i) M = fmaxf(M, gm[i]);
+    const float ms = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+    r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < NG; ++i) {
-    const float w = exp2f(gm[i] - ms);
-    const float4 x = go[i][gl_lane];
-    L += w * gl[i] + (gm[i] == -INFINITY ? gl[i] : 0.f);
-    r.x += w * x.x;
-    r.y += w * x.y;
-    r.z += w * x.z;
-    r.w += w * x.w;
+    for (int i = 0; i < NG; ++i) {
+      const float w = exp2f(gm[i] - ms);
+      const float4 x = go[i][gl_lane];
+      L += w * gl[i] + (gm[i] == -INFINITY ? gl[i] : 0.f);
+      r.x += w * x.x;
+      r.y += w * x.y;
+      r.z += w * x.z;
+      r.w += w * x.w;
+    }
   }
+  if (!valid) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;   // nothing visible: 0 and -inf
   r.x *= inv;
   r.y *= inv;
@@ -939,8 +1018,8 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   r.w *= inv;
   *reinterpret_cast<uint2*>(a.out + b * a.o_sb + t * a.o_st + h * a.o_sh + gl_lane * 4) =
       make_uint2(pack_bf16x2(r.x, r.y), pack_bf16x2(r.z, r.w));
-  if (a.out32) *reinterpret_cast<float4*>(a.out32 + row * HD + gl_lane * 4) = r;
-  if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  if (a.out32) *reinterpret_cast<float4*>(a.out32 + static_cast<long long>(row) * HD + gl_lane * 4) = r;
+  if (a.lse && gl_lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 // ============================================================================
@@ -1270,6 +1349,18 @@ __global__ void __launch_bounds__(256) k_weights_add(const WeightsArgs a, long l
 }
 
 // ---------------------------------------------------------------- host side
+// A CTA per row up to four rows per SM (latency: the splits are spread over the CTA), else a row per group.
+template <int HD>
+cudaError_t run_merge(bool q32, const PrefixArgs& a, bool pdl, cudaStream_t s) {
+  constexpr int NG = 128 / (HD / 4);
+  const unsigned rows = static_cast<unsigned>(a.rows);
+  if (a.rows <= 4 * kNumSM)
+    return q32 ? launch_k(pdl, k_prefix_merge<HD, true, true>, dim3(rows), dim3(128), 0, s, a)
+               : launch_k(pdl, k_prefix_merge<HD, false, true>, dim3(rows), dim3(128), 0, s, a);
+  return q32 ? launch_k(pdl, k_prefix_merge<HD, true, false>, dim3((rows + NG - 1) / NG), dim3(128), 0, s, a)
+             : launch_k(pdl, k_prefix_merge<HD, false, false>, dim3((rows + NG - 1) / NG), dim3(128), 0, s, a);
+}
+
 // Rows per CTA and column splits of both parts.  About two CTAs per SM in all,
 // none shorter than 256 columns: a shorter split costs more in partial results
 // (hd + 2 floats per row) than its keys and values cost to read.
@@ -1440,12 +1531,7 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
     if (e != cudaSuccess) return e;
     pdl = true;
   }
-  const dim3 mg(static_cast<unsigned>(p.rows));
-  if (c.hd == 128)
-    return L.q32 ? launch_k(pdl, k_prefix_merge<128, true>, mg, dim3(128), 0, s, a)
-                 : launch_k(pdl, k_prefix_merge<128, false>, mg, dim3(128), 0, s, a);
-  return L.q32 ? launch_k(pdl, k_prefix_merge<64, true>, mg, dim3(128), 0, s, a)
-               : launch_k(pdl, k_prefix_merge<64, false>, mg, dim3(128), 0, s, a);
+  return c.hd == 128 ? run_merge<128>(L.q32 != nullptr, a, pdl, s) : run_merge<64>(L.q32 != nullptr, a, pdl, s);
 }
 
 }  // namespace fl
@@ -1489,6 +1575,9 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
     if (i < 2 && a->P > 0 && (!stride_ok(a->kp_stride[i], pd[i], 8) || !stride_ok(a->vp_stride[i], pd[i], 8)))
       return refuse(FL_ERR_INVALID_ARG, "k_prefix and v_prefix strides must be positive multiples of 8");
   }
+  int64_t span = 0;   // the tensor-core kernel holds a query row's place in 32 bits of 16-byte units
+  for (int i = 0; i < 3; ++i) span += qd[i] > 1 ? (qd[i] - 1) * a->q_stride[i] : 0;
+  if (span >= (int64_t(1) << 34)) return refuse(FL_ERR_INVALID_ARG, "q must span less than 2^34 elements");
   const size_t need = prefix_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->P, a->S, false);
   if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
     return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");

@@ -376,7 +376,7 @@ fl_status fl_gemm_skinny_noalloc(const uint16_t* A, const uint16_t* B, float* D,
  * last visible one are never used, whatever they hold.
  *   q, out [B][Tq][H][hd]; k_prefix, v_prefix [Hkv][P][hd]; k, v [B][Hkv][S][hd]
  *   lse fp32 [B][Tq][H] contiguous, or NULL; lens int32 [B]; q_lens int32 [B], or NULL for Tq.
- * Limits: hd 64 or 128, H / Hkv <= 64, 1 <= Tq <= 64, P >= 0, S >= 0 (k_prefix and
+ * Limits: hd 64 or 128, H / Hkv <= 64, 1 <= Tq <= 64, q spans less than 2^34 elements, P >= 0, S >= 0 (k_prefix and
  * v_prefix, or k, v and lens, may be NULL where P, or S, is 0). */
 typedef struct {
   const uint16_t* q;
