@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(128, 1)
 // The prefix on the 5th-generation tensor cores, when the batch has more query
 // rows per KV head than two warp tiles: 256 rows share every K and V tile, so
 // the kernel is bound by the tensor pipe (4 * 256 FLOP per byte) for full row
-// blocks and by HBM for a few.  Two softmax warpgroups, one MMA thread, one TMA
+// blocks and by HBM for a few.  Four softmax warpgroups, one MMA warp, one TMA
 // thread.  A job is one 128-row x 128-key product: S = Q K^T into the job's half
-// of TMEM, softmax on S by its warpgroup (a thread owns a row), P as bf16 over S, O +=
-// P V with P read from TMEM.  Jobs alternate between the two halves, so one half's
+// of TMEM, softmax on S by its two warpgroups (a thread owns 64 columns of a
+// row; the two halves of a row exchange their maxima), P as bf16 over S, O += P V with P
+// read from TMEM.  Jobs alternate between the two halves, so one half's
 // products run under the other's softmax.  With more than 128 rows the halves
 // are two row tiles of the same keys; with fewer they are the same rows over
 // alternate key tiles, joined at the end.
@@ -462,9 +463,10 @@ struct TcSmem {
   static constexpr int kBox = 128 * 128;                 // 128 rows of 64 dims
   static constexpr int kTileBytes = (HD / 64) * kBox;    // 128 rows
   static constexpr int kKSlots = HD == 128 ? 3 : 6, kVSlots = HD == 128 ? 2 : 4;
-  static constexpr int kBytes = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kTiles = (2 + kKSlots + kVSlots) * kTileBytes;
+  static constexpr int kBytes = kTiles + 2048 + 256;     // then the maxima (or row places), barriers and flags
 };
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 576;   // 16 softmax warps, the MMA warp, the TMA warp
 
 template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -472,20 +474,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using C = TcSmem<HD>;
   constexpr int NB = HD / 64, KS = C::kKSlots, VS = C::kVSlots;
   constexpr int OLD = HD + 4;                            // padded row of the join buffer
-  extern __shared__ uint8_t sm_raw[];
-  uint8_t* qsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
+  // no static shared memory: the tiles start at the (1024-byte aligned) start of the block's, which they nearly fill
+  extern __shared__ __align__(1024) uint8_t tc_sm[];
+  uint8_t* qsm = tc_sm;
   uint8_t* ksm = qsm + 2 * C::kTileBytes;
   uint8_t* vsm = ksm + KS * C::kTileBytes;
-  __shared__ __align__(8) uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_ready[2], o_done[2];
-  __shared__ uint32_t tmem_slot;
-  __shared__ uint32_t row_off[kTcRows];   // a query row's place in q, in 16-byte units (~0: no row)
+  float* max_sm = reinterpret_cast<float*>(tc_sm + C::kTiles);          // [half][column half][row]; then the sums
+  uint32_t* row_off = reinterpret_cast<uint32_t*>(max_sm);               // while no maxima are there: a query row's
+                                                                         // place in q, in 16-byte units (~0: no row)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tc_sm + C::kTiles + 2048);
+  uint64_t *k_full = bars, *k_empty = k_full + KS, *v_full = k_empty + KS, *v_empty = v_full + VS, *s_full = v_empty + VS,
+           *p_ready = s_full + 2, *o_done = p_ready + 2;
+  static_assert((2 * KS + 2 * VS + 6) * 8 + 16 <= 256, "barriers");
+  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(tc_sm + C::kTiles + 2048 + 240);
+  int& total_sm = *reinterpret_cast<int*>(tc_sm + C::kTiles + 2048 + 244);
+  volatile int& bad = *reinterpret_cast<volatile int*>(tc_sm + C::kTiles + 2048 + 248);
   int* slot_sm = reinterpret_cast<int*>(qsm);            // while the query tiles are not there yet
   float2* join_ml = reinterpret_cast<float2*>(ksm + 128 * OLD * 4);
-  __shared__ int total_sm;
-  __shared__ volatile int bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
-  if (tid == 9 * 32) {
+  if (tid == 17 * 32) {
     tma_prefetch_desc(&kp);
     tma_prefetch_desc(&vp);
   }
@@ -500,13 +508,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_ready[i]), 128);
+      mbar_init(smem_u32(&p_ready[i]), 256);
       mbar_init(smem_u32(&o_done[i]), 1);
     }
     fence_mbar_init();
     bad = 0;
   }
-  if (warp == 8) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
@@ -557,7 +565,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- the segment's queries (every thread); the K and V rings fill meanwhile
     int k_at = 0, v_at = 0;                    // next tile to load (TMA thread): K_0 K_1 V_0 K_2 V_1 ...
     bool stop = false;
-    if (tid == 9 * 32) {
+    if (tid == 17 * 32) {
       // the first tiles of a segment: their slots' last readers finished with the previous segment
       while (k_at < nt && k_at < KS) {
         stop = nk >= KS && !mbar_wait(smem_u32(&k_empty[nk % KS]), ((nk / KS) - 1) & 1, nullptr);
@@ -570,22 +578,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         load_v(v_at++);
       }
     }
-    // (warps 0-8: the TMA warp is not waited for, nor does it read the queries)
+    // (warps 0-16: the TMA warp is not waited for, nor does it read the queries)
     if (warp == 0) {
       const int first = r0 / a.G, count = (r0 + rows - 1) / a.G - first + 1;
       pack_queries(a, first, count, slot_sm);
     }
-    if (warp < 8) {
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      const int r = r0 + tid, sl = tid < rows ? slot_sm[r / a.G - r0 / a.G] : 0;
-      const long long off = (sl / a.Tq) * a.q_sb + (sl % a.Tq) * a.q_st + (g * a.G + r % a.G) * a.q_sh;
-      row_off[tid] = tid < rows ? static_cast<uint32_t>(off >> 3) : ~0u;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      constexpr int CH = HD / 8;                 // chunks of a row: thread t copies chunk t % CH of every (256 / CH)-th row
+    if (warp < 16) {
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (tid < kTcRows) {
+        const int r = r0 + tid, sl = tid < rows ? slot_sm[r / a.G - r0 / a.G] : 0;
+        const long long off = (sl / a.Tq) * a.q_sb + (sl % a.Tq) * a.q_st + (g * a.G + r % a.G) * a.q_sh;
+        row_off[tid] = tid < rows ? static_cast<uint32_t>(off >> 3) : ~0u;
+      }
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      constexpr int CH = HD / 8, RP = 512 / CH;    // chunks of a row: thread t copies chunk t % CH of every RP-th row
       const int c = tid % CH;
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int qr = tid / CH + i * (256 / CH);
+      for (int i = 0; i < 256 / RP; ++i) {
+        const int qr = tid / CH + i * RP;
         if (qr < 128 || two) {
           const uint32_t off16 = row_off[qr];
           cp_async_16(smem_u32(qsm + (qr >> 7) * C::kTileBytes + sw_off(128, qr & 127, c)),
@@ -594,20 +604,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       cp_async_wait_all();
       if (flip)
-        for (int i = 0; i < CH; ++i) {           // the chunks this thread copied
-          const int qr = tid / CH + i * (256 / CH);
+        for (int i = 0; i < 256 / RP; ++i) {       // the chunks this thread copied
+          const int qr = tid / CH + i * RP;
           uint4* x = reinterpret_cast<uint4*>(qsm + (qr >> 7) * C::kTileBytes + sw_off(128, qr & 127, c));
           if (qr < 128 || two) *x = make_uint4(x->x ^ flip, x->y ^ flip, x->z ^ flip, x->w ^ flip);
         }
       fence_proxy_async();
     }
-    if (warp < 9) asm volatile("bar.sync 2, 288;" ::: "memory");   // the MMA warp too
+    if (warp < 17) asm volatile("bar.sync 2, 544;" ::: "memory");   // the MMA warp too
 
-    if (warp < 8) {
-      // ================= softmax warpgroup of one half =================
-      const int q = warp >> 2, row = (warp & 3) * 32 + lane;
+    if (warp < 16) {
+      // ================= two softmax warpgroups of one half =================
+      const int q = warp >> 3, sub = (warp >> 2) & 1, row = (warp & 3) * 32 + lane;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + q * 128, to = tmem + lanes + 256 + q * HD;
+      const uint32_t ts = tmem + lanes + q * 128, to = tmem + lanes + 256 + q * HD + sub * (HD / 2);
+      float* my_max = max_sm + (q * 2 + sub) * 128 + row;
+      const float* other_max = max_sm + (q * 2 + (sub ^ 1)) * 128 + row;
+      auto half_sync = [&]() {                 // the half's 256 threads
+        if (q == 0) asm volatile("bar.sync 3, 256;" ::: "memory");
+        else asm volatile("bar.sync 4, 256;" ::: "memory");
+      };
       const int mine = (jobs + 1 - q) / 2;     // this half's jobs
       float m = -INFINITY, l = 0.f;
       bool ok = true;
@@ -615,54 +631,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, nullptr)) != 0;
       };
       for (int j = 0; j < mine; ++j, ++ns[0]) {
-        if (!wait(&s_full[q], ns[0])) {
-          ok = false;
-          break;
-        }
+        // (after a wait that ran out the loop goes on without waiting, so that the barriers still meet)
+        ok = ok && wait(&s_full[q], ns[0]);
         tc_fence_after();
-        // S is read twice, 32 columns at a time, once for the maximum and once for the
-        // probabilities: all 128 in registers would spill.  P (bf16) goes over the columns
-        // already read: those of chunk c to columns 16 c .. 16 c + 15.
-        const int ncol = a.P - (t0 + (two ? j : 2 * j + q)) * kTcTile;   // valid columns of this tile
-        uint32_t buf[2][32];
+        const uint32_t tj = ts + sub * 64;               // these 64 columns of S; P goes over their first 32
+        const int ncol = a.P - (t0 + (two ? j : 2 * j + q)) * kTcTile - sub * 64;   // valid ones of them
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld32(ts, buf[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        auto load = [&](int c) {
+          tmem_ld32(tj + c * 32, r);
           tc_wait_ld();
-          tmem_ld32(ts + ((c + 1) & 3) * 32, buf[(c + 1) & 1]);   // (after the last: the first again)
-          const uint32_t* r = buf[c & 1];
-          if (ncol >= kTcTile) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-          } else {
+          if (ncol < 64) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              mx[e & 3] = fmaxf(mx[e & 3], c * 32 + e < ncol ? __uint_as_float(r[e]) : -INFINITY);
+              if (c * 32 + e >= ncol) r[e] = 0xFF800000u;   // -inf
           }
+        };
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {                    // (columns 32-63 stay in registers)
+          load(c);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = fmax3(mx[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
         }
-        const float mrow = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        *my_max = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+        half_sync();
+        const float mrow = fmax3(*my_max, *other_max, *other_max);
         const float mn = mrow == -INFINITY ? -INFINITY : mrow * scale2;
         const bool grow = mn > m + 8.f || (m == -INFINITY && mn > m);
         if (__any_sync(0xffffffffu, grow)) {
           const float m_new = grow ? mn : m;
           if (j > 0) {
+            // this warpgroup's half of the row's output so far
             const float al = m == m_new ? 1.f : ex2_approx(m - m_new);
-            if (!wait(&o_done[q], ns[0] - 1)) {
-              ok = false;
-              break;
-            }
+            ok = ok && wait(&o_done[q], ns[0] - 1);
             tc_fence_after();
             l *= al;
+            if (ok) {
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 16) {
-              float o[16];
-              tmem_ld16(to + c, o);
-              tc_wait_ld();
+              for (int c = 0; c < HD / 2; c += 16) {
+                float o[16];
+                tmem_ld16(to + c, o);
+                tc_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] *= al;
-              tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
+                for (int e = 0; e < 16; ++e) o[e] *= al;
+                tmem_st16(to + c, reinterpret_cast<const uint32_t*>(o));
+              }
             }
           }
           m = m_new;
@@ -670,27 +684,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float ms = m == -INFINITY ? 0.f : m;
         const uint64_t sc2 = f2_pack(scale2, scale2), ms2 = f2_pack(-ms, -ms);
         uint64_t sum2[2] = {0, 0};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tc_wait_ld();
-          if (c < 3) tmem_ld32(ts + (c + 1) * 32, buf[(c + 1) & 1]);
-          const uint32_t* r = buf[c & 1];
-          uint32_t pk[16];
+        auto probs = [&](uint32_t* pk) {   // (a column out of range: score -inf, probability 0)
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
+            const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, ms2);
             float p0, p1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, ms2), p0, p1);
+            f2_unpack(y2, p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
-            if (ncol < kTcTile) {
-              if (c * 32 + e >= ncol) p0 = 0.f;
-              if (c * 32 + e + 1 >= ncol) p1 = 0.f;
-            }
             sum2[(e >> 1) & 1] = f2_add(sum2[(e >> 1) & 1], f2_pack(p0, p1));
             pk[e >> 1] = pack2(p0, p1);
           }
-          tmem_st16(ts + c * 16, pk);
-        }
+        };
+        uint32_t pk[16];
+        probs(pk);
+        load(0);                               // before P of columns 32-63 goes over its second half
+        tmem_st16(tj + 16, pk);
+        probs(pk);
+        tmem_st16(tj, pk);
         {
           float x, y;
           f2_unpack(f2_add(sum2[0], sum2[1]), x, y);
@@ -698,26 +709,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&p_ready[q]));
+        if (ok) mbar_arrive(smem_u32(&p_ready[q]));
       }
-      if (ok && mine > 0 && !wait(&o_done[q], ns[0] - 1)) ok = false;
+      if (mine > 0) ok = ok && wait(&o_done[q], ns[0] - 1);
       if (!ok) bad = 1;
       tc_fence_after();
-      // ---- this segment's part of the rows: (max, sum) and the unnormalised output, a row at a
+      // ---- this segment's part of the rows: (max, sum) and the unnormalised output, half a row at a
       // time by bulk copies from shared memory (the rings are idle: every product is done)
       const int at_row = (two ? q * 128 : 0) + row;
       const bool have = at_row < rows;
       const long long at = (blockIdx.x + pair) * static_cast<long long>(kTcRows) + at_row;
-      float* so = reinterpret_cast<float*>(ksm) + at_row * OLD;
-      asm volatile("bar.sync 1, 256;" ::: "memory");   // both softmax warpgroups
+      float* so = reinterpret_cast<float*>(ksm) + at_row * OLD + sub * (HD / 2);
+      *my_max = l;                                     // (every maximum has been read)
+      asm volatile("bar.sync 1, 512;" ::: "memory");   // every softmax warp
+      l += *other_max;                                 // the whole row's sum
       float w0 = 1.f, w1 = 0.f, M = m, L = l;
       if (!two) {
         // the halves are the same rows over alternate tiles: the second leaves its sums and output, the first joins
         if (q == 1) {
-          join_ml[row] = make_float2(mine > 0 ? m : -INFINITY, l);
+          if (sub == 0) join_ml[row] = make_float2(mine > 0 ? m : -INFINITY, l);
           if (mine > 0 && ok) {
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 16) {
+            for (int c = 0; c < HD / 2; c += 16) {
               float o[16];
               tmem_ld16(to + c, o);
               tc_wait_ld();
@@ -726,7 +739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 512;" ::: "memory");
         if (q == 0) {
           const float2 x = join_ml[row];
           M = fmaxf(m, x.x);
@@ -738,13 +751,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (two || q == 0) {
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 64) {
-          uint32_t o[64];
+        for (int c = 0; c < HD / 2; c += 32) {
+          uint32_t o[32];
           tmem_ld32(to + c, o);
-          tmem_ld32(to + c + 32, o + 32);
           tc_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
+          for (int e = 0; e < 32; e += 4) {
             float4 x = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]), __uint_as_float(o[e + 2]),
                                    __uint_as_float(o[e + 3]));
             if (!two && jobs > 1) {
@@ -755,9 +767,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         if (have) {
-          a.tc_ml[at] = bad ? make_float2(0.f, NAN) : make_float2(M, L);
+          if (sub == 0) a.tc_ml[at] = bad ? make_float2(0.f, NAN) : make_float2(M, L);
           fence_proxy_async();
-          bulk_store(a.tc_o + at * HD, smem_u32(so), HD * 4);
+          bulk_store(a.tc_o + at * HD + sub * (HD / 2), smem_u32(so), HD * 2);
           bulk_commit();
           bulk_wait_read();
         }
@@ -765,7 +777,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       fence_proxy_async();   // the join buffer becomes a ring again
       tc_fence_before();
-    } else if (warp == 8) {
+    } else if (warp == 16) {
       // ================= MMA warp =================
       // The whole warp runs the loop and one elected lane issues: the operands are
       // then warp-uniform, as the instruction wants them.
@@ -806,7 +818,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTcTile / 16; ++k)
-            tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + k * 8, db + k * (2048 >> 4), id_o, j > 0 || k > 0);
+            tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * (2048 >> 4), id_o, j > 0 || k > 0);
           tc_commit(smem_u32(&o_done[q]));
           if (!two || q == 1) tc_commit(smem_u32(&v_empty[st]));
         }
@@ -818,7 +830,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ns[0] += (jobs + 1) / 2;
       ns[1] += jobs / 2;
       if (!ok) bad = 1;
-    } else if (tid == 9 * 32) {
+    } else if (tid == 17 * 32) {
       // ================= TMA thread =================
       if (stop) bad = 1;
       while ((k_at < nt || v_at < nt) && !bad) {
@@ -853,7 +865,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   bulk_wait();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1372,11 +1384,11 @@ struct PrefixPlan {
   size_t off_ml, off_tc_o, off_tc_ml, bytes;
 };
 constexpr int kTcMinRows = 33;   // query rows per KV head (two warp tiles hold 32)
-PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool fp32_queries) {
+PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool warp_tiles) {
   PrefixPlan p{};
   const int G = H / Hkv;
   const long long rows_p = static_cast<long long>(B) * Tq * G, rows_s = static_cast<long long>(Tq) * G;
-  if (!fp32_queries && P >= kTcTile && rows_p >= kTcMinRows) {
+  if (!warp_tiles && P >= kTcTile && rows_p >= kTcMinRows) {
     const long long pairs = static_cast<long long>(Hkv) * ceil_div_i(rows_p, kTcRows);
     p.tc_ctas = static_cast<int>(std::min<long long>(kNumSM, std::max(1LL, pairs * ceil_div_i(P, kTcTile) / kTcMinTiles)));
     p.tc_parts = static_cast<size_t>(p.tc_ctas + pairs);
@@ -1463,8 +1475,8 @@ cudaError_t serving_init_attrs() {
   set(k_prefix_split<128, 1, true>, split_smem(128, 1, true));
   set(k_prefix_split<128, 2, false>, split_smem(128, 2, false));
   set(k_prefix_split<128, 2, true>, split_smem(128, 2, true));
-  set(k_prefix_tc<64>, 1024 + TcSmem<64>::kBytes);
-  set(k_prefix_tc<128>, 1024 + TcSmem<128>::kBytes);
+  set(k_prefix_tc<64>, TcSmem<64>::kBytes);
+  set(k_prefix_tc<128>, TcSmem<128>::kBytes);
   set(k_weights_stream<64, 1>, stream_smem(64));
   set(k_weights_stream<64, 2>, stream_smem(64));
   set(k_weights_stream<128, 1>, stream_smem(128));
@@ -1476,15 +1488,18 @@ cudaError_t serving_init_attrs() {
 }
 
 size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool fp32_queries) {
-  return plan_prefix(B, Tq, H, Hkv, hd, P, S, fp32_queries).bytes;
+  // either of the prefix's kernels (the scale, known at the call, has a say)
+  const size_t warp = plan_prefix(B, Tq, H, Hkv, hd, P, S, true).bytes;
+  return fp32_queries ? warp : std::max(warp, plan_prefix(B, Tq, H, Hkv, hd, P, S, false).bytes);
 }
 
 cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) {
   const flashloop_prefix_args& c = L.a;
   cudaError_t e = serving_init_attrs();
   if (e != cudaSuccess) return e;
-  const PrefixPlan p = plan_prefix(c.B, c.Tq, c.H, c.Hkv, c.hd, c.P, c.S, L.q32 != nullptr);
   PrefixArgs a{};
+  a.scale2 = c.scale * kLog2e;   // 0: k_prefix_tc masks by scores of -inf, which 0 would turn to NaN
+  const PrefixPlan p = plan_prefix(c.B, c.Tq, c.H, c.Hkv, c.hd, c.P, c.S, L.q32 != nullptr || a.scale2 == 0.f);
   a.q = c.q; a.q32 = L.q32; a.q_sb = c.q_stride[0]; a.q_st = c.q_stride[1]; a.q_sh = c.q_stride[2];
   a.out = c.out; a.o_sb = c.out_stride[0]; a.o_st = c.out_stride[1]; a.o_sh = c.out_stride[2];
   a.out32 = L.out32; a.lse = c.lse; a.k = c.k; a.v = c.v;
@@ -1492,7 +1507,6 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
   a.v_sb = c.v_stride[0]; a.v_sg = c.v_stride[1]; a.v_sr = c.v_stride[2];
   a.lens = c.lens; a.q_lens = c.q_lens; a.lens_add = L.lens_add;
   a.B = c.B; a.Tq = c.Tq; a.H = c.H; a.Hkv = c.Hkv; a.G = c.H / c.Hkv; a.P = c.P; a.S = c.S;
-  a.scale2 = c.scale * kLog2e;
   a.rb_p = p.rb_p; a.n_p = p.n_p; a.rb_s = p.rb_s; a.n_s = p.n_s;
   a.items_p = p.rb_p * p.n_p * c.Hkv;
   a.rows = static_cast<long long>(p.rows);
@@ -1519,7 +1533,7 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
   const long long grid = a.items_p + static_cast<long long>(p.rb_s) * p.n_s * c.Hkv * c.B;
   bool pdl = L.pdl;
   if (p.tc_ctas) {
-    const int smem = 1024 + (c.hd == 128 ? TcSmem<128>::kBytes : TcSmem<64>::kBytes);
+    const int smem = c.hd == 128 ? TcSmem<128>::kBytes : TcSmem<64>::kBytes;
     e = c.hd == 128 ? launch_k(pdl, k_prefix_tc<128>, dim3(p.tc_ctas), dim3(kTcThreads), smem, s, m[0], m[1], a)
                     : launch_k(pdl, k_prefix_tc<64>, dim3(p.tc_ctas), dim3(kTcThreads), smem, s, m[0], m[1], a);
     if (e != cudaSuccess) return e;
