@@ -19,7 +19,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPxTile = 32;                       // keys of one warp's tile
 constexpr int kPxWarps = 4;
-constexpr int kPxRing = kPxWarps * 48 * 1024;     // bytes of the four warps' tile rings
+constexpr int kPxRing = kPxWarps * 24 * 1024;     // bytes of the four warps' tile rings (two CTAs per SM)
 constexpr int kMaxGroup = 64;                     // query heads per KV head
 constexpr int kMaxTq = 64;
 
@@ -146,14 +146,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // bf16 hi + lo pairs (about 16 significant bits).
 // ============================================================================
 template <int HD, int NM, bool HILO>
-__global__ void __launch_bounds__(128, 1)
+__global__ void __launch_bounds__(128, 2)
     k_prefix_split(const __grid_constant__ CUtensorMap kp, const __grid_constant__ CUtensorMap vp,
                    const __grid_constant__ CUtensorMap ks, const __grid_constant__ CUtensorMap vs, const PrefixArgs a) {
   constexpr int RB = 16 * NM;                       // query rows
   constexpr int NB = HD / 64;                       // 128-byte boxes per row
   constexpr int TILE_BYTES = kPxTile * HD * 2;      // K or V of one tile
-  constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-  constexpr int STAGES = kPxRing / kPxWarps / STAGE_BYTES;
+  constexpr int SLOTS = kPxRing / kPxWarps / TILE_BYTES;   // a warp's ring: K_0 V_0 K_1 V_1 .., a slot each
   constexpr int QBYTES = RB * HD * 2;
   constexpr int NT = HD / 8;                        // 8-dim output tiles
   constexpr int OLD = HD + 8;                       // padded row of the merge buffer
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(128, 1)
   __shared__ long long row_id[RB];
   __shared__ float sm_m[kPxWarps][RB], sm_l[kPxWarps][RB];
   __shared__ int n_valid_sm, bad_sm;
-  static_assert(STAGES <= 12, "barriers");
+  static_assert(SLOTS <= 12, "barriers");
 
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -223,18 +222,26 @@ __global__ void __launch_bounds__(128, 1)
   const CUtensorMap* km = pre ? &kp : &ks;
   const CUtensorMap* vm = pre ? &vp : &vs;
   uint8_t* wring = ring + warp * (kPxRing / kPxWarps);
-  auto issue = [&](int u) {
-    const int y = (tb + warp + u * kPxWarps) * kPxTile;
-    const uint32_t st = smem_u32(wring + (u % STAGES) * STAGE_BYTES), fb = smem_u32(&full[warp][u % STAGES]);
-    mbar_arrive_expect_tx(fb, STAGE_BYTES);
+  auto issue = [&](int n) {   // load n: K (even) or V (odd) of this warp's tile n / 2
+    const int y = (tb + warp + (n >> 1) * kPxWarps) * kPxTile;
+    const uint32_t st = smem_u32(wring + (n % SLOTS) * TILE_BYTES), fb = smem_u32(&full[warp][n % SLOTS]);
+    const CUtensorMap* map = (n & 1) ? vm : km;
+    mbar_arrive_expect_tx(fb, TILE_BYTES);
 #pragma unroll
-    for (int bx = 0; bx < NB; ++bx) {
-      tma_load_4d(st + bx * kPxTile * 128, km, fb, bx * 64, y, g, pre ? 0 : b);
-      tma_load_4d(st + TILE_BYTES + bx * kPxTile * 128, vm, fb, bx * 64, y, g, pre ? 0 : b);
-    }
+    for (int bx = 0; bx < NB; ++bx) tma_load_4d(st + bx * kPxTile * 128, map, fb, bx * 64, y, g, pre ? 0 : b);
   };
+  int issued = 0;             // (lane 0)
   if (lane == 0)
-    for (int u = 0; u < STAGES && u < mine; ++u) issue(u);
+    for (; issued < SLOTS && issued < 2 * mine; ++issued) issue(issued);
+  // whole warp: load n has arrived, or (false) its wait ran out
+  auto arrived = [&](int n) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr)) != 0;
+  };
+  // whole warp: a slot has been read; the next load takes it
+  auto refill = [&]() {
+    __syncwarp();
+    if (lane == 0 && issued < 2 * mine) issue(issued++);
+  };
 
   // ---- queries to shared memory (rows past the last: zero)
   for (int e = tid; e < RB * (HD / 8); e += 128) {
@@ -275,18 +282,9 @@ __global__ void __launch_bounds__(128, 1)
   const uint32_t qs = smem_u32(qsm);
   int done = 0;
   for (; done < mine; ++done) {
-    const int st = done % STAGES;
-    if (!mbar_wait(smem_u32(&full[warp][st]), (done / STAGES) & 1, nullptr)) break;
-    const uint32_t Kt = smem_u32(wring + st * STAGE_BYTES), Vt = Kt + TILE_BYTES;
+    if (!arrived(2 * done)) break;
+    const uint32_t Kt = smem_u32(wring + (2 * done) % SLOTS * TILE_BYTES);
     const int nc = min(kPxTile, ncols - (tb + warp + done * kPxWarps) * kPxTile);   // columns of this tile in range
-    if (nc < kPxTile) {
-      // rows past the range (another query's tokens, or never written): their
-      // probabilities are 0, and 0 times what they hold must stay 0
-      for (int e = lane; e < (kPxTile - nc) * (HD / 8); e += 32)
-        *reinterpret_cast<uint4*>(wring + st * STAGE_BYTES + TILE_BYTES +
-                                  sw_off(kPxTile, nc + e / (HD / 8), e % (HD / 8))) = make_uint4(0, 0, 0, 0);
-      __syncwarp();
-    }
     // ---- scores of the tile's 32 keys
     float s[NM][4][4] = {};
 #pragma unroll
@@ -309,6 +307,7 @@ __global__ void __launch_bounds__(128, 1)
         }
       }
     }
+    refill();
     // ---- running softmax: thread holds rows lane/4 (+8), columns 8n + 2(lane%4) + {0, 1}
     uint32_t pf[NM][2][4], pl[HILO ? NM : 1][2][4];
 #pragma unroll
@@ -360,6 +359,16 @@ __global__ void __launch_bounds__(128, 1)
         }
     }
     // ---- output += P V
+    if (!arrived(2 * done + 1)) break;
+    uint8_t* vt = wring + (2 * done + 1) % SLOTS * TILE_BYTES;
+    const uint32_t Vt = smem_u32(vt);
+    if (nc < kPxTile) {
+      // rows past the range (another query's tokens, or never written): their
+      // probabilities are 0, and 0 times what they hold must stay 0
+      for (int e = lane; e < (kPxTile - nc) * (HD / 8); e += 32)
+        *reinterpret_cast<uint4*>(vt + sw_off(kPxTile, nc + e / (HD / 8), e % (HD / 8))) = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
@@ -377,16 +386,12 @@ __global__ void __launch_bounds__(128, 1)
         }
       }
     }
-    __syncwarp();   // the slot is free again
-    if (lane == 0 && done + STAGES < mine) issue(done + STAGES);
+    refill();
   }
-  if (done < mine) {
+  if (done < mine && lane == 0) {
     // a tile never arrived: let the copies in flight land (bounded); the result becomes NaN
-    if (lane == 0) {
-      bad_sm = 1;
-      for (int u = done; u < mine && u < done + STAGES; ++u)
-        mbar_wait(smem_u32(&full[warp][u % STAGES]), (u / STAGES) & 1, nullptr);
-    }
+    bad_sm = 1;
+    for (int n = max(0, issued - SLOTS); n < issued; ++n) mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr);
   }
   // ---- the four warps' parts become one
 #pragma unroll
@@ -519,6 +524,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
+  pdl_trigger();   // (the next launch may run beside this one; see its wait)
   if (warp == 0) {
     const int total = pack_queries(a, 0, 0, slot_sm);
     if (lane == 0) total_sm = total;
@@ -526,7 +532,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_trigger();
   const uint32_t tmem = tmem_slot;
   const int queries = total_sm, nrows = queries * a.G;
   // a negative scale: negated queries and its magnitude, so that the largest score is the largest product
@@ -1400,7 +1405,7 @@ PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool
   p.rb_s = ceil_div_i(rows_s, RB);
   const double cols = static_cast<double>(p.rb_p) * Hkv * P + static_cast<double>(p.rb_s) * Hkv * B * S;
   const double per = std::max(256.0, cols / (2.0 * kNumSM));
-  auto splits = [&](int n) { return n ? std::min(64, std::max(1, static_cast<int>(std::ceil(n / per)))) : 0; };
+  auto splits = [&](int n) { return n ? std::min(64, std::max(1, static_cast<int>(n / per + 0.5))) : 0; };
   p.n_p = splits(P);
   p.n_s = splits(S);
   p.rows = static_cast<size_t>(B) * Tq * H;
