@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                                                          // place in q, in 16-byte units (~0: no row)
   uint64_t* bars = reinterpret_cast<uint64_t*>(tc_sm + C::kTiles + 2048);
   uint64_t *k_full = bars, *k_empty = k_full + KS, *v_full = k_empty + KS, *v_empty = v_full + VS, *s_full = v_empty + VS,
-           *p_ready = s_full + 2, *o_done = p_ready + 2;
-  static_assert((2 * KS + 2 * VS + 6) * 8 + 16 <= 256, "barriers");
+           *p_ready = s_full + 2, *p_first = p_ready + 2, *o_done = p_first + 2;
+  static_assert((2 * KS + 2 * VS + 8) * 8 + 16 <= 256, "barriers");
   uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(tc_sm + C::kTiles + 2048 + 240);
   int& total_sm = *reinterpret_cast<int*>(tc_sm + C::kTiles + 2048 + 244);
   volatile int& bad = *reinterpret_cast<volatile int*>(tc_sm + C::kTiles + 2048 + 248);
@@ -514,6 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&p_ready[i]), 256);
+      mbar_init(smem_u32(&p_first[i]), 256);
       mbar_init(smem_u32(&o_done[i]), 1);
     }
     fence_mbar_init();
@@ -705,6 +706,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         probs(pk);
         load(0);                               // before P of columns 32-63 goes over its second half
         tmem_st16(tj + 16, pk);
+        tc_wait_st();
+        tc_fence_before();
+        if (ok) mbar_arrive(smem_u32(&p_first[q]));      // half of P: its products can start
         probs(pk);
         tmem_st16(tj, pk);
         {
@@ -814,16 +818,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int n = 0; n < 2 && n < jobs; ++n) ok = ok && do_qk(n);
       for (int n = 0; ok && n < jobs; ++n) {
         const int q = n & 1, i = tile_of(n), vt = v0 + i, st = vt % VS, j = n >> 1;
-        if (!wait(&p_ready[q], (q ? s1 : s0) + j) || !wait(&v_full[st], vt / VS)) {
+        const uint64_t db = v_desc + st * (C::kTileBytes >> 4);
+        // O += P V for the keys of one half of P: columns 32-63 (first) or 0-31 of each 64
+        auto half_pv = [&](bool first) {
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int kk = (k >> 1) * 4 + (first ? 2 : 0) + (k & 1);   // 16 keys
+              tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + (kk >> 2) * 64 + (kk & 3) * 8, db + kk * (2048 >> 4), id_o,
+                             j > 0 || !first || k > 0);
+            }
+          }
+          __syncwarp();
+        };
+        if (!wait(&p_first[q], (q ? s1 : s0) + j) || !wait(&v_full[st], vt / VS)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint64_t db = v_desc + st * (C::kTileBytes >> 4);
+        half_pv(true);
+        if (!wait(&p_ready[q], (q ? s1 : s0) + j)) {
+          ok = false;
+          break;
+        }
+        half_pv(false);
         if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTcTile / 16; ++k)
-            tc_mma_bf16_ts(tmem + 256 + q * HD, tmem + q * 128 + (k >> 2) * 64 + (k & 3) * 8, db + k * (2048 >> 4), id_o, j > 0 || k > 0);
           tc_commit(smem_u32(&o_done[q]));
           if (!two || q == 1) tc_commit(smem_u32(&v_empty[st]));
         }
