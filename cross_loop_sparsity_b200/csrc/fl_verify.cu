@@ -21,7 +21,7 @@ constexpr int kVfThreads = 256;
 constexpr int kVfChunk = 32 * kVfThreads - 4;   // logits per CTA of the first launch: 32 per thread, 4 spare for alignment
 constexpr int kMaxDraft = 64;
 
-struct RowPart {   // one chunk of one row
+struct alignas(16) RowPart {   // one chunk of one row
   float m, s;      // maximum, sum of 2^((x - m) c)
   int at, pad;     // lowest index of the maximum
 };
@@ -33,6 +33,8 @@ struct VerifyArgs {
   struct Deciding* deciding;   // [B]
   struct Sums* sums;           // [B][n_sub] of the deciding row's token ranges
   int n_sub, sub_len;
+  unsigned* tickets;           // [B][D] finished chunks of a draft's rows, minus one (EARLY)
+  unsigned* dead;              // [B] the first position known to be rejected
 };
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
 constexpr int kSumMaxCtas = kSumThreads / kSumWarps;   // CTAs of one sequence: n_sub <= kSumThreads
@@ -46,19 +48,114 @@ __device__ __forceinline__ const float* row_of(const VerifyArgs& a, int b, int r
                   : c.draft_logits + b * c.draft_logits_stride[0] + (r - c.D - 1) * c.draft_logits_stride[1];
 }
 
+// exp((x - m) / temperature) in 64 bits, to 4e-14: with z = 64 log2(e) (x - m) / temperature = k + r, k = rint(z),
+// it is 2^(k / 64) e^(r ln 2 / 64); table[i] = 2^(i / 64), and the second factor's series to
+// its fourth power, |r ln 2 / 64| <= 0.0055 (the next term is below 4e-14).  scale64 and
+// offset give z = scale64 x + offset, x a 32-bit value with z in [-65000, 0.5].
+constexpr int kExpTable = 64;
+__device__ __forceinline__ double exp64(float x, double scale64, double offset, const double* table) {
+  const double z = fma(static_cast<double>(x), scale64, offset);
+  const double t = z + 6755399441055744.0;                  // + 1.5 * 2^52: k in the low word
+  const int k = __double2loint(t);
+  const double r = z - (t - 6755399441055744.0);
+  constexpr double h = 0.693147180559945309417 / kExpTable;
+  constexpr double c1 = h, c2 = h * h / 2, c3 = c2 * h / 3, c4 = c3 * h / 4;
+  const double p = fma(fma(fma(fma(c4, r, c3), r, c2), r, c1), r, 1.0);
+  const double f = table[k & (kExpTable - 1)];
+  return p * __hiloint2double(__double2hiint(f) + ((k >> 6) << 20), __double2loint(f));
+}
+
+// The same, 0 for x below lo.
+__device__ __forceinline__ double exp64_from(float x, float lo, double scale64, double offset, const double* table) {
+  const double e = exp64(fmaxf(x, lo), scale64, offset, table);
+  return x >= lo ? e : 0.0;
+}
+
+// The deciding row of a sequence, from 32-bit sums: target row `row`, draft row
+// `row` when with_draft, their maxima, ratio = the draft's total over the target's.
+struct Deciding {
+  int row;          // drafts accepted in front of it
+  int near;         // whether draft `row` is rejected is too near to say from 32-bit sums
+  int with_draft;   // the weights are max(p - q, 0)
+  int x_out;        // a token left out (the rejected one of a draft without probabilities), or -1
+  int fine;         // both rows have finite, positive totals
+  float lo_p, lo_q; // logits below these (2^-1000 of the maximum, -inf among them) count as nothing
+  double op, oq;    // exp64's offsets: -64 log2(e) m / temperature
+  double ratio;
+};
+
+// Sum and maximum of a row from the first launch (one warp).
+__device__ __forceinline__ void row_norm(const VerifyArgs& a, int b, int r, float& m, double& z) {
+  const int lane = threadIdx.x & 31;
+  const RowPart* part = a.part + (static_cast<size_t>(b) * (2 * a.c.D + 1) + r) * a.n_chunks;
+  m = -INFINITY;
+  z = 0.0;
+  for (int k0 = 0; k0 < a.n_chunks; k0 += 32) {
+    RowPart p{-INFINITY, 0.f, 0, 0};
+    if (k0 + lane < a.n_chunks) {   // (through L2: another SM may have written it in this launch)
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(&part[k0 + lane]));
+      p.m = f.x;
+      p.s = f.y;
+    }
+    const float mn = fmaxf(m, warp_max(p.m));
+    if (mn > m) z *= static_cast<double>(exp2f(static_cast<float>((m - mn) * a.scale2)));
+    z += p.m == -INFINITY ? p.s : p.s * exp2f(static_cast<float>((p.m - mn) * a.scale2));   // (no finite logit: 0, or NaN)
+    m = mn;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+}
+
+// Sums and maxima of the rows looked at, from the first launch: target rows and draft rows.
+struct Norms {
+  float mp[kMaxDraft + 1], mq[kMaxDraft + 1];
+  double zp[kMaxDraft + 1], zq[kMaxDraft + 1];
+};
+
+// Verdict on draft i from the 32-bit sums: 0 rejected, 1 accepted, 2 too near to say (closer than 1e-4 of p;
+// the sums and exponentials are good to about 1e-6).  One warp; the rows' norms too.
+__device__ __forceinline__ int judge_one(const VerifyArgs& a, int b, int i, float& mp, double& zp, float& mq, double& zq) {
+  const flashloop_verify_args& c = a.c;
+  const int x = c.draft[static_cast<size_t>(b) * c.D + i];
+  const bool in = x >= 0 && x < c.V;
+  const double xp = in ? row_of(a, b, i)[x] : 0.0;
+  const double xq = in && c.draft_logits ? row_of(a, b, c.D + 1 + i)[x] : 0.0;
+  const double u = c.u[static_cast<size_t>(b) * (c.D + 1) + i];
+  row_norm(a, b, i, mp, zp);
+  mq = 0.f;
+  zq = 1.0;
+  if (c.draft_logits) row_norm(a, b, c.D + 1 + i, mq, zq);
+  const double p = in ? exp2((xp - mp) * a.scale2) / zp : 0.0;
+  const double q = c.draft_logits ? exp2((xq - mq) * a.scale2) / zq : 1.0;
+  return in && fabs(u * q - p) <= 1e-4 * p ? 2 : (in && u * q < p ? 1 : 0);
+}
+
 // ============================================================================
 // One chunk of one row: 32 logits per thread in registers (16-byte loads where the
 // row's alignment allows, whatever V is), then maximum and sum.  HBM-bound.
+// Rows go position by position, each position's rows of all sequences together.
+// EARLY: rows behind a rejected draft decide nothing; the CTA that finishes a
+// draft's two rows (a ticket) judges it, and rows of later positions that have not
+// started by then are not read.  Both for large calls: the tickets need a memset in front.
 // ============================================================================
+template <bool EARLY>
 __global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) {
   __shared__ float red[kVfThreads / 32];
   __shared__ int red_i[kVfThreads / 32];
+  __shared__ int last;
   pdl_trigger();
   const flashloop_verify_args& c = a.c;
-  const int chunk = blockIdx.x, r = blockIdx.y, b = blockIdx.z;
+  const bool pairs = c.draft_logits != nullptr;
+  const int chunk = blockIdx.x, b = blockIdx.y, i = pairs ? blockIdx.z >> 1 : blockIdx.z;   // position i
+  const int r = pairs && (blockIdx.z & 1) ? c.D + 1 + i : i;
   const int n = drafts_of(a, b);
-  if (r <= c.D ? r > n : r - c.D - 1 >= n) return;   // rows of drafts that were not made
+  if (r <= c.D ? r > n : i >= n) return;   // rows of drafts that were not made
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (EARLY) {
+    if (tid == 0) last = static_cast<unsigned>(i) > __ldcg(&a.dead[b]);
+    __syncthreads();
+    if (last) return;
+  }
   const int lo = chunk * kVfChunk, hi = min(c.V, lo + kVfChunk);
   const float* x = row_of(a, b, r) + lo;
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);   // floats past a 16-byte boundary
@@ -118,87 +215,56 @@ __global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) 
     float t = 0.f;
     for (int w = 0; w < kVfThreads / 32; ++w) t += red[w];
     *out = RowPart{m, t, 0, 0};
+    if (EARLY) {
+      __threadfence();
+      last = i < n && atomicAdd(&a.tickets[static_cast<size_t>(b) * c.D + i], 1u) + 2u == (pairs ? 2u : 1u) * a.n_chunks;
+    }
+  }
+  if (EARLY) {
+    __syncthreads();
+    if (!last || warp != 0) return;
+    __threadfence();
+    float mp, mq;
+    double zp, zq;
+    if (judge_one(a, b, i, mp, zp, mq, zq) == 0 && lane == 0) atomicMin(&a.dead[b], static_cast<unsigned>(i));
   }
 }
 
-// 2^y for y <= 0 to 2e-15: y = k / 32 + r, |r| <= 1/64, and 2^r = sum (r ln 2)^n / n! to n = 5 (the
-// next term is below 2.3e-15); table[i] = 2^(i/32).  0 below 2^-1020; NaN stays NaN.
-__device__ __forceinline__ double exp2_neg(double y, const double* table) {
-  if (!(y > -1020.0)) return y == y ? 0.0 : y;
-  const double t = fma(y, 32.0, 6755399441055744.0);        // + 1.5 * 2^52: k = rint(32 y) in the low word
-  const int k = __double2loint(t);
-  const double r = fma(t - 6755399441055744.0, -0.03125, y);
-  constexpr double kLn2 = 0.693147180559945309417;
-  constexpr double c1 = kLn2, c2 = kLn2 * kLn2 / 2, c3 = c2 * kLn2 / 3, c4 = c3 * kLn2 / 4, c5 = c4 * kLn2 / 5;
-  const double p = fma(fma(fma(fma(fma(c5, r, c4), r, c3), r, c2), r, c1), r, 1.0);
-  const double f = table[k & 31];
-  return p * __hiloint2double(__double2hiint(f) + ((k >> 5) << 20), __double2loint(f));
-}
-
-// The deciding row of a sequence, from 32-bit sums: target row `row`, draft row
-// `row` when with_draft, their maxima, ratio = the draft's total over the target's.
-struct Deciding {
-  int row;          // drafts accepted in front of it
-  int near;         // whether draft `row` is rejected is too near to say from 32-bit sums
-  int with_draft;   // the weights are max(p - q, 0)
-  int x_out;        // a token left out (the rejected one of a draft without probabilities), or -1
-  double mp, mq, ratio;
-};
-
-// Sum and maximum of a row from the first launch (one warp).
-__device__ __forceinline__ void row_norm(const VerifyArgs& a, int b, int r, float& m, double& z) {
-  const int lane = threadIdx.x & 31;
-  const RowPart* part = a.part + (static_cast<size_t>(b) * (2 * a.c.D + 1) + r) * a.n_chunks;
-  m = -INFINITY;
-  z = 0.0;
-  for (int k0 = 0; k0 < a.n_chunks; k0 += 32) {
-    RowPart p{-INFINITY, 0.f, 0, 0};
-    if (k0 + lane < a.n_chunks) p = part[k0 + lane];
-    const float mn = fmaxf(m, warp_max(p.m));
-    if (mn > m) z *= static_cast<double>(exp2f(static_cast<float>((m - mn) * a.scale2)));
-    z += p.m == -INFINITY ? p.s : p.s * exp2f(static_cast<float>((p.m - mn) * a.scale2));   // (no finite logit: 0, or NaN)
-    m = mn;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-}
-
-// Verdicts of drafts [first, n) from the 32-bit sums: 0 rejected, 1 accepted, 2
-// too near to say (closer than 1e-4 of p; the sums and exponentials are good to about 1e-6).  Whole block.
-__device__ void judge(const VerifyArgs& a, int b, int first, int n, int* verdict) {
-  const flashloop_verify_args& c = a.c;
+// Verdicts of drafts [first, n), and the norms of their rows and of target row n.  Whole block.  (Rows behind a sure
+// rejection may not have been summed: what is made of them is not looked at.)
+__device__ void judge(const VerifyArgs& a, int b, int first, int n, int* verdict, Norms* norms) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  for (int i = first + warp; i < n; i += nw) {
-    const int x = c.draft[static_cast<size_t>(b) * c.D + i];
-    const bool in = x >= 0 && x < c.V;
-    const double xp = in ? row_of(a, b, i)[x] : 0.0;
-    const double xq = in && c.draft_logits ? row_of(a, b, c.D + 1 + i)[x] : 0.0;
-    const double u = c.u[static_cast<size_t>(b) * (c.D + 1) + i];
-    float m, mq = 0.f;
-    double z, zq = 1.0;
-    row_norm(a, b, i, m, z);
-    if (c.draft_logits) row_norm(a, b, c.D + 1 + i, mq, zq);
+  for (int i = first + warp; i <= n; i += nw) {
+    float mp, mq = 0.f;
+    double zp, zq = 0.0;
+    int v = 0;
+    if (i < n)
+      v = judge_one(a, b, i, mp, zp, mq, zq);
+    else
+      row_norm(a, b, i, mp, zp);
     if (lane == 0) {
-      const double p = in ? exp2((xp - m) * a.scale2) / z : 0.0;
-      const double q = c.draft_logits ? exp2((xq - mq) * a.scale2) / zq : 1.0;
-      verdict[i] = in && fabs(u * q - p) <= 1e-4 * p ? 2 : (in && u * q < p ? 1 : 0);
+      if (i < n) verdict[i] = v;
+      norms->mp[i] = mp;
+      norms->mq[i] = mq;
+      norms->zp[i] = zp;
+      norms->zq[i] = zq;
     }
   }
   __syncthreads();
 }
 
-// The deciding row when drafts [0, row) are accepted (warp 0 fills *d; then a block barrier).
-__device__ void describe(const VerifyArgs& a, int b, int row, int n, int near, Deciding* d) {
+// The deciding row when drafts [0, row) are accepted (thread 0 fills *d; then a block barrier).
+__device__ void describe(const VerifyArgs& a, int b, int row, int n, const Norms& norms, const int* verdict, Deciding* d) {
   const flashloop_verify_args& c = a.c;
-  if (threadIdx.x < 32) {
+  if (threadIdx.x == 0) {
     const bool residual = row < n, with_draft = residual && c.draft_logits;
-    float mp, mq = 0.f;
-    double zp, zq = 0.0;
-    row_norm(a, b, row, mp, zp);
-    if (with_draft) row_norm(a, b, c.D + 1 + row, mq, zq);
-    if (threadIdx.x == 0)
-      *d = Deciding{row, near, with_draft, residual && !with_draft ? c.draft[static_cast<size_t>(b) * c.D + row] : -1,
-                    mp, mq, zq / zp};
+    const float mp = norms.mp[row], mq = norms.mq[row];
+    const double zp = norms.zp[row], zq = norms.zq[row];
+    const float reach = static_cast<float>(1000.0 / a.scale2);
+    const bool fine = isfinite(zp) && zp > 0.0 && (!with_draft || (isfinite(zq) && zq > 0.0));
+    *d = Deciding{row, residual && verdict[row] == 2, with_draft,
+                  residual && !with_draft ? c.draft[static_cast<size_t>(b) * c.D + row] : -1, fine, mp - reach, mq - reach,
+                  -64.0 * a.scale2 * mp, -64.0 * a.scale2 * mq, zq / zp};
   }
   __syncthreads();
 }
@@ -212,36 +278,46 @@ __device__ void describe(const VerifyArgs& a, int b, int row, int n, int near, D
 struct Sums {
   double p, q, ap, aq;
 };
-__device__ Sums range_sums(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
-  constexpr int U = 8;   // tokens of a lane in flight
+template <bool DRAFT>
+__device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
+  constexpr int U = DRAFT ? 4 : 8;   // tokens of a lane in flight
   const int lane = threadIdx.x & 31;
   const float* xp = row_of(a, b, d.row);
-  const float* xq = d.with_draft ? row_of(a, b, a.c.D + 1 + d.row) : xp;
-  Sums s{0.0, 0.0, 0.0, 0.0};
-  for (int j = j0 + lane; j < j1; j += 32 * U) {
+  const float* xq = DRAFT ? row_of(a, b, a.c.D + 1 + d.row) : nullptr;
+  const double s64 = 64.0 * a.scale2, op = d.op, oq = d.oq, ratio = d.ratio;
+  const float lo_p = d.lo_p, lo_q = d.lo_q;
+  const int x_out = d.x_out;
+  double ap = 0.0, aq = 0.0, np = 0.0, nq = 0.0;   // tokens of positive weight, and the others
+  auto add = [&](float fp, float fq, int j) {
+    const double ep = exp64_from(fp, lo_p, s64, op, table);
+    if (DRAFT) {
+      const double eq = exp64_from(fq, lo_q, s64, oq, table);
+      if (ratio * ep > eq) {
+        ap += ep;
+        aq += eq;
+      } else {
+        np += ep;
+        nq += eq;
+      }
+    } else if (j != x_out) {
+      ap += ep;
+    } else {
+      np += ep;
+    }
+  };
+  int j = j0 + lane;
+  for (; j + 32 * (U - 1) < j1; j += 32 * U) {
     float fp[U], fq[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      fp[u] = j + u * 32 < j1 ? xp[j + u * 32] : -INFINITY;
-      fq[u] = j + u * 32 < j1 && d.with_draft ? xq[j + u * 32] : -INFINITY;
+      fp[u] = xp[j + u * 32];
+      fq[u] = DRAFT ? xq[j + u * 32] : 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (j + u * 32 >= j1) break;
-      const double ep = exp2_neg((fp[u] - d.mp) * a.scale2, table);
-      s.p += ep;
-      if (d.with_draft) {
-        const double eq = exp2_neg((fq[u] - d.mq) * a.scale2, table);
-        s.q += eq;
-        if (d.ratio * ep > eq) {
-          s.ap += ep;
-          s.aq += eq;
-        }
-      } else if (j + u * 32 != d.x_out) {
-        s.ap += ep;
-      }
-    }
+    for (int u = 0; u < U; ++u) add(fp[u], fq[u], j + u * 32);
   }
+  for (; j < j1; j += 32) add(xp[j], DRAFT ? xq[j] : 0.f, j);
+  Sums s{ap + np, aq + nq, ap, aq};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s.p += __shfl_xor_sync(0xffffffffu, s.p, o);
@@ -251,27 +327,32 @@ __device__ Sums range_sums(const VerifyArgs& a, int b, const Deciding& d, int j0
   }
   return s;
 }
+__device__ __forceinline__ Sums range_sums(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
+  if (!d.fine) return Sums{0.0, 0.0, 0.0, 0.0};   // (the token will be -1)
+  return d.with_draft ? range_sums_of<true>(a, b, d, j0, j1, table) : range_sums_of<false>(a, b, d, j0, j1, table);
+}
 
 // ============================================================================
 // Second launch: every CTA finds its sequence's deciding row from the first
 // launch's sums, then each of its warps forms the 64-bit sums of a contiguous
 // range of that row's tokens, two exponentials a token, once.  Bound by the 64-bit pipe
-// (about 13 operations per exponential) for many sequences, by the latency of
+// (about 11 operations per exponential) for many sequences, by the latency of
 // finding the row for few.
 // ============================================================================
 __global__ void __launch_bounds__(kSumThreads) k_verify_sums(const VerifyArgs a) {
-  __shared__ double table[32];
+  __shared__ double table[kExpTable];
   __shared__ int verdict[kMaxDraft];
+  __shared__ Norms norms;
   __shared__ Deciding d;
   pdl_trigger();
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) table[threadIdx.x] = exp2(threadIdx.x * 0.03125);
+  if (threadIdx.x < kExpTable) table[threadIdx.x] = exp2(threadIdx.x * (1.0 / kExpTable));
   const int n = drafts_of(a, b);
   pdl_wait();
-  judge(a, b, 0, n, verdict);
+  judge(a, b, 0, n, verdict, &norms);
   int row = 0;
   while (row < n && verdict[row] == 1) ++row;
-  describe(a, b, row, n, row < n && verdict[row] == 2, &d);
+  describe(a, b, row, n, norms, verdict, &d);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.deciding[b] = d;
   const int sub = blockIdx.x * kSumWarps + warp;
   const int j0 = min(a.c.V, sub * a.sub_len), j1 = min(a.c.V, j0 + a.sub_len);
@@ -315,14 +396,15 @@ __device__ double block_scan_f64(double v, double* buf /*[8]*/) {
 }
 
 __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a) {
-  __shared__ double table[32], buf[kSumWarps];
+  __shared__ double table[kExpTable], buf[kSumWarps];
   __shared__ int verdict[kMaxDraft];
+  __shared__ Norms norms;
   __shared__ Deciding d;
   __shared__ int cross, last;
   __shared__ double cross_start;
   const flashloop_verify_args& c = a.c;
   const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid < 32) table[tid] = exp2(tid * 0.03125);
+  if (tid < kExpTable) table[tid] = exp2(tid * (1.0 / kExpTable));
   const int n = drafts_of(a, b), D = c.D;
   const int32_t* draft = c.draft + static_cast<size_t>(b) * D;
   int32_t* tokens = c.tokens + static_cast<size_t>(b) * (D + 1);
@@ -330,6 +412,8 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a)
   pdl_wait();
   if (tid == 0) d = a.deciding[b];
   __syncthreads();
+  const double s64 = 64.0 * a.scale2;
+  auto prob = [&](float x, float lo, double offset) { return exp64_from(x, lo, s64, offset, table); };
   Sums s{0.0, 0.0, 0.0, 0.0};   // n_sub <= threads: one range each
   double zp, zq;
   auto totals = [&]() {
@@ -338,15 +422,15 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a)
     zq = block_sum_f64(s.q, buf);
   };
   totals();
-  while (d.near) {
+  while (d.near && d.fine) {
     const int x = draft[d.row];   // (in range: a token outside is never near)
-    const double p = exp2_neg((row_of(a, b, d.row)[x] - d.mp) * a.scale2, table) / zp;
-    const double q = c.draft_logits ? exp2_neg((row_of(a, b, D + 1 + d.row)[x] - d.mq) * a.scale2, table) / zq : 1.0;
+    const double p = prob(row_of(a, b, d.row)[x], d.lo_p, d.op) / zp;
+    const double q = c.draft_logits ? prob(row_of(a, b, D + 1 + d.row)[x], d.lo_q, d.oq) / zq : 1.0;
     if (!(static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + d.row]) * q < p)) break;   // rejected after all
     int row = d.row + 1;
-    judge(a, b, row, n, verdict);
+    judge(a, b, row, n, verdict, &norms);
     while (row < n && verdict[row] == 1) ++row;
-    describe(a, b, row, n, row < n && verdict[row] == 2, &d);
+    describe(a, b, row, n, norms, verdict, &d);
     for (int sub = warp; sub < a.n_sub; sub += kSumWarps) {
       const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
       const Sums t = range_sums(a, b, d, j0, j1, table);
@@ -358,10 +442,10 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a)
   const int acc = d.row;
   const bool with_draft = d.with_draft;
   const double ratio = with_draft ? zq / zp : 1.0;
-  const double w = ratio * s.ap - s.aq, mine = w > 0.0 ? w : (w == w ? 0.0 : w);
+  const double w = ratio * s.ap - s.aq, mine = w > 0.0 ? w : 0.0;
   const double before = block_scan_f64(mine, buf);
   const double total = block_sum_f64(mine, buf);
-  const bool fine = isfinite(total) && total > 0.0 && isfinite(zp) && (!with_draft || (isfinite(zq) && zq > 0.0));
+  const bool fine = d.fine && isfinite(total) && total > 0.0;
   for (int i = tid; i <= D; i += kSumThreads)
     if (i != acc || !fine) tokens[i] = i < acc ? draft[i] : -1;
   if (tid == 0) {
@@ -388,8 +472,8 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a)
   const float* xp = row_of(a, b, acc);
   const float* xq = with_draft ? row_of(a, b, D + 1 + acc) : nullptr;
   auto weight = [&](int j) {
-    const double ep = exp2_neg((xp[j] - d.mp) * a.scale2, table);
-    if (with_draft) return fmax(ratio * ep - exp2_neg((xq[j] - d.mq) * a.scale2, table), 0.0);
+    const double ep = prob(xp[j], d.lo_p, d.op);
+    if (with_draft) return fmax(ratio * ep - prob(xq[j], d.lo_q, d.oq), 0.0);
     return j == d.x_out ? 0.0 : ep;
   };
   double mass = 0.0;
@@ -456,10 +540,10 @@ __global__ void __launch_bounds__(256) k_verify_greedy(const VerifyArgs a) {
 bool verify_shape_ok(int B, int D, int V) {
   return B >= 1 && B <= 65535 && D >= 0 && D <= kMaxDraft && V >= 1 && V <= (1 << 30);
 }
-// Ranges of the deciding row: about six CTAs per SM over the batch, none with
+// Ranges of the deciding row: the CTAs of the whole batch resident at once (five per SM), none with
 // fewer than 1024 tokens (4 a thread), at most one range per thread of the third launch.
 void plan_sums(int B, int V, int& ctas, int& sub_len) {
-  ctas = std::min(std::min(kSumMaxCtas, std::max(1, 6 * kNumSM / B)), std::max(1, V / 1024));
+  ctas = std::min(std::min(kSumMaxCtas, std::max(1, 5 * kNumSM / B)), std::max(1, V / 1024));
   sub_len = (ceil_div_i(V, ctas * kSumWarps) + 31) & ~31;
 }
 int verify_chunks(int V) { return ceil_div_i(V, kVfChunk); }
@@ -474,7 +558,8 @@ extern "C" {
 size_t flashloop_verify_draft_scratch_bytes(int B, int D, int V) {
   if (!verify_shape_ok(B, D, V)) return 0;
   return align256_sz(static_cast<size_t>(B) * (2 * D + 1) * verify_chunks(V) * sizeof(RowPart)) +
-         align256_sz(B * sizeof(Deciding)) + align256_sz(static_cast<size_t>(B) * kSumThreads * sizeof(Sums)) + 256;
+         align256_sz(B * sizeof(Deciding)) + align256_sz(static_cast<size_t>(B) * kSumThreads * sizeof(Sums)) +
+         align256_sz(static_cast<size_t>(B) * (D + 1) * 4) + 256;
 }
 
 fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, size_t scratch_bytes,
@@ -502,17 +587,32 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   a.part = static_cast<RowPart*>(scratch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rows = c->D + 1 + (a.c.draft_logits ? c->D : 0);
-  cudaError_t e = launch_k(false, k_verify_rows, dim3(a.n_chunks, rows, c->B), dim3(kVfThreads), 0, s, a);
-  if (e != cudaSuccess) return cuda_status(e);
-  if (c->temperature == 0.f)
-    return cuda_status(launch_k(true, k_verify_greedy, dim3(c->B), dim3(256), 0, s, a));
   int ctas;
   plan_sums(c->B, c->V, ctas, a.sub_len);
   a.n_sub = ctas * kSumWarps;
   uint8_t* ws = static_cast<uint8_t*>(scratch) +
                 align256_sz(static_cast<size_t>(c->B) * (2 * c->D + 1) * a.n_chunks * sizeof(RowPart));
   a.deciding = reinterpret_cast<Deciding*>(ws);
-  a.sums = reinterpret_cast<Sums*>(ws + align256_sz(c->B * sizeof(Deciding)));
+  ws += align256_sz(c->B * sizeof(Deciding));
+  a.sums = reinterpret_cast<Sums*>(ws);
+  ws += align256_sz(static_cast<size_t>(c->B) * kSumThreads * sizeof(Sums));
+  a.tickets = reinterpret_cast<unsigned*>(ws);
+  a.dead = a.tickets + static_cast<size_t>(c->B) * c->D;
+  // Skipping rows behind a rejection pays when the calls' rows do not all start at once: about
+  // eight 32 KB chunks per SM are in flight, and the memset in front costs 2 us.
+  const bool early = c->temperature > 0.f && c->D >= 2 &&
+                     static_cast<double>(c->B) * rows * c->V * 4.0 > 64e6;
+  cudaError_t e;
+  const dim3 grid(a.n_chunks, c->B, rows);
+  if (early) {
+    e = cudaMemsetAsync(a.tickets, 0xFF, static_cast<size_t>(c->B) * (c->D + 1) * 4, s);
+    if (e == cudaSuccess) e = launch_k(false, k_verify_rows<true>, grid, dim3(kVfThreads), 0, s, a);
+  } else {
+    e = launch_k(false, k_verify_rows<false>, grid, dim3(kVfThreads), 0, s, a);
+  }
+  if (e != cudaSuccess) return cuda_status(e);
+  if (c->temperature == 0.f)
+    return cuda_status(launch_k(true, k_verify_greedy, dim3(c->B), dim3(256), 0, s, a));
   e = launch_k(true, k_verify_sums, dim3(ctas, c->B), dim3(kSumThreads), 0, s, a);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_k(true, k_verify_pick, dim3(c->B), dim3(kSumThreads), 0, s, a));

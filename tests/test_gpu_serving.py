@@ -371,6 +371,10 @@ VD = [
     (32, 4, 50, 1.0, None, True),
     (2, 2, 300007, 1.0, None, True),
     (300, 1, 2100, 0.9, None, True),
+    (24, 4, 100003, 1.0, [4, 3, 2, 1, 0, 4] * 4, True),
+    (40, 5, 100001, 0.8, None, False),
+    (6, 64, 30011, 1.0, None, True),
+    (5, 2, 900, 1e-9, None, True),
 ]
 
 
@@ -396,9 +400,25 @@ def check_verify(logits, dl, draft, u, n_draft, T):
 @pytest.mark.parametrize("case", VD, ids=[f"{c[0]}x{c[1]}v{c[2]}t{c[3]}" for c in VD])
 def test_verify_against_64_bits(case):
     B, D, V, T, n_draft, with_draft = case
-    for seed in range(4):
+    for seed in range(4 if B * D * V < 10 ** 6 else 1):
         logits, dl, draft, u = verify_inputs(seed * 100 + V, B, D, V, T)
         check_verify(logits, dl if with_draft else None, draft, u, n_draft, T)
+
+
+def test_verify_large_calls_skip_only_what_decides_nothing():
+    """A call large enough to stop at rejections, repeated into a dirty scratch buffer and replayed: the same tokens each
+    time; drafts taken from the target's own most likely tokens, so that long runs are accepted."""
+    B, D, V = 32, 8, 40009
+    logits, _, _, u = verify_inputs(31, B, D, V, 1.0)
+    draft = logits[:, :D].argmax(-1).to(torch.int32)
+    dl = logits[:, :D] - 0.2 * torch.rand((B, D, 1), generator=gen(3), device="cuda")
+    dl.scatter_add_(2, draft.long()[..., None], torch.full((B, D, 1), 0.1, device="cuda"))
+    wt, wa = check_verify(logits, dl, draft, u, None, 1.0)
+    assert wa.max() == D and wa.min() < D
+    scratch = torch.full((fl.verify_draft_scratch_bytes(B, D, V),), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        tok, acc = fl.verify_draft(logits, dl, draft, u, scratch=scratch)
+        assert np.array_equal(tok.cpu().numpy(), wt) and np.array_equal(acc.cpu().numpy(), wa)
 
 
 def test_verify_border_random_numbers():
