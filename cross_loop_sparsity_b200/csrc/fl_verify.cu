@@ -305,17 +305,30 @@ __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int
       np += ep;
     }
   };
-  int j = j0 + lane;
-  for (; j + 32 * (U - 1) < j1; j += 32 * U) {
-    float fp[U], fq[U];
+  // full rounds of U tokens a lane, the next round's loads under this one's arithmetic
+  const int rounds = j1 > j0 ? (j1 - j0) / (32 * U) : 0;
+  float fp[U], fq[U];
+  auto load = [&](int r) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      fp[u] = xp[j + u * 32];
-      fq[u] = DRAFT ? xq[j + u * 32] : 0.f;
+      const int j = j0 + (r * U + u) * 32 + lane;
+      fp[u] = xp[j];
+      fq[u] = DRAFT ? xq[j] : 0.f;
     }
+  };
+  if (rounds) load(0);
+  for (int r = 0; r < rounds; ++r) {
+    float gp[U], gq[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) add(fp[u], fq[u], j + u * 32);
+    for (int u = 0; u < U; ++u) {
+      gp[u] = fp[u];
+      gq[u] = fq[u];
+    }
+    if (r + 1 < rounds) load(r + 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) add(gp[u], gq[u], j0 + (r * U + u) * 32 + lane);
   }
+  int j = j0 + rounds * 32 * U + lane;
   for (; j < j1; j += 32) add(xp[j], DRAFT ? xq[j] : 0.f, j);
   Sums s{ap + np, aq + nq, ap, aq};
 #pragma unroll
@@ -339,7 +352,7 @@ __device__ __forceinline__ Sums range_sums(const VerifyArgs& a, int b, const Dec
 // (about 11 operations per exponential) for many sequences, by the latency of
 // finding the row for few.
 // ============================================================================
-__global__ void __launch_bounds__(kSumThreads) k_verify_sums(const VerifyArgs a) {
+__global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs a) {
   __shared__ double table[kExpTable];
   __shared__ int verdict[kMaxDraft];
   __shared__ Norms norms;
@@ -540,10 +553,10 @@ __global__ void __launch_bounds__(256) k_verify_greedy(const VerifyArgs a) {
 bool verify_shape_ok(int B, int D, int V) {
   return B >= 1 && B <= 65535 && D >= 0 && D <= kMaxDraft && V >= 1 && V <= (1 << 30);
 }
-// Ranges of the deciding row: the CTAs of the whole batch resident at once (five per SM), none with
+// Ranges of the deciding row: the CTAs of the whole batch resident at once (four per SM), none with
 // fewer than 1024 tokens (4 a thread), at most one range per thread of the third launch.
 void plan_sums(int B, int V, int& ctas, int& sub_len) {
-  ctas = std::min(std::min(kSumMaxCtas, std::max(1, 5 * kNumSM / B)), std::max(1, V / 1024));
+  ctas = std::min(std::min(kSumMaxCtas, std::max(1, 4 * kNumSM / B)), std::max(1, V / 1024));
   sub_len = (ceil_div_i(V, ctas * kSumWarps) + 31) & ~31;
 }
 int verify_chunks(int V) { return ceil_div_i(V, kVfChunk); }
