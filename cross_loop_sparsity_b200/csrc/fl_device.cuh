@@ -94,6 +94,35 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// 2^y of two values on the FMA pipe, to 2e-7 (0 becomes 2^-126; NaN and overflow as they should be):
+// y = k + f with k = rint(y) (adding 1.5 * 2^23 leaves k in the low bits), a polynomial for 2^f on
+// [-1/2, 1/2] times 2^k.  The coefficients are a least-maximum fit of the relative error (1.6e-7), computed for
+// this purpose.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t y2) {
+  float y0, y1;
+  f2_unpack(y2, y0, y1);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y0) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y1) : "f"(-126.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y0) : "f"(128.f));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y1) : "f"(128.f));
+  y2 = f2_pack(y0, y1);
+  auto c = [](float x) { return f2_pack(x, x); };
+  const uint64_t t2 = f2_add(y2, c(12582912.f));
+  const uint64_t f2 = f2_fma(f2_add(t2, c(-12582912.f)), c(-1.f), y2);
+  uint64_t p = f2_fma(c(0.001327647129073739f), f2, c(0.009675541892647743f));
+  p = f2_fma(p, f2, c(0.05550713092088699f));
+  p = f2_fma(p, f2, c(0.24022120237350464f));
+  p = f2_fma(p, f2, c(0.6931469440460205f));
+  p = f2_fma(p, f2, c(1.0000001192092896f));
+  float t0, t1;
+  f2_unpack(t2, t0, t1);
+  const uint64_t s2 = f2_pack(__int_as_float((__float_as_int(t0) << 23) + 0x3F800000),
+                              __int_as_float((__float_as_int(t1) << 23) + 0x3F800000));
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(p), "l"(s2));
+  return r;
+}
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");

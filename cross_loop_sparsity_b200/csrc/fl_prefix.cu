@@ -1074,8 +1074,8 @@ struct WeightsArgs {
   int B, Tq, H, Hkv, G, S;
   float scale2;
   int nt;             // k_weights_tc: queries (of G rows) per row block
-  int n_rs;           // k_weights_tc: row splits
-  float* part;        // [n_rs][B][Hkv][S] when n_rs > 1
+  int ctas;           // k_weights_tc: CTAs at most
+  float* part;        // k_weights_tc: [ctas + key tiles][kWtCols]
 };
 // What the queries of sequence b see: query t columns j < min(j0 + t + 1, len) (every column when not causal).
 struct Seen {
@@ -1212,176 +1212,285 @@ __global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_c
       mbar_wait(smem_u32(&full[warp][(u - u0) % kWsStages]), static_cast<int>((u - u0) / kWsStages) & 1, nullptr);
 }
 
-// ---- many rows: S^T = K Q^T on tcgen05, 128 keys x 128 rows a block, so that a thread
-// owns a key and its sum needs no exchange.  One TMA thread, one MMA thread, two
-// warpgroups that take alternate row blocks (a TMEM buffer each).  Two CTAs per SM.  Bound by
-// the exponentials: 16 a clock and SM against 32 multiply-adds of head_dim 128.
-constexpr int kWtCols = 128, kWtRows = 128, kWtThreads = 320;
+// ---- many rows: S^T = K Q^T on tcgen05, blocks of 256 keys (two products of 128) x 128 rows, so that a
+// thread owns a key and its sum needs no exchange.  Persistent: the (sequence, KV head, 256 keys,
+// row block) units, in this order, are divided evenly over the CTAs; a CTA's part of a
+// tile's sums is partial (CTA + tile).  One TMA thread, one MMA warp, four warpgroups (all 256 keys x
+// a quarter of a block's rows each; two TMEM buffers, so that the next block's products run under
+// this one's exponentials).  Bound by the exponentials, 16 a clock and SM, with shared memory
+// (the products' operands) close behind.
+constexpr int kWtPoly = 1;   // of 8 pairs of exponentials, those formed on the FMA pipe
+constexpr int kWtCols = 256, kWtRows = 128, kWtThreads = 576;
+constexpr int kWtStaged = 24;   // row blocks whose lse are in shared memory at once
 template <int HD>
-__global__ void __launch_bounds__(kWtThreads, 2)
+struct WtSmem {
+  static constexpr int kBox = 128 * 128, kTile = (HD / 64) * kBox;   // 128 rows
+  static constexpr int kQSlots = HD == 128 ? 2 : 4;      // and two slots of 256 keys
+  static constexpr int kBytes = 1024 + (4 + kQSlots) * kTile;
+};
+struct WtPlan {
+  int tiles_s, nb, ctas;   // key tiles per (sequence, KV head), row blocks of nt queries, CTAs
+  long long units;
+  __host__ __device__ WtPlan(int B, int Hkv, int S, int Tq, int nt, int max_ctas) {
+    tiles_s = (S + kWtCols - 1) / kWtCols;
+    nb = (Tq + nt - 1) / nt;
+    units = static_cast<long long>(B) * Hkv * tiles_s * nb;
+    ctas = static_cast<int>(units < max_ctas ? units : max_ctas);
+  }
+  __host__ __device__ long long begin(int c) const { return c * units / ctas; }
+  __host__ __device__ int cta_of(long long u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kWtThreads, 1)
     k_weights_tc(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap qm, const WeightsArgs a) {
-  constexpr int NB = HD / 64, BOX = 128 * 128, TILE = NB * BOX;
+  using C = WtSmem<HD>;
+  constexpr int NB = HD / 64, QS = C::kQSlots;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* ksm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qsm = ksm + TILE;   // two row blocks
-  __shared__ __align__(8) uint64_t k_full, q_full[2], q_empty[2], d_full[2], d_empty[2];
+  uint8_t* qsm = ksm + 4 * C::kTile;
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], q_full[QS], q_empty[QS], d_full[2], d_empty[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(16) float lse_s[2][kWtRows];
-  __shared__ float join[128];
+  __shared__ __align__(16) float lse_s[kWtStaged][kWtRows];   // of the segment's next blocks: -lse log2(e), or -inf
+  __shared__ uint8_t none_s[kWtStaged][4];                    // some row of the block's quarter adds nothing
+  __shared__ float join[4][kWtCols];
   __shared__ volatile int bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int col0 = blockIdx.x * kWtCols, g = blockIdx.y % a.Hkv, rs = blockIdx.y / a.Hkv, b = blockIdx.z;
-  const Seen see(a, b);
-  const long long base = (static_cast<long long>(b) * a.Hkv + g) * a.S;
-  float* out = a.n_rs > 1 ? a.part + static_cast<long long>(rs) * a.B * a.Hkv * a.S : a.out;
-  const int ncol = min(kWtCols, a.S - col0);
-  // queries that see any of these columns, from t0 on; this split's blocks of nt of them
-  const int t0 = see.causal ? max(0, col0 - see.j0) : 0;
-  const int all_blocks = col0 < see.len && t0 < see.ql ? (see.ql - t0 + a.nt - 1) / a.nt : 0;
-  const int first = rs * all_blocks / a.n_rs, blocks = (rs + 1) * all_blocks / a.n_rs - first;
-  if (blocks == 0) {
-    if (tid < ncol) {
-      if (a.n_rs > 1) out[base + col0 + tid] = 0.f;
-      else if (a.out != a.acc) out[base + col0 + tid] = a.acc[base + col0 + tid];
-    }
-    return;
-  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (tid == 0) {
-    mbar_init(smem_u32(&k_full), 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < QS; ++i) {
       mbar_init(smem_u32(&q_full[i]), 1);
       mbar_init(smem_u32(&q_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&k_full[i]), 1);
+      mbar_init(smem_u32(&k_empty[i]), 1);
       mbar_init(smem_u32(&d_full[i]), 1);
-      mbar_init(smem_u32(&d_empty[i]), 128);
+      mbar_init(smem_u32(&d_empty[i]), 512);
     }
     fence_mbar_init();
     bad = 0;
   }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(&tmem_slot), 256);
+  if (warp == 16) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
   const uint32_t tmem = tmem_slot;
-  if (warp < 8) {
-    // ================= a warpgroup: blocks wg, wg + 2, .. =================
-    const int wg = warp >> 2, key = (warp & 3) * 32 + lane, row = tid & 127;
-    const uint32_t td = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 128;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    const int j = col0 + key;
-    int phase = 0;
+  const WtPlan plan(a.B, a.Hkv, a.S, a.Tq, a.nt, a.ctas);
+  const long long u0 = plan.begin(blockIdx.x), u1 = plan.begin(blockIdx.x + 1);
+  // a segment: one key tile of the CTA's range, and the row blocks [first, first + count) of it that see any of its columns
+  struct Segment {
+    int b, g, col0, first, count;
+    long long tile;
+  };
+  auto segment = [&](long long u) {
+    Segment x;
+    x.tile = u / plan.nb;
+    const int pair = static_cast<int>(x.tile / plan.tiles_s);
+    x.b = pair / a.Hkv;
+    x.g = pair % a.Hkv;
+    x.col0 = static_cast<int>(x.tile % plan.tiles_s) * kWtCols;
+    const Seen see(a, x.b);
+    int lo = static_cast<int>(u % plan.nb), hi = static_cast<int>(min(static_cast<long long>(plan.nb), lo + (u1 - u)));
+    hi = x.col0 < see.len ? min(hi, (see.ql + a.nt - 1) / a.nt) : 0;   // queries there are
+    if (see.causal) lo = max(lo, max(0, x.col0 - see.j0) / a.nt);      // queries that see column col0
+    x.first = lo;
+    x.count = max(0, hi - lo);
+    return x;
+  };
+  if (warp < 16) {
+    // ================= a warpgroup: a quarter of the rows of every block, keys `key` and 128 + key a thread ====
+    // (two keys a thread: a row's lse is then read from shared memory, whose bandwidth the products'
+    // operands need too, once for both)
+    const int wg = warp >> 2, key = (warp & 3) * 32 + lane;
+    const uint32_t td = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 32;
+    const uint64_t sc2 = f2_pack(a.scale2, a.scale2);
+    int seen = 0;             // blocks of the CTA so far
     bool ok = true;
-    for (int n = wg; n < blocks; n += 2, ++phase) {
-      const int tb = t0 + (first + n) * a.nt;                 // the block's first query
-      const int t = tb + row / a.G, h = g * a.G + row % a.G;
-      float l = -INFINITY;
-      if (row < a.nt * a.G && t < see.ql) l = a.lse[(static_cast<long long>(b) * a.Tq + t) * a.H + h];
-      lse_s[wg][row] = l == -INFINITY ? INFINITY : l * kLog2e;   // +inf: the row adds nothing
-      // rows that add nothing, or columns that the block's first queries do not see: each weight is looked at
-      int edge = l == -INFINITY || (see.causal && see.limit(tb) < min(col0 + kWtCols, see.len));
-      if (wg == 0)
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\t"
-                     "selp.s32 %0, 1, 0, q;\n\t}" : "+r"(edge)::"memory");
-      else
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %0, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
-                     "selp.s32 %0, 1, 0, q;\n\t}" : "+r"(edge)::"memory");
-      // (after a wait that ran out the loop goes on without waiting, so that the barriers above still meet)
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&d_full[wg]), phase & 1, nullptr));
-      if (!ok) continue;
-      tc_fence_after();
-      // the first row (query) of the block that sees this key
-      const int r_min = see.causal ? max(0, j - see.j0 - tb) * a.G : 0;
+    for (long long u = u0; u < u1; u += plan.nb - u % plan.nb) {
+      const Segment sg = segment(u);
+      const Seen see(a, sg.b);
+      float sum[2] = {0.f, 0.f};
+      uint64_t sum2[2][2] = {{0, 0}, {0, 0}};
+      for (int n = 0; n < sg.count; ++n) {
+        const int tb = (sg.first + n) * a.nt, blk = seen + n;    // the block's first query; its number in the CTA
+        if (n % kWtStaged == 0) {
+          // the next blocks' lse: a warp's 32 consecutive rows at a time
+          asm volatile("bar.sync 5, 512;" ::: "memory");         // (the last ones have been read)
+          const int todo = min(kWtStaged, sg.count - n) * 4;
+          for (int x0 = warp; x0 < todo; x0 += 64) {
+            float l[4];                                          // four in flight
 #pragma unroll
-      for (int c = 0; c < kWtRows; c += 32) {
-        uint32_t r[32];
-        tmem_ld32(td + c, r);
+            for (int v = 0; v < 4; ++v) {
+              const int x = x0 + v * 16, row = (x & 3) * 32 + lane, row_t = row / a.G, t = tb + (x >> 2) * a.nt + row_t;
+              l[v] = x < todo && row_t < a.nt && t < see.ql
+                         ? a.lse[(static_cast<long long>(sg.b) * a.Tq + t) * a.H + sg.g * a.G + row - row_t * a.G]
+                         : -INFINITY;
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int x = x0 + v * 16;
+              if (x >= todo) break;
+              lse_s[x >> 2][(x & 3) * 32 + lane] = l[v] == -INFINITY ? -INFINITY : -l[v] * kLog2e;
+              const bool none = __any_sync(0xffffffffu, l[v] == -INFINITY);
+              if (lane == 0) none_s[x >> 2][x & 3] = none;
+            }
+          }
+          asm volatile("bar.sync 5, 512;" ::: "memory");
+        }
+        const float* lse_b = &lse_s[n % kWtStaged][wg * 32];
+        // rows that add nothing, or columns that the block's first queries do not see: each weight is looked at
+        const bool edge = none_s[n % kWtStaged][wg] || (see.causal && see.limit(tb) < min(sg.col0 + kWtCols, see.len));
+        // (after a wait that ran out the loop goes on without waiting, so that the barriers above still meet)
+        const int par = blk & 1;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(smem_u32(&d_full[par]), (blk >> 1) & 1, nullptr));
+        if (!ok) continue;
+        tc_fence_after();
+        uint32_t r[2][32];
+        tmem_ld32(td + par * 256, r[0]);
+        tmem_ld32(td + par * 256 + 128, r[1]);
         tc_wait_ld();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&d_empty[par]));       // in registers: the buffer is free
         if (!edge) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(&lse_s[wg][c + e]);
-            sum[0] += ex2_approx(fmaf(__uint_as_float(r[e]), a.scale2, -l4.x));
-            sum[1] += ex2_approx(fmaf(__uint_as_float(r[e + 1]), a.scale2, -l4.y));
-            sum[2] += ex2_approx(fmaf(__uint_as_float(r[e + 2]), a.scale2, -l4.z));
-            sum[3] += ex2_approx(fmaf(__uint_as_float(r[e + 3]), a.scale2, -l4.w));
+            const float4 l4 = *reinterpret_cast<const float4*>(&lse_b[e]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t l2 = h ? f2_pack(l4.z, l4.w) : f2_pack(l4.x, l4.y);
+#pragma unroll
+              for (int kt = 0; kt < 2; ++kt) {
+                const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(r[kt][e + 2 * h]), __uint_as_float(r[kt][e + 2 * h + 1])), sc2, l2);
+                if ((e / 2 + h) % 8 < kWtPoly) {   // part of the exponentials on the FMA pipe
+                  sum2[kt][h] = f2_add(sum2[kt][h], exp2_poly2(y2));
+                } else {
+                  float p0, p1;
+                  f2_unpack(y2, p0, p1);
+                  sum2[kt][h] = f2_add(sum2[kt][h], f2_pack(ex2_approx(p0), ex2_approx(p1)));
+                }
+              }
+            }
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float l2 = lse_s[wg][c + e];
-            const float p = ex2_approx(fmaf(__uint_as_float(r[e]), a.scale2, -l2));
-            sum[e & 3] += c + e >= r_min && l2 < INFINITY ? p : 0.f;
+          for (int kt = 0; kt < 2; ++kt) {
+            // the first of these rows (query) that sees this key
+            const int r_min = (see.causal ? max(0, sg.col0 + kt * 128 + key - see.j0 - tb) * a.G : 0) - wg * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float l2 = lse_b[e];
+              const float p = ex2_approx(fmaf(__uint_as_float(r[kt][e]), a.scale2, l2));
+              sum[kt] += e >= r_min && l2 > -INFINITY ? p : 0.f;
+            }
           }
         }
       }
-      tc_fence_before();
-      mbar_arrive(smem_u32(&d_empty[wg]));
-    }
-    if (!ok) bad = 1;
-    float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    if (j >= see.len) total = 0.f;   // (a column past the sequence: nobody sees it)
-    if (wg == 1) join[key] = total;
-    asm volatile("bar.sync 3, 256;" ::: "memory");
-    if (wg == 0 && key < ncol) {
-      total += join[key];
-      if (bad) total = NAN;
-      out[base + j] = a.n_rs > 1 ? total : a.acc[base + j] + total;
-    }
-  } else if (tid == 8 * 32) {
-    // ================= MMA thread =================
-    constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
-    bool ok = mbar_wait(smem_u32(&k_full), 0, nullptr);
-    for (int n = 0; ok && n < blocks; ++n) {
-      const int st = n & 1, ph = n >> 1;
-      ok = mbar_wait(smem_u32(&q_full[st]), ph & 1, nullptr) && (n < 2 || mbar_wait(smem_u32(&d_empty[st]), (ph - 1) & 1, nullptr));
-      if (!ok) break;
-      tc_fence_after();
+      seen += sg.count;
+      if (!ok) bad = 1;
 #pragma unroll
-      for (int k = 0; k < HD / 16; ++k)
-        tc_mma_bf16(tmem + st * 128, umma_desc_sw128(smem_u32(ksm) + (k >> 2) * BOX + (k & 3) * 32),
-                    umma_desc_sw128(smem_u32(qsm) + st * TILE + (k >> 2) * BOX + (k & 3) * 32), idesc, k > 0);
-      tc_commit(smem_u32(&q_empty[st]));
-      tc_commit(smem_u32(&d_full[st]));
+      for (int kt = 0; kt < 2; ++kt) {
+        float total, odd;
+        f2_unpack(f2_add(sum2[kt][0], sum2[kt][1]), total, odd);
+        total = (total + odd) + sum[kt];
+        join[wg][kt * 128 + key] = sg.col0 + kt * 128 + key < see.len ? total : 0.f;   // (past the sequence: nobody sees it)
+      }
+      asm volatile("bar.sync 5, 512;" ::: "memory");
+      if (tid < kWtCols)
+        a.part[(blockIdx.x + sg.tile) * kWtCols + tid] = bad ? NAN : (join[0][tid] + join[1][tid]) + (join[2][tid] + join[3][tid]);
+      asm volatile("bar.sync 5, 512;" ::: "memory");   // join read
+    }
+  } else if (warp == 16) {
+    // ================= MMA warp (one elected lane issues) =================
+    constexpr uint32_t idesc = umma_idesc_bf16(128, 128);
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, nullptr)) != 0;
+    };
+    const uint64_t k_desc = umma_desc_sw128(smem_u32(ksm)), q_desc = umma_desc_sw128(smem_u32(qsm));
+    int blocks = 0, segs = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < u1; u += plan.nb - u % plan.nb) {
+      const Segment sg = segment(u);
+      if (sg.count == 0) continue;
+      const int ks = segs & 1;
+      ok = wait(&k_full[ks], segs++ >> 1);
+      for (int n = 0; ok && n < sg.count; ++n, ++blocks) {
+        const int st = blocks % QS, par = blocks & 1, use = blocks >> 1;
+        ok = wait(&q_full[st], blocks / QS) && (use == 0 || wait(&d_empty[par], use - 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k)
+              tc_mma_bf16(tmem + par * 256 + kt * 128, k_desc + (ks * 2 + kt) * (C::kTile >> 4) + (k >> 2) * (C::kBox >> 4) + (k & 3) * 2,
+                          q_desc + st * (C::kTile >> 4) + (k >> 2) * (C::kBox >> 4) + (k & 3) * 2, idesc, k > 0);
+          tc_commit(smem_u32(&d_full[par]));
+          tc_commit(smem_u32(&q_empty[st]));
+          if (n + 1 == sg.count) tc_commit(smem_u32(&k_empty[ks]));
+        }
+        __syncwarp();
+      }
     }
     if (!ok) bad = 1;
-  } else if (tid == 9 * 32) {
+  } else if (tid == 17 * 32) {
     // ================= TMA thread =================
-    mbar_arrive_expect_tx(smem_u32(&k_full), TILE);
-    for (int bx = 0; bx < NB; ++bx) tma_load_4d(smem_u32(ksm) + bx * BOX, &km, smem_u32(&k_full), bx * 64, col0, g, b);
-    int n = 0;
-    for (; n < blocks; ++n) {
-      const int st = n & 1;
-      if (n >= 2 && !mbar_wait(smem_u32(&q_empty[st]), ((n >> 1) - 1) & 1, nullptr)) break;
-      mbar_arrive_expect_tx(smem_u32(&q_full[st]), a.nt * a.G * HD * 2);
-      // rows in the order (query, head of the group); queries past the tensor's last read as zero
-      for (int bx = 0; bx < NB; ++bx)
-        tma_load_4d(smem_u32(qsm) + st * TILE + bx * BOX, &qm, smem_u32(&q_full[st]), bx * 64, g * a.G,
-                    t0 + (first + n) * a.nt, b);
+    int blocks = 0, segs = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < u1; u += plan.nb - u % plan.nb) {
+      const Segment sg = segment(u);
+      if (sg.count == 0) continue;
+      const int ks = segs & 1;
+      ok = segs < 2 || mbar_wait(smem_u32(&k_empty[ks]), ((segs >> 1) - 1) & 1, nullptr);
+      if (!ok) break;
+      ++segs;
+      mbar_arrive_expect_tx(smem_u32(&k_full[ks]), 2 * C::kTile);
+      for (int i = 0; i < 2 * NB; ++i)   // (keys past the tensor's last read as zero)
+        tma_load_4d(smem_u32(ksm) + ks * 2 * C::kTile + i * C::kBox, &km, smem_u32(&k_full[ks]), (i % NB) * 64,
+                    sg.col0 + i / NB * 128, sg.g, sg.b);
+      for (int n = 0; n < sg.count; ++n) {
+        const int st = blocks % QS;
+        ok = blocks < QS || mbar_wait(smem_u32(&q_empty[st]), (blocks / QS - 1) & 1, nullptr);
+        if (!ok) break;
+        ++blocks;
+        mbar_arrive_expect_tx(smem_u32(&q_full[st]), a.nt * a.G * HD * 2);
+        // rows in the order (query, head of the group); queries past the tensor's last read as zero
+        for (int bx = 0; bx < NB; ++bx)
+          tma_load_4d(smem_u32(qsm) + st * C::kTile + bx * C::kBox, &qm, smem_u32(&q_full[st]), bx * 64, sg.g * a.G,
+                      (sg.first + n) * a.nt, sg.b);
+      }
     }
-    if (n < blocks) {   // the products stopped: let the copies in flight land (bounded) before the block can end
+    if (!ok) {   // the products stopped: let the copies in flight land (bounded) before the block can end
       bad = 1;
-      mbar_wait(smem_u32(&k_full), 0, nullptr);
-      for (int i = max(0, n - 2); i < n; ++i) mbar_wait(smem_u32(&q_full[i & 1]), (i >> 1) & 1, nullptr);
+      if (segs) mbar_wait(smem_u32(&k_full), (segs - 1) & 1, nullptr);
+      for (int i = max(0, blocks - QS); i < blocks; ++i) mbar_wait(smem_u32(&q_full[i % QS]), (i / QS) & 1, nullptr);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-// the row splits' sums, in order, added to acc
-__global__ void __launch_bounds__(256) k_weights_add(const WeightsArgs a, long long n) {
+// the parts of each key tile, in order, added to acc
+__global__ void __launch_bounds__(256) k_weights_add(const WeightsArgs a) {
+  const WtPlan plan(a.B, a.Hkv, a.S, a.Tq, a.nt, a.ctas);
+  const long long tile = blockIdx.x;
+  const int pair = static_cast<int>(tile / plan.tiles_s), j = static_cast<int>(tile % plan.tiles_s) * kWtCols + threadIdx.x;
+  const int c0 = plan.cta_of(tile * plan.nb), c1 = plan.cta_of((tile + 1) * plan.nb - 1);
+  if (j >= a.S) return;
+  const long long at = static_cast<long long>(pair) * a.S + j;
+  const float acc = a.acc[at];
   pdl_wait();
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
   float s = 0.f;
-  for (int r = 0; r < a.n_rs; ++r) s += a.part[r * n + i];
-  a.out[i] = a.acc[i] + s;
+  for (int c = c0; c <= c1; ++c) s += __ldcg(&a.part[(c + tile) * kWtCols + threadIdx.x]);
+  a.out[at] = acc + s;
 }
 
 // ---------------------------------------------------------------- host side
@@ -1452,28 +1561,24 @@ cudaError_t run_split_hd(int nm, bool hilo, const CUtensorMap* m, const PrefixAr
 }
 
 size_t stream_smem(int hd) { return 1024 + static_cast<size_t>(kWsWarps) * kWsStages * kPxTile * hd * 2; }
-size_t weights_tc_smem(int hd) { return 1024 + static_cast<size_t>(kWtCols + 2 * kWtRows) * hd * 2; }
 
 // Column weights on tcgen05 when a (sequence, KV head) has more rows than two warp tiles.
-// Row splits while there are fewer CTAs than two per SM and a split keeps two row blocks.
 constexpr int kStreamRows = 32;
 struct WeightsPlan {
   bool tc;
-  int nt, n_rs;
+  int nt;
+  long long tiles;
   size_t bytes;
 };
 WeightsPlan plan_weights(int B, int Tq, int H, int Hkv, int S) {
   WeightsPlan p{};
   const int G = H / Hkv;
   p.tc = static_cast<long long>(Tq) * G > kStreamRows;
-  p.n_rs = 1;
   p.bytes = 256;
   if (!p.tc) return p;
   p.nt = std::min(kWtRows / G, 256);
-  const long long ctas = static_cast<long long>(ceil_div_i(S, kWtCols)) * Hkv * B;
-  const int blocks = ceil_div_i(Tq, p.nt);
-  while (ctas * p.n_rs < 2 * kNumSM && blocks >= 4 * p.n_rs && Hkv * p.n_rs * 2 <= 65535) p.n_rs *= 2;
-  if (p.n_rs > 1) p.bytes += static_cast<size_t>(p.n_rs) * B * Hkv * S * 4;
+  p.tiles = static_cast<long long>(B) * Hkv * ceil_div_i(S, kWtCols);
+  p.bytes += static_cast<size_t>(p.tiles + kNumSM) * kWtCols * 4;
   return p;
 }
 
@@ -1505,8 +1610,8 @@ cudaError_t serving_init_attrs() {
   set(k_weights_stream<64, 2>, stream_smem(64));
   set(k_weights_stream<128, 1>, stream_smem(128));
   set(k_weights_stream<128, 2>, stream_smem(128));
-  set(k_weights_tc<64>, weights_tc_smem(64));
-  set(k_weights_tc<128>, weights_tc_smem(128));
+  set(k_weights_tc<64>, WtSmem<64>::kBytes);
+  set(k_weights_tc<128>, WtSmem<128>::kBytes);
   if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return e;
 }
@@ -1657,7 +1762,7 @@ fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratc
   const WeightsPlan p = plan_weights(a->B, a->Tq, a->H, a->Hkv, a->S);
   CUtensorMap km, qm;
   if (!encode_tmap_rows(&km, a->k, a->hd, a->S, a->Hkv, a->B, a->k_stride[2], a->k_stride[1], a->k_stride[0],
-                        p.tc ? kWtCols : kPxTile))
+                        p.tc ? 128 : kPxTile))
     return refuse(FL_ERR_INVALID_ARG, "tensor map encoding failed");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!p.tc) {
@@ -1675,14 +1780,13 @@ fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratc
   if (!encode_tmap_queries(&qm, a->q, a->hd, a->H, a->Tq, a->B, a->q_stride[2], a->q_stride[1], a->q_stride[0], w.G, p.nt))
     return refuse(FL_ERR_INVALID_ARG, "tensor map encoding failed");
   w.nt = p.nt;
-  w.n_rs = p.n_rs;
+  w.ctas = kNumSM;
   w.part = static_cast<float*>(scratch);
-  const dim3 grid(ceil_div_i(a->S, kWtCols), a->Hkv * p.n_rs, a->B);
-  e = a->hd == 128 ? launch_k(false, k_weights_tc<128>, grid, dim3(kWtThreads), weights_tc_smem(128), s, km, qm, w)
-                   : launch_k(false, k_weights_tc<64>, grid, dim3(kWtThreads), weights_tc_smem(64), s, km, qm, w);
-  if (e != cudaSuccess || p.n_rs == 1) return cuda_status(e);
-  const long long n = static_cast<long long>(a->B) * a->Hkv * a->S;
-  return cuda_status(launch_k(true, k_weights_add, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, w, n));
+  const dim3 grid(WtPlan(a->B, a->Hkv, a->S, a->Tq, p.nt, kNumSM).ctas);
+  e = a->hd == 128 ? launch_k(false, k_weights_tc<128>, grid, dim3(kWtThreads), WtSmem<128>::kBytes, s, km, qm, w)
+                   : launch_k(false, k_weights_tc<64>, grid, dim3(kWtThreads), WtSmem<64>::kBytes, s, km, qm, w);
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(launch_k(true, k_weights_add, dim3(static_cast<unsigned>(p.tiles)), dim3(256), 0, s, w));
 }
 
 }  // extern "C"
