@@ -19,6 +19,7 @@
 
 #include "flashloop.h"
 #include "fl_kernels.h"
+#include "fl_serving.h"
 
 using namespace fl;
 
@@ -110,6 +111,9 @@ struct flashloop_ctx {
   int trace_ns = 0;
   float* trace_ck = nullptr;
   int trace_tiles = 0;
+  // sequences 0..share_seqs-1 hold the same first share_n positions (0: not shared)
+  int share_seqs = 0, share_n = 0;
+  void* share_scratch = nullptr;
 };
 
 namespace {
@@ -645,7 +649,37 @@ fl_status run_layer(flashloop_ctx* ctx, const LayerRef& L, const CallShape& cs, 
   FL_GEMM(gemm(ctx, L.W, kOpQKV, L.z, n, idx, s, attn_in));
   FL_LAUNCH(FL_KIND_KV, launch_qkv_post(qa, s));
   if (L.full) {
-    if (cs.decode) {
+    if (cs.decode && ctx->share_n > 0 && cs.B >= 2 && cs.B <= ctx->share_seqs) {
+      // the common positions once for the whole batch, from sequence 0's rows; then each sequence's own
+      PrefixLaunch pl{};
+      flashloop_prefix_args& f = pl.a;
+      const CacheView& cv = *L.cv;
+      auto rows = [&](int kv, int t) {
+        return L.lazy ? cv.base_row(L.cj, kv, 0, 0, t) : cv.dense_row(L.cj, L.loop, kv, 0, 0, t);
+      };
+      f.k_prefix = rows(0, 0); f.v_prefix = rows(1, 0); f.k = rows(0, ctx->share_n); f.v = rows(1, ctx->share_n);
+      f.out = ctx->obf; f.lse = L.l_st; f.lens = ctx->pos;
+      f.B = cs.B; f.Tq = 1; f.H = H; f.Hkv = Hkv; f.hd = hd; f.P = ctx->share_n; f.S = cv.T - ctx->share_n;
+      f.scale = cs.tau;
+      for (int64_t* st : {f.q_stride, f.out_stride}) {
+        st[0] = st[1] = static_cast<int64_t>(H) * hd;
+        st[2] = hd;
+      }
+      const int64_t head = static_cast<int64_t>(cv.T) * hd;
+      for (int64_t* st : {f.kp_stride, f.vp_stride}) {
+        st[0] = head;
+        st[1] = hd;
+      }
+      for (int64_t* st : {f.k_stride, f.v_stride}) {
+        st[0] = Hkv * head;
+        st[1] = head;
+        st[2] = hd;
+      }
+      pl.q32 = ctx->q_cur; pl.out32 = L.o_st; pl.lens_add = 1 - ctx->share_n;   // pos holds the new token's position
+      pl.pdl = ctx->pdl != 0;
+      FL_LAUNCH(FL_KIND_ATTN, launch_prefix(pl, ctx->share_scratch, s));
+      ++ctx->launches;   // two kernels: the splits and their merge
+    } else if (cs.decode) {
       AttnDecArgs aa{};
       // a full loop covers every token in order: no index indirection
       aa.q_cur = ctx->q_cur; aa.idx = idx == ctx->idx_all ? nullptr : idx; aa.seq = ctx->seq; aa.pos = ctx->pos;
@@ -896,6 +930,28 @@ bool build_tmaps(flashloop_ctx* ctx) {
     ok &= encode_tmap_bf16(&ctx->tm_act_b[i], ctx->act, f, R, 0, bns[i]);
   }
   return ok;
+}
+
+// Captured decode graphs hold the arguments of the launches they were captured with: drop them.
+void drop_graphs(flashloop_ctx* ctx) {
+  for (cudaGraphExec_t e : ctx->graph_exec)
+    if (e) cudaGraphExecDestroy(e);
+  ctx->graph_exec.clear();
+  ctx->graph_b.clear();
+}
+
+void end_sharing(flashloop_ctx* ctx) {
+  if (!ctx->share_n) return;
+  ctx->share_n = ctx->share_seqs = 0;
+  ctx->share_scratch = nullptr;
+  drop_graphs(ctx);
+}
+
+size_t share_bytes(const flashloop_config& c, int n_seq, int n) {
+  size_t need = 0;
+  for (int b = 2; b <= n_seq; ++b)
+    need = std::max(need, prefix_scratch_bytes(b, 1, c.n_heads, c.n_kv_heads, c.head_dim, n, c.max_ctx - n, true));
+  return need;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -1157,6 +1213,11 @@ fl_status flashloop_reset(flashloop_ctx* ctx, const int* seq_len, fl_stream_t st
       if (seq_len[b] < 0 || seq_len[b] > ctx->cfg.max_ctx) return FL_ERR_CAPACITY;
       v[b] = seq_len[b];
     }
+  for (int b = 0; b < ctx->share_seqs; ++b)
+    if (v[b] < ctx->share_n) {   // what follows may rewrite the common positions
+      end_sharing(ctx);
+      break;
+    }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (B <= kLensByValue) {
     LensArg a{};
@@ -1239,6 +1300,7 @@ fl_status flashloop_import_lazy(flashloop_ctx* ctx, int layer, int seq, int n, c
   if (!base_k || !base_v || (c.n_loops > 1 && (!codes_k || !codes_v || !scales_k || !scales_v)))
     return FL_ERR_INVALID_ARG;
   if (n == 0) return FL_OK;
+  end_sharing(ctx);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int Hkv = c.n_kv_heads, hd = c.head_dim, ns = hd / c.group_size;
   const CacheView& cv = ctx->cv;
@@ -1277,6 +1339,7 @@ fl_status flashloop_import_dense(flashloop_ctx* ctx, int layer, int seq, int n, 
   if (layer < 0 || layer >= c.n_layers || seq < 0 || seq >= c.max_batch || n < 0 || n > c.max_ctx || !kv_k || !kv_v)
     return FL_ERR_INVALID_ARG;
   if (n == 0) return FL_OK;
+  end_sharing(ctx);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int Hkv = c.n_kv_heads, hd = c.head_dim;
   for (int kv = 0; kv < 2; ++kv) {
@@ -1296,6 +1359,7 @@ fl_status flashloop_import_extra(flashloop_ctx* ctx, int x, int seq, int n, cons
   const flashloop_config& c = ctx->cfg;
   if (x < 0 || x >= c.n_prelude + c.n_coda || seq < 0 || seq >= c.max_batch || n < 0 || n > c.max_ctx)
     return FL_ERR_INVALID_ARG;
+  if (n > 0) end_sharing(ctx);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int Hkv = c.n_kv_heads, hd = c.head_dim;
   for (int kv = 0; kv < 2 && n > 0; ++kv)
@@ -1409,11 +1473,33 @@ fl_status flashloop_set_trace(flashloop_ctx* ctx, float* kv_rows, int n_slots, f
   ctx->trace_ns = kv_rows ? n_slots : 0;
   ctx->trace_ck = col_keys;
   ctx->trace_tiles = col_keys ? n_tiles : 0;
-  // captured decode graphs hold the old pointers: capture again
-  for (cudaGraphExec_t e : ctx->graph_exec)
-    if (e) cudaGraphExecDestroy(e);
-  ctx->graph_exec.clear();
-  ctx->graph_b.clear();
+  drop_graphs(ctx);   // they hold the old pointers: capture again
+  return FL_OK;
+}
+
+size_t flashloop_share_prefix_scratch_bytes(const flashloop_config* cfg, int n_seq, int n) {
+  if (!valid_config(cfg) || n_seq < 2 || n_seq > cfg->max_batch || n < 1 || n >= cfg->max_ctx) return 0;
+  return share_bytes(*cfg, n_seq, n);
+}
+
+fl_status flashloop_share_prefix(flashloop_ctx* ctx, int n_seq, int n, void* scratch, size_t scratch_bytes) {
+  if (!ctx) return FL_ERR_INVALID_ARG;
+  if (n == 0) {
+    end_sharing(ctx);
+    return FL_OK;
+  }
+  const flashloop_config& c = ctx->cfg;
+  if (n_seq < 2 || n < 0) return FL_ERR_INVALID_ARG;
+  if (n_seq > c.max_batch || n >= c.max_ctx) return FL_ERR_CAPACITY;
+  for (int b = 0; b < n_seq; ++b)
+    if (ctx->lens[b] < n) return FL_ERR_INVALID_ARG;
+  if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255) || scratch_bytes < share_bytes(c, n_seq, n))
+    return FL_ERR_WORKSPACE;
+  FL_TRY(serving_init_attrs());
+  ctx->share_seqs = n_seq;
+  ctx->share_n = n;
+  ctx->share_scratch = scratch;
+  drop_graphs(ctx);
   return FL_OK;
 }
 

@@ -126,6 +126,8 @@ _SIG = {
     "fl_test_gemm_scratch_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "fl_test_gemm": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, ctypes.c_size_t, _P]),
     "fl_gemm_skinny_noalloc": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "flashloop_share_prefix_scratch_bytes": (ctypes.c_size_t, [ctypes.POINTER(Config), _I, _I]),
+    "flashloop_share_prefix": (_I, [_P, _I, _I, _P, ctypes.c_size_t]),
     "flashloop_prefix_attention_scratch_bytes": (ctypes.c_size_t, [_I] * 7),
     "flashloop_prefix_attention": (_I, [_P, _P, ctypes.c_size_t, _P]),
     "flashloop_column_weights_scratch_bytes": (ctypes.c_size_t, [_I] * 6),
@@ -279,6 +281,18 @@ class FlashLoop:
             arr = v.ctypes.data_as(ctypes.c_void_p)
             self._lens_keep = v
         _check(lib().flashloop_reset(self.ctx, arr, _stream_ptr(stream)), "flashloop_reset", self.ctx)
+
+    def share_prefix(self, n_seq: int, n: int):
+        """Sequences 0..n_seq-1 hold the same first n positions: decode steps read them once for
+        the batch (``flashloop_share_prefix``).  n = 0 ends it."""
+        import torch
+        scratch, nbytes = None, 0
+        if n:
+            nbytes = int(lib().flashloop_share_prefix_scratch_bytes(ctypes.byref(self.c), n_seq, n))
+            scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.workspace.device)
+        _check(lib().flashloop_share_prefix(self.ctx, n_seq, n, None if scratch is None else _ptr(scratch), nbytes),
+               "flashloop_share_prefix", self.ctx)
+        self._share_scratch = scratch   # keep alive: the library borrows it
 
     def sync_status(self, stream=None) -> int:
         return int(lib().flashloop_sync_status(self.ctx, _stream_ptr(stream)))

@@ -189,6 +189,21 @@ fl_status flashloop_kv_bytes_for(const flashloop_config* cfg, size_t* total, dou
  * without waiting. */
 fl_status flashloop_reset(flashloop_ctx* ctx, const int* seq_len, fl_stream_t stream);
 
+/* State that sequences 0..n_seq-1 hold the same first n positions (samples of one
+ * prompt): decode steps of 2..n_seq sequences then read those positions' keys and
+ * values once for the whole batch wherever they attend to every column (loop 1 of
+ * the lazy path, every loop of the dense baseline, prelude and coda layers), from
+ * sequence 0, instead of once per sequence (flashloop_prefix_attention with fp32 queries).  The
+ * caches are not compared: a statement that does not hold gives another result.
+ * n = 0 ends it, and so does an import, or a reset that sets one of those
+ * sequences shorter than n.  scratch: device memory of
+ * flashloop_share_prefix_scratch_bytes(), 256-byte aligned, the caller's, in use
+ * until sharing ends.  Captured decode graphs are dropped and captured again.
+ * Errors: FL_ERR_INVALID_ARG (n_seq < 2, n < 0, or a sequence shorter than n),
+ * FL_ERR_CAPACITY (n_seq > max_batch, n >= max_ctx), FL_ERR_WORKSPACE. */
+size_t flashloop_share_prefix_scratch_bytes(const flashloop_config* cfg, int n_seq, int n);
+fl_status flashloop_share_prefix(flashloop_ctx* ctx, int n_seq, int n, void* scratch, size_t scratch_bytes);
+
 /* Synchronise `stream` and report the first error a kernel recorded since
  * the last call, clearing it: FL_ERR_TIMEOUT (a bounded wait ran out),
  * FL_ERR_CAPACITY (a sparse residual pool was full), FL_ERR_NONFINITE (a
