@@ -168,11 +168,12 @@ __global__ void __launch_bounds__(128, 2)
 
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    for (int i = 0; i < kPxWarps * 12; ++i) mbar_init(smem_u32(&full[0][0] + i), 1);
+  if (lane == 0) {   // a warp's barriers are its own
+    for (int i = 0; i < SLOTS; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
     fence_mbar_init();
-    bad_sm = 0;
+    if (warp == 0) bad_sm = 0;
   }
+  __syncwarp();
   // Behind k_prefix_tc (which started after everything this call reads was
   // written, and shares nothing with this kernel) the wait moves to the end: the
   // two overlap, and the merge, which waits for this kernel, finds both complete.
@@ -187,38 +188,17 @@ __global__ void __launch_bounds__(128, 2)
   it /= nsp;
   const int g = it % a.Hkv, b = it / a.Hkv;
   const int r0 = rb * RB;
-  int ncols, nrows;
-  if (pre) {
-    const int first = r0 / a.G, count = (r0 + RB - 1) / a.G - first + 1;
-    if (warp == 0) {
-      const int total = pack_queries(a, first, count, slot_sm);
-      if (lane == 0) n_valid_sm = total;
-    }
-    __syncthreads();
-    nrows = n_valid_sm * a.G;
-    ncols = a.P;
-    if (tid < RB) {
-      const int s = r0 + tid < nrows ? slot_sm[(r0 + tid) / a.G - first] : -1;
-      row_id[tid] = s < 0 ? -1 : static_cast<long long>(s) * a.H + g * a.G + (r0 + tid) % a.G;
-    }
-  } else {
+  int ncols = a.P, nrows;
+  if (!pre) {
     const int ql = q_len_of(a, b), len = len_of(a, b);
     nrows = ql * a.G;
     ncols = min(max(len - ql + 1, 0), len);
-    if (tid < RB) {
-      const int r = r0 + tid;
-      row_id[tid] = r < nrows ? (static_cast<long long>(b) * a.Tq + r / a.G) * a.H + g * a.G + r % a.G : -1;
-    }
   }
-  __syncthreads();   // barriers, row_id
-  if (r0 >= nrows) {
-    if (a.tc_ctas) pdl_wait();
-    return;
-  }
+  // ---- this warp's tiles, the first of them requested while the rows are still being looked up
   const int ntiles = (ncols + kPxTile - 1) / kPxTile;
   const int tb = static_cast<int>(static_cast<long long>(sp) * ntiles / nsp);
   const int te = static_cast<int>(static_cast<long long>(sp + 1) * ntiles / nsp);
-  const int mine = te - tb > warp ? (te - tb - warp + kPxWarps - 1) / kPxWarps : 0;   // this warp's tiles
+  const int mine = te - tb > warp ? (te - tb - warp + kPxWarps - 1) / kPxWarps : 0;
   const CUtensorMap* km = pre ? &kp : &ks;
   const CUtensorMap* vm = pre ? &vp : &vs;
   uint8_t* wring = ring + warp * (kPxRing / kPxWarps);
@@ -231,7 +211,7 @@ __global__ void __launch_bounds__(128, 2)
     for (int bx = 0; bx < NB; ++bx) tma_load_4d(st + bx * kPxTile * 128, map, fb, bx * 64, y, g, pre ? 0 : b);
   };
   int issued = 0;             // (lane 0)
-  if (lane == 0)
+  if (lane == 0 && (pre || r0 < nrows))
     for (; issued < SLOTS && issued < 2 * mine; ++issued) issue(issued);
   // whole warp: load n has arrived, or (false) its wait ran out
   auto arrived = [&](int n) {
@@ -242,6 +222,29 @@ __global__ void __launch_bounds__(128, 2)
     __syncwarp();
     if (lane == 0 && issued < 2 * mine) issue(issued++);
   };
+  if (pre) {
+    const int first = r0 / a.G, count = (r0 + RB - 1) / a.G - first + 1;
+    if (warp == 0) {
+      const int total = pack_queries(a, first, count, slot_sm);
+      if (lane == 0) n_valid_sm = total;
+    }
+    __syncthreads();
+    nrows = n_valid_sm * a.G;
+    if (tid < RB) {
+      const int s = r0 + tid < nrows ? slot_sm[(r0 + tid) / a.G - first] : -1;
+      row_id[tid] = s < 0 ? -1 : static_cast<long long>(s) * a.H + g * a.G + (r0 + tid) % a.G;
+    }
+  } else if (tid < RB) {
+    const int r = r0 + tid;
+    row_id[tid] = r < nrows ? (static_cast<long long>(b) * a.Tq + r / a.G) * a.H + g * a.G + r % a.G : -1;
+  }
+  __syncthreads();   // row_id
+  if (r0 >= nrows) {
+    if (lane == 0)     // (no rows after all: the copies land before the block ends)
+      for (int n = 0; n < issued; ++n) mbar_wait(smem_u32(&full[warp][n]), 0, nullptr);
+    if (a.tc_ctas) pdl_wait();
+    return;
+  }
 
   // ---- queries to shared memory (rows past the last: zero)
   for (int e = tid; e < RB * (HD / 8); e += 128) {
@@ -917,8 +920,10 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   const int row = ALL ? blockIdx.x : min(static_cast<int>(a.rows) - 1, static_cast<int>(blockIdx.x * NG + threadIdx.x / LPG));
   const bool last = ALL || static_cast<int>(blockIdx.x * NG + threadIdx.x / LPG) < a.rows;   // (a group past the end repeats the last row)
   const int slot = row / a.H, h = row - slot * a.H, b = slot / a.Tq, t = slot - b * a.Tq;
-  pdl_wait();
-  const int ql = q_len_of(a, b);
+  // (a decode step's fp32 queries and lengths come from kernels the wait covers; a caller's were there before the first launch)
+  if (Q32) pdl_wait();
+  const int ql = q_len_of(a, b), len = len_of(a, b);
+  if (!Q32) pdl_wait();
   if (ALL && t >= ql) return;
   const bool valid = last && t < ql;
   float m = -INFINITY, l = 0.f;
@@ -995,7 +1000,6 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
     const int c1 = plan.cta_of(static_cast<long long>(pair + 1) * plan.ntiles - 1);
     add_parts(a.tc_o, a.tc_ml, static_cast<long long>(c0 + pair) * kTcRows + r % kTcRows, kTcRows, valid ? c1 - c0 + 1 : 0);
   }
-  const int len = len_of(a, b);
   const int base = min(max(len - ql + 1, 0), len), lim = min(max(len - ql + t + 1, 0), len);
   if (valid && lim > base) {
     const int g = h / a.G;
