@@ -351,7 +351,7 @@ fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t s
   }
   const size_t need = evict_bytes(c->B, c->Hkv, c->S, c->keep);
   if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
-    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+    return refuse_scratch(need);
   static bool done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -1388,7 +1388,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             for (int e = 0; e < 32; ++e) {
               const float l2 = lse_b[e];
               const float p = ex2_approx(fmaf(__uint_as_float(r[kt][e]), a.scale2, l2));
-              sum[kt] += e >= r_min && l2 > -INFINITY ? p : 0.f;
+              sum[kt] += e >= r_min && l2 != -INFINITY ? p : 0.f;
             }
           }
         }
@@ -1727,7 +1727,7 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
   if (span >= (int64_t(1) << 34)) return refuse(FL_ERR_INVALID_ARG, "q must span less than 2^34 elements");
   const size_t need = prefix_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->P, a->S, false);
   if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
-    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+    return refuse_scratch(need);
   PrefixLaunch L{};
   L.a = *a;
   return cuda_status(launch_prefix(L, scratch, reinterpret_cast<cudaStream_t>(stream)));
@@ -1755,7 +1755,7 @@ fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratc
       return refuse(FL_ERR_INVALID_ARG, "q and k strides must be positive multiples of 8");
   const size_t need = flashloop_column_weights_scratch_bytes(a->B, a->Tq, a->H, a->Hkv, a->hd, a->S);
   if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
-    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+    return refuse_scratch(need);
   cudaError_t e = serving_init_attrs();
   if (e != cudaSuccess) return cuda_status(e);
   WeightsArgs w{};

@@ -2,6 +2,7 @@
 // checks, the tensor maps of strided caches, and the prefix attention's launch
 // (also made by a context's decode step).
 #pragma once
+#include <cstdio>
 #include <string>
 
 #include "flashloop.h"
@@ -14,9 +15,18 @@ inline size_t align256_sz(size_t v) { return (v + 255) & ~size_t(255); }
 inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Failures leave their reason where flashloop_last_cuda_error(NULL) reports it.
-inline fl_status refuse(fl_status st, const std::string& why) {
-  set_last_error(why);
+// (Keeping the reason may need memory: without any, the status alone is left, and no exception crosses a C entry.)
+inline fl_status refuse(fl_status st, const char* why) {
+  try {
+    set_last_error(why);
+  } catch (...) {
+  }
   return st;
+}
+inline fl_status refuse_scratch(size_t need) {
+  char why[96];
+  std::snprintf(why, sizeof why, "scratch must be 256-byte aligned and hold %zu bytes", need);
+  return refuse(FL_ERR_WORKSPACE, why);
 }
 inline fl_status cuda_status(cudaError_t e) {
   return e == cudaSuccess ? FL_OK : refuse(FL_ERR_CUDA, cudaGetErrorString(e));

@@ -579,8 +579,8 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
                                  fl_stream_t stream) {
   if (!c) return refuse(FL_ERR_INVALID_ARG, "NULL arguments");
   if (!verify_shape_ok(c->B, c->D, c->V)) return refuse(FL_ERR_INVALID_ARG, "B, D (0 to 64) or V out of range");
-  if (!(c->temperature >= 0.f) || !std::isfinite(c->temperature))
-    return refuse(FL_ERR_INVALID_ARG, "temperature must be finite and not negative");
+  if (!(c->temperature == 0.f || c->temperature >= 1e-20f) || !std::isfinite(c->temperature))
+    return refuse(FL_ERR_INVALID_ARG, "temperature must be 0, or finite and at least 1e-20");
   if (!c->logits || !c->tokens || !c->n_accepted || (c->D > 0 && !c->draft) || (c->temperature > 0.f && !c->u))
     return refuse(FL_ERR_INVALID_ARG, "logits, draft, u, tokens and n_accepted must be non-NULL");
   const void* p4[7] = {c->logits, c->draft_logits, c->draft, c->u, c->n_draft, c->tokens, c->n_accepted};
@@ -591,7 +591,7 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
     return refuse(FL_ERR_INVALID_ARG, "strides must be positive");
   const size_t need = flashloop_verify_draft_scratch_bytes(c->B, c->D, c->V);
   if (!scratch || scratch_bytes < need || !is_aligned(scratch, 256))
-    return refuse(FL_ERR_WORKSPACE, "scratch must be 256-byte aligned and hold " + std::to_string(need) + " bytes");
+    return refuse_scratch(need);
   VerifyArgs a{};
   a.c = *c;
   if (c->temperature == 0.f) a.c.draft_logits = nullptr;   // greedy: the target's rows alone

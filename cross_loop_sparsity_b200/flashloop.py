@@ -7,6 +7,7 @@ fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -569,6 +570,12 @@ def _addr(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _on(stream):
+    """Buffers a call allocates belong to the stream it runs on, and are filled there."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _run(what: str, fn, ptrs: bytes, block, scratch, stream, device: int):
     import torch
     tail, nbytes = block
@@ -576,9 +583,8 @@ def _run(what: str, fn, ptrs: bytes, block, scratch, stream, device: int):
         with torch.cuda.device(device):
             return _run(what, fn, ptrs, block, scratch, stream, device)
     if scratch is None:
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-        if stream is not None:
-            scratch.record_stream(stream)   # the allocator must not reuse it under the call
+        with _on(stream):
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
     elif scratch.get_device() != device or not scratch.is_contiguous():
         raise FlashLoopError(1, what, f"scratch must be contiguous and on cuda device {device}")
     s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
@@ -607,11 +613,12 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, lens, q_lens=None, scale=None,
     import torch
     what = "flashloop_prefix_attention"
     _need(q.dim() == 4, what, "q must be [B, Tq, H, hd]")
-    if out is None:
-        out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device) if q_lens is not None else torch.empty(
-            q.shape, dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.full(q.shape[:3], -float("inf"), device=q.device)
+    if out is None or lse is None:
+        with _on(stream):
+            if out is None:
+                out = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+            if lse is None:
+                lse = torch.full(q.shape[:3], -float("inf"), device=q.device)
     dev = q.get_device()
 
     def make():
@@ -662,7 +669,8 @@ def column_weights(q, k, lse, acc, lens=None, q_lens=None, scale=None, out=None,
     import torch
     what = "flashloop_column_weights"
     if out is None:
-        out = torch.empty(acc.shape, device=acc.device)
+        with _on(stream):
+            out = torch.empty(acc.shape, device=acc.device)
     dev = q.get_device()
 
     def make():
@@ -744,10 +752,12 @@ def verify_draft(logits, draft_logits, draft, u, n_draft=None, temperature: floa
     import torch
     what = "flashloop_verify_draft"
     _need(logits.dim() == 3 and logits.shape[1] >= 1, what, "logits must be [B, D + 1, V]")
-    if tokens is None:
-        tokens = torch.empty(logits.shape[:2], dtype=torch.int32, device=logits.device)
-    if n_accepted is None:
-        n_accepted = torch.empty(logits.shape[:1], dtype=torch.int32, device=logits.device)
+    if tokens is None or n_accepted is None:
+        with _on(stream):
+            if tokens is None:
+                tokens = torch.empty(logits.shape[:2], dtype=torch.int32, device=logits.device)
+            if n_accepted is None:
+                n_accepted = torch.empty(logits.shape[:1], dtype=torch.int32, device=logits.device)
     if logits.shape[1] == 1:   # nothing drafted: one token is sampled
         draft = draft_logits = None
     dev = logits.get_device()

@@ -419,7 +419,7 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
 /* Attention weight of every key column, added to a running sum:
  *   out[b][g][j] = acc[b][g][j] + sum over queries (t, h in group g) that see j of
  *                  exp(scale * q[b][t][h] . k[b][g][j] - lse[b][t][h])
- * in fp32.  lens NULL: every query sees every column; otherwise query t < q_lens[b]
+ * in fp32.  lens NULL: every query sees every column (q_lens is not read); otherwise query t < q_lens[b]
  * sees j <= lens[b] - q_lens[b] + t, j < lens[b], as in flashloop_prefix_attention, whose lse it takes.
  * A query whose lse is -inf adds nothing.  Columns that no query sees keep acc's
  * value.  (A shared prefix is one sequence, B = 1, of B * Tq queries, lens NULL.)
@@ -491,7 +491,7 @@ fl_status flashloop_evict(const flashloop_evict_args* a, void* scratch, size_t s
  *   logits fp32 [B][D+1][V], draft_logits fp32 [B][D][V]: rows contiguous, 4-byte aligned, strides of b and i;
  *   draft int32 [B][D]; u fp32 [B][D+1] in [0, 1); n_draft int32 [B] or NULL for D;
  *   tokens int32 [B][D+1]; n_accepted int32 [B], all contiguous.
- * Limits: 0 <= D <= 64 (D = 0 samples one token), 1 <= V, temperature >= 0 and finite. */
+ * Limits: 0 <= D <= 64 (D = 0 samples one token), 1 <= V <= 2^30, temperature 0 or finite and >= 1e-20. */
 typedef struct {
   const float* logits;
   const float* draft_logits;

@@ -100,6 +100,40 @@ def test_attention_scales(scale):
                     normal(g, 2, 2, 40, 64), [40, 11], [2, 2], scale=scale)
 
 
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3])
+@pytest.mark.parametrize("hd,B", [(64, 15), (128, 40)])
+def test_attention_scales_many_rows(hd, B, scale):
+    """The same with the prefix on the tensor-core kernel (over 32 rows per KV head), scores growing along the prefix so that
+    the running maximum moves often, and one or two row tiles."""
+    g = gen(31)
+    kp, vp = normal(g, 2, 700, hd), normal(g, 2, 700, hd)
+    kp = (kp.float() * torch.linspace(0.1, 3.0, 700, device="cuda")[None, :, None]).to(torch.bfloat16)
+    check_attention(normal(g, B, 2, 6, hd), kp, vp, normal(g, B, 2, 8, hd), normal(g, B, 2, 8, hd), [8, 3, 2] * (B // 3) +
+                    [5] * (B % 3), None, scale=scale)
+
+
+def test_attention_non_finite_scores_many_rows():
+    """On the tensor-core kernel: a visible NaN key makes the rows NaN, columns of -inf score weigh nothing, a +inf score gives
+    NaN, and no finite score at all 0 and -inf."""
+    g = gen(32)
+    q = normal(g, 24, 1, 8, 64).abs()
+    kp, vp = normal(g, 4, 500, 64), normal(g, 4, 500, 64)
+    kp[0, 130] = NAN
+    kp[1, 5:300] = -INF                  # q > 0: scores -inf, the first two tiles all of them
+    kp[2, 499] = INF
+    kp[3] = -INF
+    out, lse = fl.prefix_attention(q, kp, vp, None, None, None)
+    o = out.float()
+    for h in (0, 1, 4, 5):
+        assert bool(torch.isnan(o[:, 0, h]).all()) and bool(torch.isnan(lse[:, 0, h]).all())
+    assert bool((o[:, 0, 6:] == 0).all()) and bool((lse[:, 0, 6:] == -INF).all())
+    keep = [i for i in range(500) if not 5 <= i < 300]
+    want, wl = fl.prefix_attention(q, kp[:, keep].contiguous(), vp[:, keep].contiguous(), None, None, None)
+    # each side within its bound of 2^-8 of A + |out|, A the mean |v| under the weights (below 5 here)
+    assert bool(((o - want.float())[:, 0, 2:4].abs() <= 2 * 2 ** -8 * 10).all())
+    assert bool(((lse - wl)[:, 0, 2:4].abs() <= 1e-4).all())
+
+
 def test_attention_strided_layouts():
     """Queries inside a wider projection, caches as [B][S][Hkv][hd] and [P][Hkv][hd], a strided output."""
     g = gen(4)
@@ -243,6 +277,20 @@ def test_column_weights_ignore_masked_rows():
         k[b, :, n:] = NAN
     got = fl.column_weights(q, k, lse, acc, lens=lens)
     assert torch.equal(got, want) and bool((got[1, :, 60:] == 0).all())
+
+
+def test_column_weights_nan_lse_reaches_every_column_it_weighs():
+    """A query whose lse is NaN makes the columns it sees NaN, and no other: few rows and many."""
+    for Tq in (3, 40):
+        g = gen(13)
+        q, k = normal(g, 1, Tq, 4, 64), normal(g, 1, 2, 100, 64)
+        lse = torch.full((1, Tq, 4), 5.0, device="cuda")
+        lse[0, 1, 2] = NAN                       # KV head 1; sees columns 0 .. 100 - Tq + 1
+        lse[0, 0, 0] = -INF
+        out = fl.column_weights(q, k, lse, torch.zeros((1, 2, 100), device="cuda"), lens=ints([100]))
+        seen = 100 - Tq + 2
+        assert bool(torch.isfinite(out[0, 0]).all())
+        assert bool(torch.isnan(out[0, 1, :seen]).all()) and bool(torch.isfinite(out[0, 1, seen:]).all())
 
 
 def test_column_weights_sum_to_the_queries():

@@ -70,7 +70,7 @@ BAD = {
         dict(k_stride=fl._I3(12800, 6400, 0)), dict(acc_stride=fl._I2(0, 50)),
         dict(k_out=PTR, v_out=PTR * 2, acc_out=PTR * 3, pos_out=PTR * 4, lens_out=PTR * 5)]),
     "verify_draft": (verify, [
-        dict(B=0), dict(D=-1), dict(D=65), dict(V=0), dict(temperature=-0.5), dict(temperature=NAN),
+        dict(B=0), dict(D=-1), dict(D=65), dict(V=0), dict(temperature=-0.5), dict(temperature=1e-30), dict(temperature=NAN),
         dict(temperature=INF), dict(logits=None), dict(draft=None), dict(u=None), dict(tokens=None),
         dict(n_accepted=PTR + 2), dict(logits=PTR + 1), dict(logits_stride=fl._I2(-400, 100)),
         dict(draft_logits_stride=fl._I2(300, 0))]),
