@@ -19,7 +19,8 @@ namespace fl {
 namespace {
 
 constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
-constexpr int kEvCopies = 8;              // histograms a CTA's lanes share
+constexpr int kEvDigit = 11, kEvBins = 1 << kEvDigit;   // bits of a digit (the last has 10): four bins a thread
+constexpr int kEvHeld = 16;               // slots a thread holds the positions of
 constexpr int kEvCluster = 16;            // CTAs of one (sequence, KV head) at most (over 8: non-portable)
 constexpr int kEvKeys = 32 * kEvThreads;  // keys one CTA holds in shared memory (64 KB), a word of 32 slots per thread
 constexpr int kEvSlots = kEvCluster * kEvKeys;
@@ -29,8 +30,6 @@ struct EvictArgs {
   int cap;              // min(keep, S): slots of a segment's map
   int chunk;            // slots per CTA of the selection
   int32_t* src;         // [B * Hkv][cap] source slot of each destination slot
-  int32_t* from;        // [B * Hkv][cap] kept slots >= keep, ascending
-  int32_t* to;          // [B * Hkv][cap] freed slots < keep, ascending
   int32_t* n_kept;      // [B * Hkv]
 };
 
@@ -50,48 +49,73 @@ __device__ __forceinline__ void scan_warps(int* v, int* total) {
 // ============================================================================
 // Selection: a cluster of 1-16 CTAs per (sequence, KV head), each with a contiguous
 // chunk of slots, its keys in shared memory.  Key: 0xFFFFFFFF when protected, else the
-// weight's bits (at most 0xFFFFFFFE).  Four 8-bit digits, largest first: every
+// weight's bits (at most 0xFFFFFFFE).  Three digits of 11, 11 and 10 bits, largest first
+// (weights share their leading bits, so wide digits part more of them): every
 // CTA histograms the keys that match the digits found so far, and after a
-// cluster barrier reads all CTAs' histograms over distributed shared memory and
-// finds the next digit by itself.  Latency-bound (a round trip to memory, then
+// cluster barrier sums all CTAs' histograms over distributed shared memory and
+// finds the next digit by itself.  The freed slots' list stays in shared memory, where
+// the CTAs look up where their kept slots go.  Latency-bound (a round trip to memory, then
 // about ten barriers).
 // ============================================================================
-__global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) {
+__global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const EvictArgs a) {
+  pdl_trigger();   // the move is launched, and waits for the result, while this runs
   cg::cluster_group cl = cg::this_cluster();
-  extern __shared__ uint32_t keys[];        // [chunk]
-  __shared__ int lane_hist[kEvCopies * 257]; // counters of lanes l, l + 8, ..: keys of one magnitude share their
-                                            // leading digits, and adds to one address go one after the other
-  __shared__ int hist[2][256];              // this CTA's, one per digit parity: a cluster barrier per digit suffices
-  __shared__ int tot[256];
-  __shared__ int newest_sm, sel_digit, sel_before, sel_count;
+  extern __shared__ uint32_t keys[];        // [chunk]; in the end the freed and the moving slots' lists
+  __shared__ __align__(16) int hist[2][kEvBins];   // this CTA's, one per digit parity: a cluster barrier per digit suffices
+  __shared__ int group[2][32];              // its sums of 64 bins
+  __shared__ int newest_sm, sel_digit, sel_before, sel_count, move_base;
   __shared__ int warp_a[kEvWarps];
   __shared__ int cta_eq, cta_both;
   __shared__ uint32_t kept_w[kEvThreads];   // kept slots, a bit each: word t is thread t's
-  __shared__ int hole_at[kEvThreads], move_at[kEvThreads];
+  __shared__ int list_at[kEvThreads];       // before a word: freed slots (low half) and moving ones of this CTA
+  __shared__ int hole_base[kEvCluster + 1]; // freed slots before each CTA's, and all of them
   const flashloop_evict_args& c = a.c;
   const int nc = cl.num_blocks(), rank = cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = blockIdx.y, b = blockIdx.z;
   const long long seg = static_cast<long long>(b) * c.Hkv + g;
-  const int n = min(max(c.lens[b], 0), c.S);
+  const int len = c.lens[b];
+  // ---- weights and positions (requested before the length is known: the slots are there, used or not)
+  const int lo = min(c.S, rank * a.chunk), cap = min(c.S, lo + a.chunk) - lo;
+  const float* acc = c.acc + b * c.acc_stride[0] + g * c.acc_stride[1] + lo;
+  const int32_t* pos = c.pos + b * c.pos_stride[0] + g * c.pos_stride[1] + lo;
+  int held[kEvHeld];
+  {
+    float w[kEvHeld];
+#pragma unroll
+    for (int j = 0; j < kEvHeld; ++j) {
+      const int i = tid + j * kEvThreads;
+      if (i < cap) {
+        w[j] = acc[i];
+        held[j] = pos[i];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kEvHeld; ++j) {
+      const int i = tid + j * kEvThreads;
+      if (i < cap) keys[i] = min(__float_as_uint(w[j]), 0xFFFFFFFEu);
+    }
+  }
+  const int n = min(max(len, 0), c.S), m = max(0, min(n - lo, cap));
   int32_t* src = a.src + seg * a.cap;
   if (rank == 0 && tid == 0) a.n_kept[seg] = min(n, c.keep);
   if (n <= c.keep) {   // the whole cluster alike
     for (int i = rank * kEvThreads + tid; i < n; i += nc * kEvThreads) src[i] = i;
     return;
   }
-  const int lo = min(n, rank * a.chunk), hi = min(n, lo + a.chunk), m = hi - lo;
-  const float* acc = c.acc + b * c.acc_stride[0] + g * c.acc_stride[1] + lo;
-  const int32_t* pos = c.pos + b * c.pos_stride[0] + g * c.pos_stride[1] + lo;
   // ---- the newest token
-  if (tid == 0) newest_sm = INT_MIN;
-  __syncthreads();
   int newest = INT_MIN;
-#pragma unroll 4
-  for (int i = tid; i < m; i += kEvThreads) {
+#pragma unroll
+  for (int j = 0; j < kEvHeld; ++j)
+    if (tid + j * kEvThreads < m) newest = max(newest, held[j]);
+  for (int i = tid + kEvHeld * kEvThreads; i < m; i += kEvThreads) {
     keys[i] = min(__float_as_uint(acc[i]), 0xFFFFFFFEu);
     newest = max(newest, pos[i]);
   }
+  if (tid == 0) newest_sm = INT_MIN;
+  *reinterpret_cast<int4*>(&hist[0][4 * tid]) = make_int4(0, 0, 0, 0);
+  *reinterpret_cast<int4*>(&hist[1][4 * tid]) = make_int4(0, 0, 0, 0);
+  __syncthreads();
   newest = __reduce_max_sync(0xffffffffu, newest);
   if (lane == 0) atomicMax(&newest_sm, newest);
   auto sync_all = [&]() {   // the cluster, or its one CTA
@@ -99,81 +123,99 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
     else __syncthreads();
   };
   sync_all();
-  for (int r = 0; r < nc; ++r) newest = max(newest, *cl.map_shared_rank(&newest_sm, r));
+  newest = __reduce_max_sync(0xffffffffu, lane < nc ? *cl.map_shared_rank(&newest_sm, lane) : INT_MIN);
   const long long oldest_safe = static_cast<long long>(newest) - c.recent;   // protected above it
-  // ---- keys, and the digits of the keep-th one
-  for (int i = tid; i < kEvCopies * 257; i += kEvThreads) lane_hist[i] = 0;
-#pragma unroll 4
-  for (int i = tid; i < m; i += kEvThreads) {
-    const int p = pos[i];
-    if (p < c.sinks || p > oldest_safe) keys[i] = 0xFFFFFFFFu;
-  }
-  __syncthreads();
+  auto scan_warp = [&](int v) {   // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    return v;
+  };
+  auto scan_block = [&](int v, int* total) {   // exclusive prefix sum over the threads (two barriers)
+    const int incl = scan_warp(v);
+    if (lane == 31) warp_a[warp] = incl;
+    __syncthreads();
+    if (warp == 0) scan_warps(warp_a, total);
+    __syncthreads();
+    return warp_a[warp] + incl - v;
+  };
+  // ---- the digits of the keep-th key
   uint32_t prefix = 0, mask = 0;
   int k_rem = c.keep;      // keys still to keep among those that match the digits so far
   bool ties = true;        // more keys than that match
 #pragma unroll 1
-  for (int d = 0; d < 4 && ties; ++d) {
-    const int shift = 24 - 8 * d;
+  for (int d = 0; d < 3 && ties; ++d) {
+    const int shift = d == 2 ? 0 : 32 - kEvDigit * (d + 1);
+    const uint32_t digit = d == 2 ? (1u << (32 - 2 * kEvDigit)) - 1u : kEvBins - 1u;
     int* h = hist[d & 1];
-#pragma unroll 4
-    for (int i = tid; i < m; i += kEvThreads) {
-      const uint32_t u = keys[i];
-      if ((u & mask) == prefix) atomicAdd(&lane_hist[(lane % kEvCopies) * 257 + ((u >> shift) & 0xFF)], 1);
-    }
-    __syncthreads();
-    if (tid < 256) {
-      int s = 0;
+    if (d == 0) {   // every key: the protected ones are found, and odd lanes count apart
+      int* const hl = hist[lane & 1];
+      auto count = [&](int i, int p) {
+        uint32_t u = 0xFFFFFFFFu;
+        if (p < c.sinks || p > oldest_safe) keys[i] = u;
+        else u = keys[i];
+        atomicAdd(&hl[u >> (32 - kEvDigit)], 1);
+      };
 #pragma unroll
-      for (int l = 0; l < kEvCopies; ++l) s += lane_hist[l * 257 + tid];
-      h[tid] = s;
-    }
-    if (nc > 1) {
-      cl.sync();
-      if (tid < 256) {
-        int s = 0;
-        for (int r = 0; r < nc; ++r) s += cl.map_shared_rank(h, r)[tid];
-        tot[tid] = s;
-      }
-    }
-    __syncthreads();
-    if (warp != 0) {   // meanwhile: the next digit's counters
-      for (int i = tid - 32; i < kEvCopies * 257; i += kEvThreads - 32) lane_hist[i] = 0;
+      for (int j = 0; j < kEvHeld; ++j)
+        if (tid + j * kEvThreads < m) count(tid + j * kEvThreads, held[j]);
+      for (int i = tid + kEvHeld * kEvThreads; i < m; i += kEvThreads) count(i, pos[i]);
     } else {
-      const int* t = nc > 1 ? tot : h;
-      int cnt[8], mine = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        cnt[e] = t[255 - 8 * lane - e];
-        mine += cnt[e];
+#pragma unroll 8
+      for (int i = tid; i < m; i += kEvThreads) {
+        const uint32_t u = keys[i];
+        if ((u & mask) == prefix) atomicAdd(&h[u >> shift & digit], 1);
       }
-      int incl = mine;
+    }
+    __syncthreads();
+    // sums of 64 bins first: the crossing one's bins are all that is read of the others' histograms
+    int4 x = *reinterpret_cast<int4*>(&h[4 * tid]);
+    if (d == 0) {
+      const int4 y = *reinterpret_cast<int4*>(&hist[1][4 * tid]);
+      x = make_int4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+      *reinterpret_cast<int4*>(&h[4 * tid]) = x;
+    }
+    int sum = x.x + x.y + x.z + x.w;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((lane & 15) == 0) group[d & 1][tid >> 4] = sum;
+    sync_all();
+    // the next digit's counters: no other CTA reads them any more (it passed this digit's barrier)
+    *reinterpret_cast<int4*>(&hist[(d & 1) ^ 1][4 * tid]) = make_int4(0, 0, 0, 0);
+    if (warp == 0) {
+      int cnt = 0;   // of a lane's group, the largest digits first
+#pragma unroll 8
+      for (int r = 0; r < nc; ++r) cnt += cl.map_shared_rank(group[d & 1], r)[31 - lane];
+      int at = __ffs(__ballot_sync(0xffffffffu, scan_warp(cnt) >= k_rem)) - 1;
+      const int above = __shfl_sync(0xffffffffu, scan_warp(cnt) - cnt, at);
+      const int top = 64 * (31 - at) + 62 - 2 * lane;   // a lane's two bins are top and top + 1
+      int2 two = make_int2(0, 0);
+#pragma unroll 8
+      for (int r = 0; r < nc; ++r) {
+        const int2 y = *reinterpret_cast<const int2*>(cl.map_shared_rank(h, r) + top);
+        two = make_int2(two.x + y.x, two.y + y.y);
       }
-      int before = incl - mine;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (before < k_rem && before + cnt[e] >= k_rem) {
-          sel_digit = 255 - 8 * lane - e;
-          sel_before = before;
-          sel_count = cnt[e];
-        }
-        before += cnt[e];
+      const int incl = above + scan_warp(two.x + two.y), mid = incl - two.x, low = mid - two.y;
+      if (low < k_rem && incl >= k_rem) {
+        const bool upper = mid >= k_rem;
+        sel_digit = top + upper;
+        sel_before = upper ? low : mid;
+        sel_count = upper ? two.y : two.x;
       }
     }
     __syncthreads();
     k_rem -= sel_before;
     prefix |= static_cast<uint32_t>(sel_digit) << shift;
-    mask |= 0xFFu << shift;
+    mask |= digit << shift;
     ties = sel_count > k_rem;   // else every key with these digits is kept: the threshold is found
   }
   // ---- kept: every key from the threshold on or, when keys equal to it are left out, those above it
   // and the k_rem lowest slots equal to it.  32 slots to a word, a word to a thread.
   const unsigned below = (1u << lane) - 1u;
   const int words = (m + 31) / 32;
+#pragma unroll 4
   for (int w = warp; w < words; w += kEvWarps) {
     const int i = w * 32 + lane;
     const uint32_t u = i < m ? keys[i] : 0u;
@@ -181,28 +223,15 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
     const unsigned e = ties ? __ballot_sync(0xffffffffu, i < m && u == prefix) : 0u;
     if (lane == 0) {
       kept_w[w] = k;
-      hole_at[w] = static_cast<int>(e);
+      list_at[w] = static_cast<int>(e);
     }
   }
   __syncthreads();
-  auto scan_block = [&](int v, int* warps, int* total) {   // exclusive prefix sum over the threads (two barriers)
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) warps[warp] = incl;
-    __syncthreads();
-    if (warp == 0) scan_warps(warps, total);
-    __syncthreads();
-    return warps[warp] + incl - v;
-  };
   if (ties) {   // (the cluster alike)
-    uint32_t e = tid < words ? static_cast<uint32_t>(hole_at[tid]) : 0u;
-    int seen = scan_block(__popc(e), warp_a, &cta_eq);
+    uint32_t e = tid < words ? static_cast<uint32_t>(list_at[tid]) : 0u;
+    int seen = scan_block(__popc(e), &cta_eq);
     sync_all();
-    for (int r = 0; r < rank; ++r) seen += *cl.map_shared_rank(&cta_eq, r);
+    seen += __reduce_add_sync(0xffffffffu, lane < rank ? *cl.map_shared_rank(&cta_eq, lane) : 0);
     for (; e && seen < k_rem; e &= e - 1, ++seen) kept_w[tid] |= e & (0u - e);
     __syncthreads();
   }
@@ -211,37 +240,44 @@ __global__ void __launch_bounds__(kEvThreads) k_evict_select(const EvictArgs a) 
   const uint32_t low = n_low >= 32 ? 0xFFFFFFFFu : (1u << n_low) - 1u;
   const uint32_t there = m - s0 >= 32 ? 0xFFFFFFFFu : (m - s0 > 0 ? (1u << (m - s0)) - 1u : 0u);
   // holes in the low half, moves in the high one: at most kEvKeys = 2^14 of each in a CTA
-  const uint32_t both = static_cast<uint32_t>(
-      scan_block(__popc(~kw & low & there) | __popc(kw & ~low) << 16, warp_a, &cta_both));
-  int h0 = both & 0xFFFF, m0 = both >> 16;
-  sync_all();
-  int all = 0;
-  for (int r = 0; r < nc; ++r) {
-    const uint32_t x = static_cast<uint32_t>(*cl.map_shared_rank(&cta_both, r));
-    if (r < rank) {
-      h0 += x & 0xFFFF;
-      m0 += x >> 16;
-    }
-    all += x & 0xFFFF;
-  }
-  if (tid < words) {
-    hole_at[tid] = h0;
-    move_at[tid] = m0;
-  }
+  const int both = scan_block(__popc(~kw & low & there) | __popc(kw & ~low) << 16, &cta_both);
+  list_at[tid] = both;
   __syncthreads();
+  uint16_t* holes = reinterpret_cast<uint16_t*>(keys);   // [chunk] each, of this CTA's slots; the keys are done with
+  uint16_t* moves = holes + a.chunk;
+#pragma unroll 4
   for (int w = warp; w < words; w += kEvWarps) {
-    const int i = w * 32 + lane, slot = lo + i;
+    const int i = w * 32 + lane, slot = lo + i, at = list_at[w];
     const uint32_t k = kept_w[w];
     const bool kept = k >> lane & 1u, is_low = slot < c.keep;
     const unsigned lowb = __ballot_sync(0xffffffffu, is_low), hb = __ballot_sync(0xffffffffu, i < m && is_low && !kept);
-    if (kept && is_low) src[slot] = slot;
-    if (hb >> lane & 1u) a.to[seg * a.cap + hole_at[w] + __popc(hb & below)] = slot;
-    if (kept && !is_low) a.from[seg * a.cap + move_at[w] + __popc(k & ~lowb & below)] = slot;
+    if (hb >> lane & 1u) holes[(at & 0xFFFF) + __popc(hb & below)] = static_cast<uint16_t>(i);
+    if (kept && !is_low) moves[(at >> 16) + __popc(k & ~lowb & below)] = static_cast<uint16_t>(i);
   }
-  if (nc > 1) __threadfence();
-  sync_all();   // every CTA's lists are written (and nobody reads another's shared memory any more)
-  for (int i = rank * kEvThreads + tid; i < all; i += nc * kEvThreads)
-    src[__ldcg(&a.to[seg * a.cap + i])] = __ldcg(&a.from[seg * a.cap + i]);
+  sync_all();   // every CTA's lists and counts are written (and nothing else yet: a barrier waits for its CTA's stores)
+  for (int w = warp; w < words; w += kEvWarps) {
+    const int slot = lo + w * 32 + lane;
+    if ((kept_w[w] >> lane & 1u) && slot < c.keep) src[slot] = slot;
+  }
+  if (warp == 0) {
+    const int x = lane < nc ? *cl.map_shared_rank(&cta_both, lane) : 0;
+    const int ih = scan_warp(x & 0xFFFF), im = scan_warp(x >> 16);
+    if (lane < nc) hole_base[lane + 1] = ih;
+    if (lane == 0) hole_base[0] = 0;
+    if (lane == rank) move_base = im - (x >> 16);
+  }
+  __syncthreads();
+  // ---- the i-th moving slot takes the i-th freed one (as many of the ones as of the others)
+  const int n_moves = cta_both >> 16;
+  int r = 0;
+#pragma unroll 2
+  for (int i = tid; i < n_moves; i += kEvThreads) {
+    const int x = move_base + i;
+    while (r + 1 < nc && x >= hole_base[r + 1]) ++r;
+    src[r * a.chunk + cl.map_shared_rank(holes, r)[x - hole_base[r]]] = lo + moves[i];
+  }
+  if (nc > 1)   // nobody reads another's shared memory any more
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // ============================================================================
@@ -306,7 +342,7 @@ bool evict_shape_ok(int B, int Hkv, int S, int keep) {
 }
 size_t evict_bytes(int B, int Hkv, int S, int keep) {
   const size_t seg = static_cast<size_t>(B) * Hkv, cap = std::min(keep, S);
-  return 3 * align256_sz(seg * cap * 4) + align256_sz(seg * 4) + 256;
+  return align256_sz(seg * cap * 4) + align256_sz(seg * 4) + 256;
 }
 
 }  // namespace
@@ -368,9 +404,7 @@ fl_status flashloop_evict(const flashloop_evict_args* c, void* scratch, size_t s
   const size_t seg = static_cast<size_t>(c->B) * c->Hkv, list = align256_sz(seg * a.cap * 4);
   uint8_t* ws = static_cast<uint8_t*>(scratch);
   a.src = reinterpret_cast<int32_t*>(ws);
-  a.from = reinterpret_cast<int32_t*>(ws + list);
-  a.to = reinterpret_cast<int32_t*>(ws + 2 * list);
-  a.n_kept = reinterpret_cast<int32_t*>(ws + 3 * list);
+  a.n_kept = reinterpret_cast<int32_t*>(ws + list);
   // CTAs per segment: chunks of at most 8192 slots (8 per thread and pass) while the cluster allows
   int nc = 1;
   while ((nc < 8 && c->S > nc * 8192) || c->S > nc * kEvKeys) nc *= 2;
