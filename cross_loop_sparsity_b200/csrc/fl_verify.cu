@@ -1,10 +1,10 @@
 // fl_verify.cu -- verification of drafted tokens against the target's
 // probabilities, from given random numbers.
 //
-// Three launches (two when greedy).  The first reads every row of logits once and leaves, per
+// Two launches.  The first reads every row of logits once and leaves, per
 // chunk, the maximum, where it is, and the sum of exponentials relative to it.  The second
-// decides the accepted drafts and forms again, in 64 bits, the sums of the one row that
-// decides the last token; the third finds the token.  64 bits because a token
+// decides the accepted drafts, forms again, in 64 bits, the sums of the one row that
+// decides the last token, and finds the token.  64 bits because a token
 // is the index where a running sum crosses u times its total: with V tokens between 0 and
 // 1 that index is only well defined when the sum is known far better than 1 / V.
 #include <algorithm>
@@ -29,8 +29,9 @@ struct VerifyArgs {
   flashloop_verify_args c;
   int n_chunks;
   double scale2;   // log2(e) / temperature
+  float reach;     // logits further than this below the maximum, 2^-1000 of it, count as nothing
   RowPart* part;   // [B][2D + 1][n_chunks]: target rows, then draft rows
-  struct Deciding* deciding;   // [B]
+  unsigned* done;              // [B] finished CTAs of the second launch
   struct Sums* sums;           // [B][n_sub] of the deciding row's token ranges
   int n_sub, sub_len;
   unsigned* tickets;           // [B][D] finished chunks of a draft's rows, minus one (EARLY)
@@ -112,22 +113,28 @@ struct Norms {
   double zp[kMaxDraft + 1], zq[kMaxDraft + 1];
 };
 
-// Verdict on draft i from the 32-bit sums: 0 rejected, 1 accepted, 2 too near to say (closer than 1e-4 of p;
-// the sums and exponentials are good to about 1e-6).  One warp; the rows' norms too.
-__device__ __forceinline__ int judge_one(const VerifyArgs& a, int b, int i, float& mp, double& zp, float& mq, double& zq) {
+// Verdict on a draft from the 32-bit sums: 0 rejected, 1 accepted, 2 too near to say (closer than 1e-4 of p;
+// the sums and exponentials are good to about 1e-6).  u q < p without the divisions: u e_q Z_p < e_p Z_q.
+__device__ __forceinline__ int verdict_on(const VerifyArgs& a, int x, double u, float xp, float mp, double zp, float xq, float mq,
+                                          double zq) {
+  if (x < 0 || x >= a.c.V) return 0;
+  const double ep = exp2((static_cast<double>(xp) - mp) * a.scale2);
+  const double eq = a.c.draft_logits ? exp2((static_cast<double>(xq) - mq) * a.scale2) : 1.0;
+  const double l = u * eq * zp, r = ep * zq;
+  return isfinite(r) && fabs(l - r) <= 1e-4 * r ? 2 : (l < r ? 1 : 0);
+}
+// ... on draft i (one warp)
+__device__ __forceinline__ int judge_one(const VerifyArgs& a, int b, int i) {
   const flashloop_verify_args& c = a.c;
   const int x = c.draft[static_cast<size_t>(b) * c.D + i];
   const bool in = x >= 0 && x < c.V;
-  const double xp = in ? row_of(a, b, i)[x] : 0.0;
-  const double xq = in && c.draft_logits ? row_of(a, b, c.D + 1 + i)[x] : 0.0;
-  const double u = c.u[static_cast<size_t>(b) * (c.D + 1) + i];
+  const float xp = in ? row_of(a, b, i)[x] : 0.f, xq = in && c.draft_logits ? row_of(a, b, c.D + 1 + i)[x] : 0.f;
+  const float u = c.u[static_cast<size_t>(b) * (c.D + 1) + i];
+  float mp, mq = 0.f;
+  double zp, zq = 1.0;
   row_norm(a, b, i, mp, zp);
-  mq = 0.f;
-  zq = 1.0;
   if (c.draft_logits) row_norm(a, b, c.D + 1 + i, mq, zq);
-  const double p = in ? exp2((xp - mp) * a.scale2) / zp : 0.0;
-  const double q = c.draft_logits ? exp2((xq - mq) * a.scale2) / zq : 1.0;
-  return in && fabs(u * q - p) <= 1e-4 * p ? 2 : (in && u * q < p ? 1 : 0);
+  return verdict_on(a, x, u, xp, mp, zp, xq, mq, zq);
 }
 
 // ============================================================================
@@ -149,6 +156,7 @@ __global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) 
   const int chunk = blockIdx.x, b = blockIdx.y, i = pairs ? blockIdx.z >> 1 : blockIdx.z;   // position i
   const int r = pairs && (blockIdx.z & 1) ? c.D + 1 + i : i;
   const int n = drafts_of(a, b);
+  if (r == 0 && chunk == 0 && threadIdx.x == 0) a.done[b] = 0;   // (row 0 is always read)
   if (r <= c.D ? r > n : i >= n) return;   // rows of drafts that were not made
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (EARLY) {
@@ -224,46 +232,60 @@ __global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) 
     __syncthreads();
     if (!last || warp != 0) return;
     __threadfence();
-    float mp, mq;
-    double zp, zq;
-    if (judge_one(a, b, i, mp, zp, mq, zq) == 0 && lane == 0) atomicMin(&a.dead[b], static_cast<unsigned>(i));
+    if (judge_one(a, b, i) == 0 && lane == 0) atomicMin(&a.dead[b], static_cast<unsigned>(i));
   }
 }
 
-// Verdicts of drafts [first, n), and the norms of their rows and of target row n.  Whole block.  (Rows behind a sure
-// rejection may not have been summed: what is made of them is not looked at.)
-__device__ void judge(const VerifyArgs& a, int b, int first, int n, int* verdict, Norms* norms) {
+// What the verdicts need of the inputs, read while the first launch still runs.
+struct Ahead {
+  int x[kMaxDraft];
+  float xp[kMaxDraft], xq[kMaxDraft], u[kMaxDraft + 1];
+};
+__device__ __forceinline__ void look_ahead(const VerifyArgs& a, int b, int n, Ahead* h) {
+  const flashloop_verify_args& c = a.c;
+  const int i = threadIdx.x;
+  if (i <= c.D) h->u[i] = c.u[static_cast<size_t>(b) * (c.D + 1) + i];
+  if (i >= n) return;
+  const int x = c.draft[static_cast<size_t>(b) * c.D + i];
+  const bool in = x >= 0 && x < c.V;
+  h->x[i] = x;
+  h->xp[i] = in ? row_of(a, b, i)[x] : 0.f;
+  h->xq[i] = in && c.draft_logits ? row_of(a, b, c.D + 1 + i)[x] : 0.f;
+}
+
+// Norms of target rows [first, n] and draft rows [first, n), a warp each, then the drafts' verdicts, a thread
+// each.  Whole block.  (Rows behind a sure rejection may not have been summed: what is made of them is not looked at.)
+__device__ void judge(const VerifyArgs& a, int b, int first, int n, const Ahead& h, int* verdict, Norms* norms) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  for (int i = first + warp; i <= n; i += nw) {
-    float mp, mq = 0.f;
-    double zp, zq = 0.0;
-    int v = 0;
-    if (i < n)
-      v = judge_one(a, b, i, mp, zp, mq, zq);
-    else
-      row_norm(a, b, i, mp, zp);
+  const bool pairs = a.c.draft_logits != nullptr;
+  const int targets = n - first + 1;
+  for (int k = warp; k < targets + (pairs ? targets - 1 : 0); k += nw) {
+    float m;
+    double z;
+    const int i = first + (k < targets ? k : k - targets);
+    row_norm(a, b, k < targets ? i : a.c.D + 1 + i, m, z);
     if (lane == 0) {
-      if (i < n) verdict[i] = v;
-      norms->mp[i] = mp;
-      norms->mq[i] = mq;
-      norms->zp[i] = zp;
-      norms->zq[i] = zq;
+      (k < targets ? norms->mp : norms->mq)[i] = m;
+      (k < targets ? norms->zp : norms->zq)[i] = z;
     }
   }
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i >= first && i < n)
+    verdict[i] = verdict_on(a, h.x[i], h.u[i], h.xp[i], norms->mp[i], norms->zp[i], h.xq[i], pairs ? norms->mq[i] : 0.f,
+                            pairs ? norms->zq[i] : 1.0);
   __syncthreads();
 }
 
 // The deciding row when drafts [0, row) are accepted (thread 0 fills *d; then a block barrier).
-__device__ void describe(const VerifyArgs& a, int b, int row, int n, const Norms& norms, const int* verdict, Deciding* d) {
-  const flashloop_verify_args& c = a.c;
+__device__ void describe(const VerifyArgs& a, int row, int n, const Ahead& h, const Norms& norms, const int* verdict, Deciding* d) {
   if (threadIdx.x == 0) {
-    const bool residual = row < n, with_draft = residual && c.draft_logits;
-    const float mp = norms.mp[row], mq = norms.mq[row];
-    const double zp = norms.zp[row], zq = norms.zq[row];
-    const float reach = static_cast<float>(1000.0 / a.scale2);
+    const bool residual = row < n, with_draft = residual && a.c.draft_logits;
+    const float mp = norms.mp[row], mq = with_draft ? norms.mq[row] : 0.f, reach = a.reach;
+    const double zp = norms.zp[row], zq = with_draft ? norms.zq[row] : 1.0;
     const bool fine = isfinite(zp) && zp > 0.0 && (!with_draft || (isfinite(zq) && zq > 0.0));
     *d = Deciding{row, residual && verdict[row] == 2, with_draft,
-                  residual && !with_draft ? c.draft[static_cast<size_t>(b) * c.D + row] : -1, fine, mp - reach, mq - reach,
+                  residual && !with_draft ? h.x[row] : -1, fine, mp - reach, mq - reach,
                   -64.0 * a.scale2 * mp, -64.0 * a.scale2 * mq, zq / zp};
   }
   __syncthreads();
@@ -345,53 +367,23 @@ __device__ __forceinline__ Sums range_sums(const VerifyArgs& a, int b, const Dec
   return d.with_draft ? range_sums_of<true>(a, b, d, j0, j1, table) : range_sums_of<false>(a, b, d, j0, j1, table);
 }
 
-// ============================================================================
-// Second launch: every CTA finds its sequence's deciding row from the first
-// launch's sums, then each of its warps forms the 64-bit sums of a contiguous
-// range of that row's tokens, two exponentials a token, once.  Bound by the 64-bit pipe
-// (about 11 operations per exponential) for many sequences, by the latency of
-// finding the row for few.
-// ============================================================================
-__global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs a) {
-  __shared__ double table[kExpTable];
-  __shared__ int verdict[kMaxDraft];
-  __shared__ Norms norms;
-  __shared__ Deciding d;
-  pdl_trigger();
-  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < kExpTable) table[threadIdx.x] = exp2(threadIdx.x * (1.0 / kExpTable));
-  const int n = drafts_of(a, b);
-  pdl_wait();
-  judge(a, b, 0, n, verdict, &norms);
-  int row = 0;
-  while (row < n && verdict[row] == 1) ++row;
-  describe(a, b, row, n, norms, verdict, &d);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.deciding[b] = d;
-  const int sub = blockIdx.x * kSumWarps + warp;
-  const int j0 = min(a.c.V, sub * a.sub_len), j1 = min(a.c.V, j0 + a.sub_len);
-  const Sums s = range_sums(a, b, d, j0, j1, table);
-  if (lane == 0) a.sums[static_cast<size_t>(b) * a.n_sub + sub] = s;
-}
-
-// ============================================================================
-// Third launch, one CTA per sequence: totals of the ranges' sums, the range that holds
-// the crossing, and the crossing token in it.  A near decision is settled by the
-// 64-bit totals of its row; when it turns out accepted, this CTA goes on to the next rows by
-// itself (about one call in ten thousand per draft).
-// ============================================================================
-__device__ double block_sum_f64(double v, double* buf /*[8]*/) {
+// both sums over the block
+__device__ double2 block_sums_f64(double x, double y, double2* buf /*[kSumWarps]*/) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_double2(x, y);
   __syncthreads();
-  double t = 0.0;
+  double2 t = make_double2(0.0, 0.0);
 #pragma unroll
-  for (int w = 0; w < kSumWarps; ++w) t += buf[w];
+  for (int w = 0; w < kSumWarps; ++w) t = make_double2(t.x + buf[w].x, t.y + buf[w].y);
   return t;
 }
-// exclusive prefix sum over the block's threads, in thread order
-__device__ double block_scan_f64(double v, double* buf /*[8]*/) {
+// exclusive prefix sum over the block's threads, in thread order, and the sum of all
+__device__ double block_scan_f64(double v, double2* buf, double& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double incl = v;
 #pragma unroll
@@ -400,50 +392,88 @@ __device__ double block_scan_f64(double v, double* buf /*[8]*/) {
     if (lane >= o) incl += y;
   }
   __syncthreads();
-  if (lane == 31) buf[warp] = incl;
+  if (lane == 31) buf[warp].x = incl;
   __syncthreads();
   double base = 0.0;
-  for (int w = 0; w < warp; ++w) base += buf[w];
+  total = 0.0;
+#pragma unroll
+  for (int w = 0; w < kSumWarps; ++w) {
+    if (w == warp) base = total;
+    total += buf[w].x;
+  }
   const double excl = __shfl_up_sync(0xffffffffu, incl, 1);
   return base + (lane ? excl : 0.0);
 }
 
-__global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a) {
-  __shared__ double table[kExpTable], buf[kSumWarps];
+// ============================================================================
+// Second launch: every CTA finds its sequence's deciding row from the first
+// launch's sums, then each of its warps forms the 64-bit sums of a contiguous
+// range of that row's tokens, two exponentials a token, once.  Bound by the 64-bit pipe
+// (about 11 operations per exponential) for many sequences, by the latency of
+// finding the row for few.
+//   The CTA that finishes a sequence's last ranges picks its token: totals of the
+// ranges' sums, the range that holds the crossing, and the crossing token in it.  A near
+// decision is settled by the 64-bit totals of its row; when it turns out accepted, this CTA
+// goes on to the next rows by itself (about one call in ten thousand per draft).
+// ============================================================================
+__global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs a) {
+  __shared__ double table[kExpTable], start_of[kSumThreads];
+  __shared__ double2 buf[kSumWarps];
+  __shared__ Ahead ahead;
   __shared__ int verdict[kMaxDraft];
   __shared__ Norms norms;
   __shared__ Deciding d;
-  __shared__ int cross, last;
-  __shared__ double cross_start;
+  __shared__ int last, cross[2], top[2];
   const flashloop_verify_args& c = a.c;
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < kExpTable) table[tid] = exp2(tid * (1.0 / kExpTable));
   const int n = drafts_of(a, b), D = c.D;
-  const int32_t* draft = c.draft + static_cast<size_t>(b) * D;
   int32_t* tokens = c.tokens + static_cast<size_t>(b) * (D + 1);
+  look_ahead(a, b, n, &ahead);
+  if (tid < 2) cross[tid] = INT_MAX, top[tid] = -1;
   Sums* sums = a.sums + static_cast<size_t>(b) * a.n_sub;
   pdl_wait();
-  if (tid == 0) d = a.deciding[b];
+  judge(a, b, 0, n, ahead, verdict, &norms);
+  {
+    int row = 0;
+    while (row < n && verdict[row] == 1) ++row;
+    describe(a, row, n, ahead, norms, verdict, &d);
+    const int sub = blockIdx.x * kSumWarps + warp;
+    const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
+    const Sums s = range_sums(a, b, d, j0, j1, table);
+    if (lane == 0) sums[sub] = s;
+  }
   __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    last = atomicAdd(&a.done[b], 1u) + 1u == gridDim.x;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!last) return;
   const double s64 = 64.0 * a.scale2;
   auto prob = [&](float x, float lo, double offset) { return exp64_from(x, lo, s64, offset, table); };
   Sums s{0.0, 0.0, 0.0, 0.0};   // n_sub <= threads: one range each
   double zp, zq;
   auto totals = [&]() {
-    if (tid < a.n_sub) s = sums[tid];
-    zp = block_sum_f64(s.p, buf);
-    zq = block_sum_f64(s.q, buf);
+    if (tid < a.n_sub) {   // (from L2: other CTAs wrote most of them)
+      const double2* from = reinterpret_cast<const double2*>(&sums[tid]);
+      const double2 x = __ldcg(from), y = __ldcg(from + 1);
+      s = Sums{x.x, x.y, y.x, y.y};
+    }
+    const double2 z = block_sums_f64(s.p, s.q, buf);
+    zp = z.x;
+    zq = z.y;
   };
   totals();
   while (d.near && d.fine) {
-    const int x = draft[d.row];   // (in range: a token outside is never near)
-    const double p = prob(row_of(a, b, d.row)[x], d.lo_p, d.op) / zp;
-    const double q = c.draft_logits ? prob(row_of(a, b, D + 1 + d.row)[x], d.lo_q, d.oq) / zq : 1.0;
-    if (!(static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + d.row]) * q < p)) break;   // rejected after all
+    const double p = prob(ahead.xp[d.row], d.lo_p, d.op) / zp;   // (a token outside the vocabulary is never near)
+    const double q = c.draft_logits ? prob(ahead.xq[d.row], d.lo_q, d.oq) / zq : 1.0;
+    if (!(static_cast<double>(ahead.u[d.row]) * q < p)) break;   // rejected after all
     int row = d.row + 1;
-    judge(a, b, row, n, verdict, &norms);
+    judge(a, b, row, n, ahead, verdict, &norms);
     while (row < n && verdict[row] == 1) ++row;
-    describe(a, b, row, n, norms, verdict, &d);
+    describe(a, row, n, ahead, norms, verdict, &d);
     for (int sub = warp; sub < a.n_sub; sub += kSumWarps) {
       const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
       const Sums t = range_sums(a, b, d, j0, j1, table);
@@ -456,29 +486,23 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a)
   const bool with_draft = d.with_draft;
   const double ratio = with_draft ? zq / zp : 1.0;
   const double w = ratio * s.ap - s.aq, mine = w > 0.0 ? w : 0.0;
-  const double before = block_scan_f64(mine, buf);
-  const double total = block_sum_f64(mine, buf);
+  double total;
+  const double before = block_scan_f64(mine, buf, total);
   const bool fine = d.fine && isfinite(total) && total > 0.0;
   for (int i = tid; i <= D; i += kSumThreads)
-    if (i != acc || !fine) tokens[i] = i < acc ? draft[i] : -1;
-  if (tid == 0) {
-    c.n_accepted[b] = acc;
-    cross = INT_MAX;
-    last = -1;
-  }
+    if (i != acc || !fine) tokens[i] = i < acc ? ahead.x[i] : -1;
+  if (tid == 0) c.n_accepted[b] = acc;
   if (!fine) return;
-  __syncthreads();
-  const double target = static_cast<double>(c.u[static_cast<size_t>(b) * (D + 1) + D]) * total;
+  const double target = static_cast<double>(ahead.u[D]) * total;
   // the first range whose end is past the target (the last with any weight, should rounding leave none)
+  start_of[tid] = before;
   if (mine > 0.0) {
-    atomicMax(&last, tid);
-    if (target < before + mine) atomicMin(&cross, tid);
+    atomicMax(&top[0], tid);
+    if (target < before + mine) atomicMin(&cross[0], tid);
   }
   __syncthreads();
-  const int sub = cross != INT_MAX ? cross : last;
-  if (tid == sub) cross_start = before;
-  __syncthreads();
-  const double start = cross_start;
+  const int sub = cross[0] != INT_MAX ? cross[0] : top[0];
+  const double start = start_of[sub];
   const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
   const int per = (j1 - j0 + kSumThreads - 1) / kSumThreads;
   const int t0 = min(j1, j0 + tid * per), t1 = min(j1, t0 + per);
@@ -491,21 +515,16 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_pick(const VerifyArgs a)
   };
   double mass = 0.0;
   for (int j = t0; j < t1; ++j) mass += weight(j);
-  const double at = start + block_scan_f64(mass, buf);
-  __syncthreads();
-  if (tid == 0) {
-    cross = INT_MAX;
-    last = -1;
-  }
-  __syncthreads();
+  double all;
+  const double at = start + block_scan_f64(mass, buf, all);
   if (mass > 0.0) {
-    atomicMax(&last, tid);
-    if (target < at + mass) atomicMin(&cross, tid);
+    atomicMax(&top[1], tid);
+    if (target < at + mass) atomicMin(&cross[1], tid);
   }
   __syncthreads();
-  if (tid != (cross != INT_MAX ? cross : last)) return;
+  if (tid != (cross[1] != INT_MAX ? cross[1] : max(top[1], 0))) return;
   double run = at;
-  int y = t0;
+  int y = -1;   // (no weight at all where p and q differ by roundings alone: empty)
   for (int j = t0; j < t1; ++j) {
     const double x = weight(j);
     run += x;
@@ -554,7 +573,7 @@ bool verify_shape_ok(int B, int D, int V) {
   return B >= 1 && B <= 65535 && D >= 0 && D <= kMaxDraft && V >= 1 && V <= (1 << 30);
 }
 // Ranges of the deciding row: the CTAs of the whole batch resident at once (four per SM), none with
-// fewer than 1024 tokens (4 a thread), at most one range per thread of the third launch.
+// fewer than 1024 tokens (4 a thread), at most one range per thread of the CTA that picks the token.
 void plan_sums(int B, int V, int& ctas, int& sub_len) {
   ctas = std::min(std::min(kSumMaxCtas, std::max(1, 4 * kNumSM / B)), std::max(1, V / 1024));
   sub_len = (ceil_div_i(V, ctas * kSumWarps) + 31) & ~31;
@@ -571,8 +590,8 @@ extern "C" {
 size_t flashloop_verify_draft_scratch_bytes(int B, int D, int V) {
   if (!verify_shape_ok(B, D, V)) return 0;
   return align256_sz(static_cast<size_t>(B) * (2 * D + 1) * verify_chunks(V) * sizeof(RowPart)) +
-         align256_sz(B * sizeof(Deciding)) + align256_sz(static_cast<size_t>(B) * kSumThreads * sizeof(Sums)) +
-         align256_sz(static_cast<size_t>(B) * (D + 1) * 4) + 256;
+         align256_sz(static_cast<size_t>(B) * kSumThreads * sizeof(Sums)) +
+         align256_sz(static_cast<size_t>(B) * (D + 2) * 4) + 256;
 }
 
 fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, size_t scratch_bytes,
@@ -597,6 +616,7 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   if (c->temperature == 0.f) a.c.draft_logits = nullptr;   // greedy: the target's rows alone
   a.n_chunks = verify_chunks(c->V);
   a.scale2 = c->temperature > 0.f ? 1.4426950408889634 / static_cast<double>(c->temperature) : 0.0;
+  a.reach = c->temperature > 0.f ? static_cast<float>(1000.0 / a.scale2) : 0.f;
   a.part = static_cast<RowPart*>(scratch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rows = c->D + 1 + (a.c.draft_logits ? c->D : 0);
@@ -605,12 +625,11 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   a.n_sub = ctas * kSumWarps;
   uint8_t* ws = static_cast<uint8_t*>(scratch) +
                 align256_sz(static_cast<size_t>(c->B) * (2 * c->D + 1) * a.n_chunks * sizeof(RowPart));
-  a.deciding = reinterpret_cast<Deciding*>(ws);
-  ws += align256_sz(c->B * sizeof(Deciding));
   a.sums = reinterpret_cast<Sums*>(ws);
   ws += align256_sz(static_cast<size_t>(c->B) * kSumThreads * sizeof(Sums));
   a.tickets = reinterpret_cast<unsigned*>(ws);
   a.dead = a.tickets + static_cast<size_t>(c->B) * c->D;
+  a.done = a.dead + c->B;
   // Skipping rows behind a rejection pays when the calls' rows do not all start at once: about
   // eight 32 KB chunks per SM are in flight, and the memset in front costs 2 us.
   const bool early = c->temperature > 0.f && c->D >= 2 &&
@@ -626,9 +645,7 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   if (e != cudaSuccess) return cuda_status(e);
   if (c->temperature == 0.f)
     return cuda_status(launch_k(true, k_verify_greedy, dim3(c->B), dim3(256), 0, s, a));
-  e = launch_k(true, k_verify_sums, dim3(ctas, c->B), dim3(kSumThreads), 0, s, a);
-  if (e != cudaSuccess) return cuda_status(e);
-  return cuda_status(launch_k(true, k_verify_pick, dim3(c->B), dim3(kSumThreads), 0, s, a));
+  return cuda_status(launch_k(true, k_verify_sums, dim3(ctas, c->B), dim3(kSumThreads), 0, s, a));
 }
 
 }  // extern "C"

@@ -568,3 +568,20 @@ def test_verify_strided_logits_streams_and_graph():
         torch.cuda.synchronize()
         wt, wa = ref.verify(l2.cpu().numpy(), d2.cpu().numpy(), x2.cpu().numpy(), u2.cpu().numpy(), None, 1.0)
         assert np.array_equal(tok.cpu().numpy(), wt) and np.array_equal(acc.cpu().numpy(), wa)
+
+
+@pytest.mark.parametrize("V", [17, 4099, 40000])
+def test_verify_writes_a_token_where_target_and_draft_differ_by_roundings(V):
+    """A draft token outside the vocabulary is rejected; what is left of the target's row after the draft's is then
+    nothing but roundings.  Whether that counts as empty (-1) or gives some token, one of the two is written."""
+    B, D = 8, 2
+    g = gen(V)
+    x = torch.randn((B, D + 1, V), device="cuda", generator=g) * 3
+    q = x[:, :D].clone()
+    q[1::2] += 0.75   # the same distribution up to the rounding of the sums
+    tokens = torch.full((B, D + 1), 12345678, dtype=torch.int32, device="cuda")
+    draft = torch.full((B, D), V, dtype=torch.int32, device="cuda")
+    got, n = fl.verify_draft(x, q, draft, torch.rand((B, D + 1), device="cuda", generator=g), tokens=tokens)
+    assert (n == 0).all()
+    assert ((got[:, 0] >= -1) & (got[:, 0] < V)).all() and (got[:, 1:] == -1).all()
+    assert (got[0::2, 0] == -1).all()   # equal rows: exactly nothing is left
