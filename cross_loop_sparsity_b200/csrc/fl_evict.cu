@@ -55,7 +55,9 @@ __device__ __forceinline__ void scan_warps(int* v, int* total) {
 // cluster barrier sums all CTAs' histograms over distributed shared memory and
 // finds the next digit by itself.  The freed slots' list stays in shared memory, where
 // the CTAs look up where their kept slots go.  Latency-bound (a round trip to memory, then
-// about ten barriers).
+// about ten barriers): 10 us at 32 segments of 4160 slots, 20 us at 32 of 65536 (8 bytes a slot
+// would take 3 us).  Digits of 8 bits with 8 copies of the counters took 12 and 27 us; reading every
+// bin of the other CTAs instead of sums of 64 first, 33 us at 65536.
 // ============================================================================
 __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const EvictArgs a) {
   pdl_trigger();   // the move is launched, and waits for the result, while this runs
@@ -284,10 +286,13 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const EvictArgs 
 // Move: a row's K and V as 16-byte vectors, kEvVecs of them per thread in flight
 // at once; in place only rows whose source is another slot.  HBM-bound: 8 hd
 // bytes per copied row.  W: vectors of a K or V row as a constant (head_dim 64, 128; 0: any).
+//   Four vectors and five CTAs per SM: 1 GB out of place (32 x 8 heads, 4160 slots to 4096, hd 128,
+// with the selection) in 181 us, 90 % of the measured copy bandwidth; 8 vectors and 3 or 4 CTAs
+// 190-193, 4 and 6 or 8 190-231 (registers spill), 2 and 8 193.
 // ============================================================================
-constexpr int kEvVecs = 8;
+constexpr int kEvVecs = 4;
 template <int W>
-__global__ void __launch_bounds__(256) k_evict_move(const EvictArgs a, int vec_any, int rows_cta) {
+__global__ void __launch_bounds__(256, 5) k_evict_move(const EvictArgs a, int vec_any, int rows_cta) {
   pdl_wait();
   const flashloop_evict_args& c = a.c;
   const int vec = W ? W : vec_any;

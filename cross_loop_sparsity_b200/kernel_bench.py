@@ -24,6 +24,13 @@
 * ``quantize``: the KV-residual quantiser over a residual shaped like the
   65536-token context (65536 tokens x 4 layers x 2 (K, V) x 4 KV heads rows of
   128 fp32, int4 / int2, group 64), bytes moved against HBM.
+* ``prefix_attention``, ``column_weights``, ``evict``, ``verify_draft``: the
+  serving operators as a decode loop calls them (captured into a graph over
+  the rotated operand sets): 64 samples of an 8192-token prompt and 160 drafted
+  tokens over a 65531-token one; the weights of a decode step's and of a
+  prompt's queries; a cache two percent over its budget and 65536-token
+  prompts cut to 8192; 5 drafts of 32 sequences and 8 of 64.  Time against the
+  larger of bytes over the measured HBM bandwidth and FLOPs over the bf16 peak.
 * ``decode_step_capture`` and ``lazy_call_capture`` (only on request, for ncu;
   no measurement): one decode step at the decode GEMM shapes with one shared
   layer and a 512-token context, and one lazy call of ``--workload`` with
@@ -223,6 +230,102 @@ def quantize_residual(reps):
              "achieved": gbs, "unit": "GB/s", "peak": hbm, "frac": gbs / hbm, "peak_source": f"{src} hbm_gbs"}]
 
 
+def _operator(name, shape, sets, call, moved, flops, reps):
+    """A line for call(*set) over the operand sets, from a replayed graph."""
+    import torch
+    hbm, tc, src = _peaks()
+    for x in sets:
+        call(*x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            for x in sets:
+                call(*x)
+    ms = _time(lambda i: graph.replay(), reps) / (4 * len(sets))
+    floor = max(moved / hbm / 1e6, flops / tc / 1e9)
+    return {"kernel": name, "shape": shape, "ms": ms, "achieved": moved / ms / 1e6, "unit": "GB/s",
+            "tflops": flops / ms / 1e9, "floor_ms": floor, "frac": floor / ms,
+            "peak_source": f"{src} hbm_gbs, bf16_tflops"}
+
+
+def _bf16(*shape):
+    import torch
+    return torch.randn(shape, device="cuda", dtype=torch.bfloat16)
+
+
+def _int32(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def prefix_attention(reps):
+    import torch
+    from cross_loop_sparsity_b200 import flashloop as fl
+    out = []
+    for B, Tq, H, Hkv, hd, P, S in ((64, 1, 32, 8, 128, 8192, 1000), (32, 5, 32, 8, 128, 65531, 300)):
+        scratch = torch.empty(fl.prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S), dtype=torch.uint8,
+                              device="cuda")
+        sets = [(_bf16(B, Tq, H, hd), _bf16(Hkv, P, hd), _bf16(Hkv, P, hd), _bf16(B, Hkv, S, hd), _bf16(B, Hkv, S, hd),
+                 _int32([S] * B), None, None, _bf16(B, Tq, H, hd), torch.empty((B, Tq, H), device="cuda"), scratch)
+                for _ in range(2)]
+        moved = 4 * hd * Hkv * (P + B * S) + 4 * B * Tq * H * hd
+        out.append(_operator("prefix_attention", f"{B} x {Tq} queries, {P} + {S} columns, {H}/{Hkv} heads x {hd}", sets,
+                             fl.prefix_attention, moved, 4 * B * Tq * H * hd * (P + S), reps))
+    return out
+
+
+def column_weights(reps):
+    import torch
+    from cross_loop_sparsity_b200 import flashloop as fl
+    out = []
+    for B, Tq, H, Hkv, hd, S in ((8, 1, 16, 4, 128, 4097), (1, 512, 16, 4, 128, 16384)):
+        scratch = torch.empty(fl.column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S), dtype=torch.uint8, device="cuda")
+        sets = [(_bf16(B, Tq, H, hd), _bf16(B, Hkv, S, hd), torch.full((B, Tq, H), 9.0, device="cuda"),
+                 torch.rand((B, Hkv, S), device="cuda"), _int32([S] * B), None, None,
+                 torch.empty((B, Hkv, S), device="cuda"), scratch) for _ in range(8)]
+        moved = B * Hkv * S * (2 * hd + 8) + B * Tq * H * (2 * hd + 4)
+        out.append(_operator("column_weights", f"{B} x {Tq} queries, {S} columns, {H}/{Hkv} heads x {hd}", sets,
+                             fl.column_weights, moved, 2 * B * H * hd * (Tq * S - Tq * (Tq - 1) // 2), reps))
+    return out
+
+
+def evict(reps):
+    import torch
+    from cross_loop_sparsity_b200 import flashloop as fl
+    out = []
+    for B, Hkv, hd, S, keep, recent in ((8, 4, 128, 4160, 4096, 64), (4, 8, 128, 65536, 8192, 256)):
+        scratch = torch.empty(fl.evict_scratch_bytes(B, Hkv, S, keep), dtype=torch.uint8, device="cuda")
+        sets = []
+        for _ in range(2):
+            pos = torch.arange(S, dtype=torch.int32, device="cuda").expand(B, Hkv, S).contiguous()
+            to = (_bf16(B, Hkv, keep, hd), _bf16(B, Hkv, keep, hd), torch.empty((B, Hkv, keep), device="cuda"),
+                  pos[:, :, :keep].clone(), _int32([0] * B))
+            sets.append((_bf16(B, Hkv, S, hd), _bf16(B, Hkv, S, hd), torch.rand((B, Hkv, S), device="cuda") ** 4, pos,
+                         _int32([S] * B), keep, recent, 4, to, scratch))
+        out.append(_operator("evict", f"{B} x {Hkv} heads x {hd}, {S} columns to {keep}", sets, fl.evict,
+                             B * Hkv * (8 * S + keep * (8 * hd + 8)), 0, reps))
+    return out
+
+
+def verify_draft(reps):
+    import torch
+    from cross_loop_sparsity_b200 import flashloop as fl
+    out = []
+    for B, D, V in ((32, 5, 32000), (64, 8, 131071)):
+        scratch = torch.empty(fl.verify_draft_scratch_bytes(B, D, V), dtype=torch.uint8, device="cuda")
+        sets = []
+        for _ in range(2):
+            x = torch.randn((B, D + 1, V), device="cuda") * 3
+            q = x[:, :D] + 0.3 * torch.randn((B, D, V), device="cuda")
+            draft = torch.distributions.Categorical(logits=q).sample().to(torch.int32)
+            sets.append((x, q, draft, torch.rand((B, D + 1), device="cuda"), None, 1.0, _int32([[0] * (D + 1)] * B),
+                         _int32([0] * B), scratch))
+        out.append(_operator("verify_draft", f"{B} sequences, {D} drafts, {V} tokens", sets, fl.verify_draft,
+                             4 * B * (2 * D + 1) * V, 0, reps))
+    return out
+
+
 def decode_step_capture(reps):
     """One decode step at the decode workload's GEMM shapes (8 tokens, d_model
     2048, ffn 5632, vocab 32000) with one shared layer and a 512-token context,
@@ -300,8 +403,8 @@ def main():
     import time
     import torch
     from cross_loop_sparsity_b200.clocks import ClockSampler
-    fns = (gemm_wide, gemm_skinny, topk, attn_decode, quantize_residual, quantize, decode_step_capture,
-           lazy_call_capture)
+    fns = (gemm_wide, gemm_skinny, topk, attn_decode, quantize_residual, quantize, prefix_attention,
+           column_weights, evict, verify_draft, decode_step_capture, lazy_call_capture)
     captures = (decode_step_capture, lazy_call_capture)
     only = {x for x in args.only.split(",") if x}
     for fn in fns:
