@@ -139,22 +139,27 @@ __device__ __forceinline__ int judge_one(const VerifyArgs& a, int b, int i) {
 
 // ============================================================================
 // One chunk of one row: 32 logits per thread in registers (16-byte loads where the
-// row's alignment allows, whatever V is), then maximum and sum.  HBM-bound.
+// row's alignment allows, whatever V is), then maximum and sum.  HBM-bound, by CTAs that come
+// and go (five of 32 KB per SM): 32 x 11 rows of 32000 logits in 7.3 us.
 // Rows go position by position, each position's rows of all sequences together.
-// EARLY: rows behind a rejected draft decide nothing; the CTA that finishes a
-// draft's two rows (a ticket) judges it, and rows of later positions that have not
-// started by then are not read.  Both for large calls: the tickets need a memset in front.
+//   EARLY: rows behind a rejected draft decide nothing; a CTA takes its chunk of a position's
+// target row and then of its draft row, the one that finishes a draft (a ticket) judges it, and
+// later positions that have not started by then are not read.  For large calls: the
+// tickets need a memset in front.  64 sequences, 8 drafts, 131071 logits with the samples' usual
+// rejections: 54 us, the whole call 93; a CTA per row 60 (skipped CTAs cost 1 us of their place each,
+// and a row as many tickets), persistent CTAs fed from a ring of bulk copies 67.
 // ============================================================================
 template <bool EARLY>
-__global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVfThreads, 5) k_verify_rows(const VerifyArgs a) {
   __shared__ float red[kVfThreads / 32];
   __shared__ int red_i[kVfThreads / 32];
   __shared__ int last;
   pdl_trigger();
   const flashloop_verify_args& c = a.c;
   const bool pairs = c.draft_logits != nullptr;
-  const int chunk = blockIdx.x, b = blockIdx.y, i = pairs ? blockIdx.z >> 1 : blockIdx.z;   // position i
-  const int r = pairs && (blockIdx.z & 1) ? c.D + 1 + i : i;
+  // position i; EARLY: its target row and then its draft row, else one of the two
+  const int chunk = blockIdx.x, b = blockIdx.y, i = !EARLY && pairs ? blockIdx.z >> 1 : blockIdx.z;
+  int r = !EARLY && pairs && (blockIdx.z & 1) ? c.D + 1 + i : i;
   const int n = drafts_of(a, b);
   if (r == 0 && chunk == 0 && threadIdx.x == 0) a.done[b] = 0;   // (row 0 is always read)
   if (r <= c.D ? r > n : i >= n) return;   // rows of drafts that were not made
@@ -165,70 +170,76 @@ __global__ void __launch_bounds__(kVfThreads) k_verify_rows(const VerifyArgs a) 
     if (last) return;
   }
   const int lo = chunk * kVfChunk, hi = min(c.V, lo + kVfChunk);
-  const float* x = row_of(a, b, r) + lo;
-  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);   // floats past a 16-byte boundary
-  const int len = hi - lo;
-  float v[8][4];
+#pragma unroll 1
+  for (;;) {   // (EARLY: the target row, then the draft row)
+    const float* x = row_of(a, b, r) + lo;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) >> 2) & 3);   // floats past a 16-byte boundary
+    const int len = hi - lo;
+    float v[8][4];
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    const int j = (u * kVfThreads + tid) * 4 - off;   // index of the vector's first logit
-    if (j >= 0 && j + 4 <= len) {
-      const float4 f = __ldcs(reinterpret_cast<const float4*>(x + j));
-      v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
-    } else {
+    for (int u = 0; u < 8; ++u) {
+      const int j = (u * kVfThreads + tid) * 4 - off;   // index of the vector's first logit
+      if (j >= 0 && j + 4 <= len) {
+        const float4 f = __ldcs(reinterpret_cast<const float4*>(x + j));
+        v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[u][e] = j + e >= 0 && j + e < len ? x[j + e] : -INFINITY;
-    }
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int u = 0; u < 8; ++u)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = fmaxf(m, v[u][e]);
-  m = warp_max(m);
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kVfThreads / 32; ++w) m = fmaxf(m, red[w]);
-  __syncthreads();
-  RowPart* out = a.part + (static_cast<size_t>(b) * (2 * c.D + 1) + r) * a.n_chunks + chunk;
-  if (c.temperature == 0.f) {
-    int at = INT_MAX;
-#pragma unroll
-    for (int u = 7; u >= 0; --u)
-#pragma unroll
-      for (int e = 3; e >= 0; --e) {
-        const int j = (u * kVfThreads + tid) * 4 - off + e;
-        if (v[u][e] == m && j >= 0 && j < len) at = lo + j;
+        for (int e = 0; e < 4; ++e) v[u][e] = j + e >= 0 && j + e < len ? x[j + e] : -INFINITY;
       }
-    at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == 0) red_i[warp] = at;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, v[u][e]);
+    m = warp_max(m);
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kVfThreads / 32; ++w) m = fmaxf(m, red[w]);
+    __syncthreads();
+    RowPart* out = a.part + (static_cast<size_t>(b) * (2 * c.D + 1) + r) * a.n_chunks + chunk;
+    if (c.temperature == 0.f) {
+      int at = INT_MAX;
+#pragma unroll
+      for (int u = 7; u >= 0; --u)
+#pragma unroll
+        for (int e = 3; e >= 0; --e) {
+          const int j = (u * kVfThreads + tid) * 4 - off + e;
+          if (v[u][e] == m && j >= 0 && j < len) at = lo + j;
+        }
+      at = __reduce_min_sync(0xffffffffu, at);
+      if (lane == 0) red_i[warp] = at;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 1; w < kVfThreads / 32; ++w) at = min(at, red_i[w]);
+        *out = RowPart{m, 0.f, at, 0};
+      }
+      return;
+    }
+    const float c2 = static_cast<float>(a.scale2), ms = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += exp2f((v[u][e] - ms) * c2);
+    s = warp_sum(s);
+    if (lane == 0) red[warp] = s;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kVfThreads / 32; ++w) at = min(at, red_i[w]);
-      *out = RowPart{m, 0.f, at, 0};
+      float t = 0.f;
+      for (int w = 0; w < kVfThreads / 32; ++w) t += red[w];
+      *out = RowPart{m, t, 0, 0};
     }
-    return;
-  }
-  const float c2 = static_cast<float>(a.scale2), ms = m == -INFINITY ? 0.f : m;
-  float s = 0.f;
-#pragma unroll
-  for (int u = 0; u < 8; ++u)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s += exp2f((v[u][e] - ms) * c2);
-  s = warp_sum(s);
-  if (lane == 0) red[warp] = s;
-  __syncthreads();
-  if (tid == 0) {
-    float t = 0.f;
-    for (int w = 0; w < kVfThreads / 32; ++w) t += red[w];
-    *out = RowPart{m, t, 0, 0};
-    if (EARLY) {
-      __threadfence();
-      last = i < n && atomicAdd(&a.tickets[static_cast<size_t>(b) * c.D + i], 1u) + 2u == (pairs ? 2u : 1u) * a.n_chunks;
-    }
+    if (!EARLY || !pairs || r > c.D || i >= n) break;
+    r = c.D + 1 + i;
+    __syncthreads();   // red
   }
   if (EARLY) {
+    if (tid == 0) {
+      __threadfence();
+      last = i < n && atomicAdd(&a.tickets[static_cast<size_t>(b) * c.D + i], 1u) + 2u == a.n_chunks;
+    }
     __syncthreads();
     if (!last || warp != 0) return;
     __threadfence();
@@ -638,7 +649,7 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   const dim3 grid(a.n_chunks, c->B, rows);
   if (early) {
     e = cudaMemsetAsync(a.tickets, 0xFF, static_cast<size_t>(c->B) * (c->D + 1) * 4, s);
-    if (e == cudaSuccess) e = launch_k(false, k_verify_rows<true>, grid, dim3(kVfThreads), 0, s, a);
+    if (e == cudaSuccess) e = launch_k(false, k_verify_rows<true>, dim3(a.n_chunks, c->B, c->D + 1), dim3(kVfThreads), 0, s, a);
   } else {
     e = launch_k(false, k_verify_rows<false>, grid, dim3(kVfThreads), 0, s, a);
   }
