@@ -139,7 +139,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // the prefix (rows of every sequence, packed) or of one sequence's own rows.
 // Four warps take alternate 32-key tiles, each from a TMA ring of its own, with
 // its own running (max, sum, output): no barrier between warps until the end.
-// HBM-bound: a tile's 16 KB feed 16 NM rows.  A row sees every column of
+// HBM-bound: a tile's 16 KB feed 16 NM rows.  mma.sync, because a query row block of a decode
+// step has 1 to 32 rows: a 128-row tcgen05 tile would be mostly padding (k_prefix_tc takes over from 33 rows).
+// Two CTAs per SM, 24 KB of ring per warp, reused by halves (K, then V): with 64 samples' own 500 to 1000
+// columns of 8 heads x 128 behind an 8192-column prefix the whole call takes 68 us, 74 with one CTA
+// per SM and twice the ring.  A row sees every column of
 // the range -- a sequence's columns stop at the last one all its queries see;
 // the few that only later queries see are added by the merge -- so what a masked
 // row of V holds never meets a product.  HILO: fp32 queries and probabilities as
@@ -465,6 +469,11 @@ __global__ void __launch_bounds__(128, 2)
 // most 2^8, and bf16's relative precision is the same there.
 //   P enters the second product rounded to bf16 (as in the prefill attention);
 // the sums use the fp32 values.
+//   Measured: 256 rows x 65536 columns x 8 heads, hd 128, 69 GFLOP: 75 us (42 at the measured GEMM rate; about 20
+// of the 75 are start and end: queries in, TMEM, pipeline fill, partial results out).  Two softmax
+// warpgroups instead of four took 84.  In the steady state Q K^T, with both operands in
+// shared memory, is what the rest waits for (128 x 128 x 128 in about 890 clocks, 512 ideal), so
+// exponentials on the FMA pipe gained nothing here.
 // ============================================================================
 template <int HD>
 struct TcSmem {
@@ -1095,7 +1104,8 @@ struct Seen {
 };
 
 // ---- few rows (decode): 32-key tiles streamed by each warp from a TMA ring of its own, the
-// rows' fragments in registers.  HBM-bound: the keys are read once and nothing else is large.
+// rows' fragments in registers.  HBM-bound: the keys are read once and nothing else is large (8 sequences x 4097
+// columns x 4 heads x 128, 34 MB: 10.5 us, launch included; tiles shared by the whole CTA took 13.7).
 // Warps take contiguous runs of the tiles of all (sequence, KV head) pairs.
 constexpr int kWsWarps = 8, kWsStages = 3;
 template <int HD, int NM>
@@ -1222,8 +1232,10 @@ __global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_c
 // tile's sums is partial (CTA + tile).  One TMA thread, one MMA warp, four warpgroups (all 256 keys x
 // a quarter of a block's rows each; two TMEM buffers, so that the next block's products run under
 // this one's exponentials).  Bound by the exponentials, 16 a clock and SM, with shared memory
-// (the products' operands) close behind.
-constexpr int kWtPoly = 1;   // of 8 pairs of exponentials, those formed on the FMA pipe
+// (the products' operands) close behind.  512 queries of 16 heads x 16384 columns of 4 KV heads x 128, causal: 52 us,
+// of which the exponentials alone would take 30 and the products 21; warpgroups that take alternate
+// blocks 54, or half the rows of a key 57, mma.sync warp tiles 206.
+constexpr int kWtPoly = 1;   // of 8 pairs of exponentials, those formed on the FMA pipe (0: 56 us there, 1: 52, 2: 54, 3: 55)
 constexpr int kWtCols = 256, kWtRows = 128, kWtThreads = 576;
 constexpr int kWtStaged = 24;   // row blocks whose lse are in shared memory at once
 template <int HD>
@@ -1498,7 +1510,9 @@ __global__ void __launch_bounds__(256) k_weights_add(const WeightsArgs a) {
 }
 
 // ---------------------------------------------------------------- host side
-// A CTA per row up to four rows per SM (latency: the splits are spread over the CTA), else a row per group.
+// A CTA per row up to four rows per SM (latency: the splits are spread over the CTA), else a row per group: with 4096 +
+// 257 columns, a CTA per row against a row per group, whole calls in us: 128 rows 12.4 / 13.8, 512 17.3 / 17.8,
+// 768 22.7 / 20.5, 2048 45.0 / 40.2.
 template <int HD>
 cudaError_t run_merge(bool q32, const PrefixArgs& a, bool pdl, cudaStream_t s) {
   constexpr int NG = 128 / (HD / 4);
@@ -1520,12 +1534,19 @@ struct PrefixPlan {
   size_t rows, tc_parts;
   size_t off_ml, off_tc_o, off_tc_ml, bytes;
 };
-constexpr int kTcMinRows = 33;   // query rows per KV head (two warp tiles hold 32)
+// The prefix goes to the 5th-generation tensor cores when its rows take two blocks of warp tiles (which then read
+// every column twice) and there is enough of it for their 16 us of start and end: blocks x columns x KV heads x
+// head_dim.  Whole calls with 8 heads x 128, tensor cores against warp tiles, us: 36 rows x 1024 columns 16.3 / 12.3,
+// x 4096 19.5 / 15.3, x 32768 38.8 / 42.6; 64 rows x 512 16.5 / 12.8, x 4096 20.3 / 19.3, x 32768
+// 40.0 / 46.7; 128 rows x 4096 22.4 / 25.8; and of one block, 32 rows x 4096 19.3 / 13.4, x 32768 38.7 / 37.8.
+constexpr int kTcMinRows = 33;
+constexpr double kTcMinWork = 1.2e7;
 PrefixPlan plan_prefix(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool warp_tiles) {
   PrefixPlan p{};
   const int G = H / Hkv;
   const long long rows_p = static_cast<long long>(B) * Tq * G, rows_s = static_cast<long long>(Tq) * G;
-  if (!warp_tiles && P >= kTcTile && rows_p >= kTcMinRows) {
+  if (!warp_tiles && P >= kTcTile && rows_p >= kTcMinRows &&
+      static_cast<double>(ceil_div_i(rows_p, 32)) * P * Hkv * hd >= kTcMinWork) {
     const long long pairs = static_cast<long long>(Hkv) * ceil_div_i(rows_p, kTcRows);
     p.tc_ctas = static_cast<int>(std::min<long long>(kNumSM, std::max(1LL, pairs * ceil_div_i(P, kTcTile) / kTcMinTiles)));
     p.tc_parts = static_cast<size_t>(p.tc_ctas + pairs);
@@ -1566,7 +1587,8 @@ cudaError_t run_split_hd(int nm, bool hilo, const CUtensorMap* m, const PrefixAr
 
 size_t stream_smem(int hd) { return 1024 + static_cast<size_t>(kWsWarps) * kWsStages * kPxTile * hd * 2; }
 
-// Column weights on tcgen05 when a (sequence, KV head) has more rows than two warp tiles.
+// Column weights on tcgen05 when a (sequence, KV head) has more rows than two warp tiles hold (tensor cores
+// against warp tiles: 32 rows, 8 x 4096 columns x 4 heads 23.4 / 15.7 us, 65536 columns 37.8 / 22.9).
 constexpr int kStreamRows = 32;
 struct WeightsPlan {
   bool tc;

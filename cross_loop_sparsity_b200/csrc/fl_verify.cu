@@ -420,8 +420,9 @@ __device__ double block_scan_f64(double v, double2* buf, double& total) {
 // Second launch: every CTA finds its sequence's deciding row from the first
 // launch's sums, then each of its warps forms the 64-bit sums of a contiguous
 // range of that row's tokens, two exponentials a token, once.  Bound by the 64-bit pipe
-// (about 11 operations per exponential) for many sequences, by the latency of
-// finding the row for few.
+// (about 11 operations per exponential) and its conversions for many sequences, by a chain of round
+// trips for few: 64 rows of 131071 tokens about 37 us (18 of them the sums), one sequence of
+// 32000 8 us.
 //   The CTA that finishes a sequence's last ranges picks its token: totals of the
 // ranges' sums, the range that holds the crossing, and the crossing token in it.  A near
 // decision is settled by the 64-bit totals of its row; when it turns out accepted, this CTA
@@ -548,7 +549,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
 }
 
 // ============================================================================
-// Greedy: one CTA per sequence; the first launch left every chunk's maximum.
+// Greedy: one CTA per sequence; the first launch left every chunk's maximum.  Latency-bound (16 sequences of up to
+// 5 rows x 50001 tokens: 5.6 us with the first launch).
 // ============================================================================
 __global__ void __launch_bounds__(256) k_verify_greedy(const VerifyArgs a) {
   __shared__ int best[kMaxDraft + 1];
@@ -641,10 +643,10 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   a.tickets = reinterpret_cast<unsigned*>(ws);
   a.dead = a.tickets + static_cast<size_t>(c->B) * c->D;
   a.done = a.dead + c->B;
-  // Skipping rows behind a rejection pays when the calls' rows do not all start at once: about
-  // eight 32 KB chunks per SM are in flight, and the memset in front costs 2 us.
-  const bool early = c->temperature > 0.f && c->D >= 2 &&
-                     static_cast<double>(c->B) * rows * c->V * 4.0 > 64e6;
+  // Skipping rows behind a rejection costs a memset in front and a ticket per chunk, and pays when most rows
+  // have not started by the first verdicts: with drafts of which most are accepted, with against
+  // without it, 45 MB of logits 27.6 / 20.8 us, 139 MB 44.2 / 37.8, 570 MB 110 / 117 (with more rejections 92).
+  const bool early = c->temperature > 0.f && c->D >= 2 && static_cast<double>(c->B) * rows * c->V * 4.0 > 350e6;
   cudaError_t e;
   const dim3 grid(a.n_chunks, c->B, rows);
   if (early) {

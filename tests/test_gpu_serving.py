@@ -79,6 +79,19 @@ ATT = [
     (33, 4, 4, 2, 128, 5000, 6, [6, 5, 4] * 11, [4, 3, 2] * 11),
     (64, 8, 2, 1, 64, 3333, 9, [9] * 64, [i % 9 for i in range(64)]),
     (9, 4, 8, 2, 128, 300, 4, [4] * 9, [0] * 9),
+    # prefixes long enough for the tensor-core kernel: lengths off its 128-column tiles, one row tile and several blocks
+    # of two, a last block with one, sequences without queries
+    (40, 1, 4, 4, 128, 12007, 0, None, None),
+    (12, 3, 4, 1, 64, 37633, 4, [4, 3, 2] * 4, [3, 1, 2] * 4),
+    (65, 1, 6, 2, 128, 7041, 2, [2] * 65, None),
+    (33, 1, 8, 1, 64, 21001, 3, [3] * 33, None),
+    (33, 4, 4, 2, 128, 6000, 6, [6, 5, 4] * 11, [4, 3, 2] * 11),
+    (64, 8, 2, 1, 64, 6145, 9, [9] * 64, [i % 9 for i in range(64)]),
+    (70, 2, 4, 1, 128, 5249, 5, [5] * 70, [2, 0] * 35),
+    (40, 8, 8, 2, 128, 1291, 20, list(range(8, 20)) * 3 + [20] * 4, [1 + i % 8 for i in range(40)]),
+    (3, 7, 64, 1, 64, 4600, 12, [12, 7, 9], [7, 7, 2]),
+    (9, 4, 8, 2, 128, 9500, 4, [4] * 9, [0] * 9),
+    (9, 4, 8, 2, 128, 9473, 4, [4] * 9, [1] * 9),
 ]
 
 
@@ -101,50 +114,52 @@ def test_attention_scales(scale):
 
 
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.3])
-@pytest.mark.parametrize("hd,B", [(64, 15), (128, 40)])
-def test_attention_scales_many_rows(hd, B, scale):
-    """The same with the prefix on the tensor-core kernel (over 32 rows per KV head), scores growing along the prefix so that
-    the running maximum moves often, and one or two row tiles."""
+@pytest.mark.parametrize("hd,B,P", [(64, 15, 700), (128, 40, 700), (64, 64, 16001), (128, 40, 12007)])
+def test_attention_scales_many_rows(hd, B, P, scale):
+    """The same with more than 32 rows per KV head (the longer prefixes on the tensor-core kernel), scores growing along the
+    prefix so that the running maximum moves often, and one or two row tiles."""
     g = gen(31)
-    kp, vp = normal(g, 2, 700, hd), normal(g, 2, 700, hd)
-    kp = (kp.float() * torch.linspace(0.1, 3.0, 700, device="cuda")[None, :, None]).to(torch.bfloat16)
+    kp, vp = normal(g, 2, P, hd), normal(g, 2, P, hd)
+    kp = (kp.float() * torch.linspace(0.1, 3.0, P, device="cuda")[None, :, None]).to(torch.bfloat16)
     check_attention(normal(g, B, 2, 6, hd), kp, vp, normal(g, B, 2, 8, hd), normal(g, B, 2, 8, hd), [8, 3, 2] * (B // 3) +
                     [5] * (B % 3), None, scale=scale)
 
 
-def test_attention_non_finite_scores_many_rows():
-    """On the tensor-core kernel: a visible NaN key makes the rows NaN, columns of -inf score weigh nothing, a +inf score gives
-    NaN, and no finite score at all 0 and -inf."""
+@pytest.mark.parametrize("P", [500, 24301])
+def test_attention_non_finite_scores_many_rows(P):
+    """More than 32 rows per KV head (the longer prefix on the tensor-core kernel): a visible NaN key makes the rows NaN,
+    columns of -inf score weigh nothing, a +inf score gives NaN, and no finite score at all 0 and -inf."""
     g = gen(32)
     q = normal(g, 24, 1, 8, 64).abs()
-    kp, vp = normal(g, 4, 500, 64), normal(g, 4, 500, 64)
+    kp, vp = normal(g, 4, P, 64), normal(g, 4, P, 64)
     kp[0, 130] = NAN
     kp[1, 5:300] = -INF                  # q > 0: scores -inf, the first two tiles all of them
-    kp[2, 499] = INF
+    kp[2, P - 1] = INF
     kp[3] = -INF
     out, lse = fl.prefix_attention(q, kp, vp, None, None, None)
     o = out.float()
     for h in (0, 1, 4, 5):
         assert bool(torch.isnan(o[:, 0, h]).all()) and bool(torch.isnan(lse[:, 0, h]).all())
     assert bool((o[:, 0, 6:] == 0).all()) and bool((lse[:, 0, 6:] == -INF).all())
-    keep = [i for i in range(500) if not 5 <= i < 300]
+    keep = [i for i in range(P) if not 5 <= i < 300]
     want, wl = fl.prefix_attention(q, kp[:, keep].contiguous(), vp[:, keep].contiguous(), None, None, None)
     # each side within its bound of 2^-8 of A + |out|, A the mean |v| under the weights (below 5 here)
     assert bool(((o - want.float())[:, 0, 2:4].abs() <= 2 * 2 ** -8 * 10).all())
     assert bool(((lse - wl)[:, 0, 2:4].abs() <= 1e-4).all())
 
 
-def test_attention_strided_layouts():
+@pytest.mark.parametrize("B,P", [(3, 150), (24, 8001)])
+def test_attention_strided_layouts(B, P):
     """Queries inside a wider projection, caches as [B][S][Hkv][hd] and [P][Hkv][hd], a strided output."""
     g = gen(4)
-    B, Tq, H, Hkv, hd, P, S = 3, 2, 8, 2, 128, 150, 70
+    Tq, H, Hkv, hd, S = 2, 8, 2, 128, 70
     qkv = normal(g, B, Tq, (H + 2 * Hkv) * hd)
     q = qkv[..., :H * hd].view(B, Tq, H, hd)
     pre = normal(g, 2, P, Hkv, hd)
     own = normal(g, 2, B, S, Hkv, hd)
     kp, vp = (pre[i].transpose(0, 1) for i in (0, 1))
     k, v = (own[i].transpose(1, 2) for i in (0, 1))
-    lens, qn = [70, 2, 33], [2, 1, 2]
+    lens, qn = [70, 2, 33] * (B // 3), [2, 1, 2] * (B // 3)
     want, _ = check_attention(q, kp, vp, k, v, lens, qn)
     wide = torch.full((B, Tq, H, 2 * hd), 3.0, dtype=torch.bfloat16, device="cuda")
     wide[..., :hd] = 7.0
@@ -152,13 +167,14 @@ def test_attention_strided_layouts():
     assert torch.equal(wide[..., :hd], want) and bool((wide[..., hd:] == 3.0).all())
 
 
-def test_attention_ignores_what_masked_rows_hold():
+@pytest.mark.parametrize("B,P", [(2, 70), (16, 12007)])
+def test_attention_ignores_what_masked_rows_hold(B, P):
     """NaN and infinities past a sequence's length, and in tokens that only later queries see."""
     g = gen(5)
-    B, Tq, H, Hkv, hd, P, S = 2, 4, 4, 2, 128, 70, 80
+    Tq, H, Hkv, hd, S = 4, 4, 2, 128, 80
     q, kp, vp = normal(g, B, Tq, H, hd), normal(g, Hkv, P, hd), normal(g, Hkv, P, hd)
     k, v = normal(g, B, Hkv, S, hd), normal(g, B, Hkv, S, hd)
-    lens, qn = [50, 33], [4, 3]
+    lens, qn = [50, 33] * (B // 2), [4, 3] * (B // 2)
     clean, clse = check_attention(q, kp, vp, k, v, lens, qn)
     for b in range(B):
         k[b, :, lens[b]:] = NAN
@@ -189,21 +205,24 @@ def test_attention_non_finite_scores():
     assert bool((out[0, 0, 1] == 0).all()) and float(lse[0, 0, 1]) == -INF
 
 
-def test_attention_clamps_bad_lengths():
+@pytest.mark.parametrize("B,P", [(3, 40), (24, 31007)])
+def test_attention_clamps_bad_lengths(B, P):
     g = gen(7)
-    q, kp, vp = normal(g, 3, 2, 4, 64), normal(g, 2, 40, 64), normal(g, 2, 40, 64)
-    k, v = normal(g, 3, 2, 24, 64), normal(g, 3, 2, 24, 64)
-    a, al = fl.prefix_attention(q, kp, vp, k, v, ints([24, 0, 24]), q_lens=ints([2, 2, 0]))
-    b, bl = fl.prefix_attention(q, kp, vp, k, v, ints([1000000, -5, 24]), q_lens=ints([77, 2, -3]))
+    q, kp, vp = normal(g, B, 2, 4, 64), normal(g, 2, P, 64), normal(g, 2, P, 64)
+    k, v = normal(g, B, 2, 24, 64), normal(g, B, 2, 24, 64)
+    n = B // 3
+    a, al = fl.prefix_attention(q, kp, vp, k, v, ints([24, 0, 24] * n), q_lens=ints([2, 2, 0] * n))
+    b, bl = fl.prefix_attention(q, kp, vp, k, v, ints([1000000, -5, 24] * n), q_lens=ints([77, 2, -3] * n))
     assert torch.equal(a, b) and torch.equal(al, bl)
 
 
-def test_attention_streams_graphs_and_scratch():
+@pytest.mark.parametrize("B,P", [(4, 3000), (24, 8001)])
+def test_attention_streams_graphs_and_scratch(B, P):
     """The same bits on another stream, replayed from a graph with new inputs, and with a dirty scratch buffer."""
     g = gen(8)
-    B, Tq, H, Hkv, hd, P, S = 4, 2, 8, 2, 128, 3000, 500
+    Tq, H, Hkv, hd, S = 2, 8, 2, 128, 500
     q, kp, vp = normal(g, B, Tq, H, hd), normal(g, Hkv, P, hd), normal(g, Hkv, P, hd)
-    k, v, lens = normal(g, B, Hkv, S, hd), normal(g, B, Hkv, S, hd), ints([500, 2, 77, 300])
+    k, v, lens = normal(g, B, Hkv, S, hd), normal(g, B, Hkv, S, hd), ints([500, 2, 77, 300] * (B // 4))
     want, wl = fl.prefix_attention(q, kp, vp, k, v, lens)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -221,7 +240,7 @@ def test_attention_streams_graphs_and_scratch():
     torch.cuda.synchronize()
     assert torch.equal(o2, want) and torch.equal(l2, wl)
     q2.copy_(normal(g, B, Tq, H, hd))
-    lens.copy_(ints([3, 500, 9, 2]))
+    lens.copy_(ints([3, 500, 9, 2] * (B // 4)))
     graph.replay()
     want, wl = fl.prefix_attention(q2, kp, vp, k, v, lens)
     torch.cuda.synchronize()
@@ -467,6 +486,27 @@ def test_verify_large_calls_skip_only_what_decides_nothing():
     for _ in range(3):
         tok, acc = fl.verify_draft(logits, dl, draft, u, scratch=scratch)
         assert np.array_equal(tok.cpu().numpy(), wt) and np.array_equal(acc.cpu().numpy(), wa)
+
+
+def test_verify_large_calls_stop_at_rejections():
+    """The same beyond the size from which rows behind a rejection are not read (350 MB of logits), with unequal draft
+    counts, and without draft probabilities."""
+    B, D, V = 24, 8, 230003
+    g = gen(41)
+    logits = 3.0 * torch.randn((B, D + 1, V), generator=g, device="cuda")
+    draft = logits[:, :D].argmax(-1).to(torch.int32)
+    dl = logits[:, :D] - 0.2 * torch.rand((B, D, 1), generator=g, device="cuda")
+    dl.scatter_add_(2, draft.long()[..., None], torch.full((B, D, 1), 0.1, device="cuda"))
+    u = torch.rand((B, D + 1), generator=g, device="cuda")
+    n_draft = ints([D, 0, 3, 1] * (B // 4))
+    scratch = torch.full((fl.verify_draft_scratch_bytes(B, D, V),), 255, dtype=torch.uint8, device="cuda")
+    wt, wa = check_verify(logits, dl, draft, u, n_draft, 1.0)
+    for _ in range(3):
+        tok, acc = fl.verify_draft(logits, dl, draft, u, n_draft=n_draft, scratch=scratch)
+        assert np.array_equal(tok.cpu().numpy(), wt) and np.array_equal(acc.cpu().numpy(), wa)
+    logits = torch.cat([logits, logits], 1)[:, :D + 1 + 5].contiguous()   # 13 drafts of one row of logits each
+    draft = torch.cat([draft, draft], 1)[:, :D + 5].contiguous()
+    check_verify(logits, None, draft, torch.rand((B, D + 6), generator=g, device="cuda") ** 8, None, 0.3)
 
 
 def test_verify_border_random_numbers():
