@@ -95,8 +95,9 @@ __device__ __forceinline__ int len_of(const PrefixArgs& a, int b) {
 
 // The valid queries of the batch, packed: query number i of all sequences'
 // first q_lens[b] ones, i in [first, first + count), as slots b * Tq + t (-1 past
-// the last).  Called by one warp; returns how many there are in all.
-__device__ int pack_queries(const PrefixArgs& a, int first, int count, int* slot) {
+// the last).  Called by one warp with the lanes' q_len_of sequences 0..31 (0 past the last); returns how
+// many queries there are in all.
+__device__ int pack_queries(const PrefixArgs& a, int first, int count, int n, int* slot) {
   const int lane = threadIdx.x & 31;
   if (!a.q_lens) {
     const int total = a.B * a.Tq;
@@ -107,7 +108,7 @@ __device__ int pack_queries(const PrefixArgs& a, int first, int count, int* slot
   __syncwarp();
   int base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int n = b0 + lane < a.B ? q_len_of(a, b0 + lane) : 0;
+    if (b0) n = b0 + lane < a.B ? q_len_of(a, b0 + lane) : 0;
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -165,7 +166,8 @@ __global__ void __launch_bounds__(128, 2)
   uint8_t* qsm = ring + kPxRing;
   __shared__ __align__(8) uint64_t full[kPxWarps][12];
   __shared__ int slot_sm[RB + 1];
-  __shared__ long long row_id[RB];
+  __shared__ long long row_id[RB], q_at[RB];   // of a row: its number in the call (-1: none), its place in q
+  __shared__ float sm_w[RB][kPxWarps];
   __shared__ float sm_m[kPxWarps][RB], sm_l[kPxWarps][RB];
   __shared__ int n_valid_sm, bad_sm;
   static_assert(SLOTS <= 12, "barriers");
@@ -193,15 +195,19 @@ __global__ void __launch_bounds__(128, 2)
   const int g = it % a.Hkv, b = it / a.Hkv;
   const int r0 = rb * RB;
   int ncols = a.P, nrows;
+  int ql = 0;   // (pre: of the lane's sequence, for pack_queries)
   if (!pre) {
-    const int ql = q_len_of(a, b), len = len_of(a, b);
+    const int len = len_of(a, b);
+    ql = q_len_of(a, b);
     nrows = ql * a.G;
     ncols = min(max(len - ql + 1, 0), len);
+  } else if (warp == 0 && lane < a.B) {
+    ql = q_len_of(a, lane);
   }
   // ---- this warp's tiles, the first of them requested while the rows are still being looked up
   const int ntiles = (ncols + kPxTile - 1) / kPxTile;
-  const int tb = static_cast<int>(static_cast<long long>(sp) * ntiles / nsp);
-  const int te = static_cast<int>(static_cast<long long>(sp + 1) * ntiles / nsp);
+  const int tb = static_cast<int>(quick_div(static_cast<long long>(sp) * ntiles, nsp));
+  const int te = static_cast<int>(quick_div(static_cast<long long>(sp + 1) * ntiles, nsp));
   const int mine = te - tb > warp ? (te - tb - warp + kPxWarps - 1) / kPxWarps : 0;
   const CUtensorMap* km = pre ? &kp : &ks;
   const CUtensorMap* vm = pre ? &vp : &vs;
@@ -226,21 +232,26 @@ __global__ void __launch_bounds__(128, 2)
     __syncwarp();
     if (lane == 0 && issued < 2 * mine) issue(issued++);
   };
+  auto place = [&](int slot, int in_group) {   // (thread tid's row)
+    const int h = g * a.G + in_group, sb = slot / a.Tq;
+    row_id[tid] = slot < 0 ? -1 : static_cast<long long>(slot) * a.H + h;
+    q_at[tid] = sb * a.q_sb + (slot - sb * a.Tq) * a.q_st + h * a.q_sh;
+  };
   if (pre) {
     const int first = r0 / a.G, count = (r0 + RB - 1) / a.G - first + 1;
     if (warp == 0) {
-      const int total = pack_queries(a, first, count, slot_sm);
+      const int total = pack_queries(a, first, count, ql, slot_sm);
       if (lane == 0) n_valid_sm = total;
     }
     __syncthreads();
     nrows = n_valid_sm * a.G;
     if (tid < RB) {
-      const int s = r0 + tid < nrows ? slot_sm[(r0 + tid) / a.G - first] : -1;
-      row_id[tid] = s < 0 ? -1 : static_cast<long long>(s) * a.H + g * a.G + (r0 + tid) % a.G;
+      const int q = (r0 + tid) / a.G;
+      place(r0 + tid < nrows ? slot_sm[q - first] : -1, r0 + tid - q * a.G);
     }
   } else if (tid < RB) {
-    const int r = r0 + tid;
-    row_id[tid] = r < nrows ? (static_cast<long long>(b) * a.Tq + r / a.G) * a.H + g * a.G + r % a.G : -1;
+    const int q = (r0 + tid) / a.G;
+    place(r0 + tid < nrows ? b * a.Tq + q : -1, r0 + tid - q * a.G);
   }
   __syncthreads();   // row_id
   if (r0 >= nrows) {
@@ -251,13 +262,12 @@ __global__ void __launch_bounds__(128, 2)
   }
 
   // ---- queries to shared memory (rows past the last: zero)
+#pragma unroll
   for (int e = tid; e < RB * (HD / 8); e += 128) {
     const int r = e / (HD / 8), c = e % (HD / 8);
-    const long long id = row_id[r];
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-    if (id >= 0) {
-      const long long s = id / a.H, h = id % a.H;
-      const long long off = (s / a.Tq) * a.q_sb + (s % a.Tq) * a.q_st + h * a.q_sh + c * 8;
+    if (row_id[r] >= 0) {
+      const long long off = q_at[r] + c * 8;
       if (!HILO) {
         hi = *reinterpret_cast<const uint4*>(a.q + off);
       } else {
@@ -423,31 +433,38 @@ __global__ void __launch_bounds__(128, 2)
       *reinterpret_cast<float2*>(d0) = make_float2(acc[i][n][0], acc[i][n][1]);
       *reinterpret_cast<float2*>(d0 + 8 * OLD) = make_float2(acc[i][n][2], acc[i][n][3]);
     }
-  __syncthreads();
   const long long split = pre ? sp : a.n_p + sp;
+  if (tid < RB) {
+    const long long id = row_id[tid];
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPxWarps; ++w) M = fmaxf(M, sm_m[w][tid]);
+    const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < kPxWarps; ++w) {
+      const float wt = exp2f(sm_m[w][tid] - ms);
+      sm_w[tid][w] = wt;
+      L += wt * sm_l[w][tid];
+    }
+    if (id >= 0) a.part_ml[split * a.rows + id] = bad_sm ? make_float2(0.f, NAN) : make_float2(M, L);
+  }
+  __syncthreads();
+  // (a row with nothing finite too: the merge does not look at what stands behind a maximum of -inf)
+#pragma unroll 4
   for (int e = tid; e < RB * (HD / 4); e += 128) {
     const int r = e / (HD / 4), d = (e % (HD / 4)) * 4;
     const long long id = row_id[r];
-    if (id < 0) continue;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kPxWarps; ++w) M = fmaxf(M, sm_m[w][r]);
-    const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kPxWarps; ++w) {
-      const float wt = exp2f(sm_m[w][r] - ms);
+      const float wt = sm_w[r][w];
       const float4 x = *reinterpret_cast<const float4*>(om + (w * RB + r) * OLD + d);
-      L += wt * sm_l[w][r];
       o.x += wt * x.x;
       o.y += wt * x.y;
       o.z += wt * x.z;
       o.w += wt * x.w;
     }
-    if (M > -INFINITY || !(L == 0.f) || bad_sm)
-      *reinterpret_cast<float4*>(a.part_o + (split * a.rows + id) * HD + d) = o;
-    if (d == 0) a.part_ml[split * a.rows + id] = bad_sm ? make_float2(0.f, NAN) : make_float2(M, L);
+    if (id >= 0) *reinterpret_cast<float4*>(a.part_o + (split * a.rows + id) * HD + d) = o;
   }
   if (a.tc_ctas) pdl_wait();
 }
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   pdl_wait();
   pdl_trigger();   // (the next launch may run beside this one; see its wait)
   if (warp == 0) {
-    const int total = pack_queries(a, 0, 0, slot_sm);
+    const int total = pack_queries(a, 0, 0, lane < a.B ? q_len_of(a, lane) : 0, slot_sm);
     if (lane == 0) total_sm = total;
   }
   tc_fence_before();
@@ -599,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // (warps 0-16: the TMA warp is not waited for, nor does it read the queries)
     if (warp == 0) {
       const int first = r0 / a.G, count = (r0 + rows - 1) / a.G - first + 1;
-      pack_queries(a, first, count, slot_sm);
+      pack_queries(a, first, count, lane < a.B ? q_len_of(a, lane) : 0, slot_sm);
     }
     if (warp < 16) {
       asm volatile("bar.sync 1, 512;" ::: "memory");
