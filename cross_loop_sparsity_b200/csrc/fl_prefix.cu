@@ -1726,6 +1726,7 @@ using namespace fl;
 
 namespace {
 // Head shapes that the attention operators take.
+constexpr int kMaxCols = 1 << 30;   // columns of a prefix or a sequence (tile ends are held in 32 bits)
 bool heads_ok(int B, int Tq, int H, int Hkv, int hd) {
   return B >= 1 && Tq >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= kMaxGroup && (hd == 64 || hd == 128) &&
          Hkv <= 65535 && B <= 65535 && static_cast<long long>(B) * Tq * H <= (1LL << 30);
@@ -1735,14 +1736,14 @@ bool heads_ok(int B, int Tq, int H, int Hkv, int hd) {
 extern "C" {
 
 size_t flashloop_prefix_attention_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S) {
-  if (!heads_ok(B, Tq, H, Hkv, hd) || Tq > kMaxTq || P < 0 || S < 0) return 0;
+  if (!heads_ok(B, Tq, H, Hkv, hd) || Tq > kMaxTq || P < 0 || S < 0 || P > kMaxCols || S > kMaxCols) return 0;
   return prefix_scratch_bytes(B, Tq, H, Hkv, hd, P, S, false);
 }
 
 fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scratch, size_t scratch_bytes,
                                      fl_stream_t stream) {
   if (!a) return refuse(FL_ERR_INVALID_ARG, "NULL arguments");
-  if (!heads_ok(a->B, a->Tq, a->H, a->Hkv, a->hd) || a->Tq > kMaxTq || a->P < 0 || a->S < 0)
+  if (!heads_ok(a->B, a->Tq, a->H, a->Hkv, a->hd) || a->Tq > kMaxTq || a->P < 0 || a->S < 0 || a->P > kMaxCols || a->S > kMaxCols)
     return refuse(FL_ERR_INVALID_ARG, "B, Tq (<= 64), H, Hkv (H % Hkv == 0, H / Hkv <= 64), hd (64 or 128), P or S out of range");
   if (!std::isfinite(a->scale)) return refuse(FL_ERR_INVALID_ARG, "scale must be finite");
   if (!a->q || !a->out || !is_aligned(a->q, 16) || !is_aligned(a->out, 16) || !is_aligned(a->lse, 4) ||
@@ -1773,14 +1774,14 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
 }
 
 size_t flashloop_column_weights_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int S) {
-  if (!heads_ok(B, Tq, H, Hkv, hd) || S < 0) return 0;
+  if (!heads_ok(B, Tq, H, Hkv, hd) || S < 0 || S > kMaxCols) return 0;
   return plan_weights(B, Tq, H, Hkv, S).bytes;
 }
 
 fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratch, size_t scratch_bytes,
                                    fl_stream_t stream) {
   if (!a) return refuse(FL_ERR_INVALID_ARG, "NULL arguments");
-  if (!heads_ok(a->B, a->Tq, a->H, a->Hkv, a->hd) || a->S < 0)
+  if (!heads_ok(a->B, a->Tq, a->H, a->Hkv, a->hd) || a->S < 0 || a->S > kMaxCols)
     return refuse(FL_ERR_INVALID_ARG, "B, Tq, H, Hkv (H % Hkv == 0, H / Hkv <= 64), hd (64 or 128) or S out of range");
   if (!std::isfinite(a->scale)) return refuse(FL_ERR_INVALID_ARG, "scale must be finite");
   if (a->S == 0) return FL_OK;

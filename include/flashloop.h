@@ -391,8 +391,8 @@ fl_status fl_gemm_skinny_noalloc(const uint16_t* A, const uint16_t* B, float* D,
  * last visible one are never used, whatever they hold.
  *   q, out [B][Tq][H][hd]; k_prefix, v_prefix [Hkv][P][hd]; k, v [B][Hkv][S][hd]
  *   lse fp32 [B][Tq][H] contiguous, or NULL; lens int32 [B]; q_lens int32 [B], or NULL for Tq.
- * Limits: hd 64 or 128, H / Hkv <= 64, 1 <= Tq <= 64, q spans less than 2^34 elements, P >= 0, S >= 0 (k_prefix and
- * v_prefix, or k, v and lens, may be NULL where P, or S, is 0). */
+ * Limits: hd 64 or 128, H / Hkv <= 64, 1 <= Tq <= 64, q spans less than 2^34 elements, 0 <= P, S <= 2^30 (k_prefix
+ * and v_prefix, or k, v and lens, may be NULL where P, or S, is 0). */
 typedef struct {
   const uint16_t* q;
   const uint16_t* k_prefix;
@@ -425,7 +425,7 @@ fl_status flashloop_prefix_attention(const flashloop_prefix_args* a, void* scrat
  * value.  (A shared prefix is one sequence, B = 1, of B * Tq queries, lens NULL.)
  *   q bf16 [B][Tq][H][hd]; k bf16 [B][Hkv][S][hd]; lse fp32 [B][Tq][H], acc and out
  *   fp32 [B][Hkv][S], contiguous; out may be acc.
- * Limits: hd 64 or 128, H / Hkv <= 64, Tq >= 1, S >= 0. */
+ * Limits: hd 64 or 128, H / Hkv <= 64, Tq >= 1, 0 <= S <= 2^30. */
 typedef struct {
   const uint16_t* q;
   const uint16_t* k;

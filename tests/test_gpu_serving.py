@@ -625,3 +625,84 @@ def test_verify_writes_a_token_where_target_and_draft_differ_by_roundings(V):
     assert (n == 0).all()
     assert ((got[:, 0] >= -1) & (got[:, 0] < V)).all() and (got[:, 1:] == -1).all()
     assert (got[0::2, 0] == -1).all()   # equal rows: exactly nothing is left
+
+
+# ---------------------------------------------------------------------------- long strides
+@pytest.fixture(scope="module")
+def far():
+    """A bf16 buffer whose second part starts past 2^31 elements (2^32 bytes)."""
+    gap = 2 ** 31 + 4096
+    buf = torch.empty(gap + 2 ** 22, dtype=torch.bfloat16, device="cuda")
+    yield lambda x, dim: far_copy(buf, gap, x, dim)
+    del buf
+    torch.cuda.empty_cache()
+
+
+def far_copy(buf, gap, x, dim):
+    """x (two elements long in `dim`) with that dimension's stride past 2^31."""
+    assert x.shape[dim] == 2
+    strides = list(x.select(dim, 0).contiguous().stride())
+    strides.insert(dim, gap)
+    y = buf.as_strided(x.shape, strides)
+    y.copy_(x)
+    return y
+
+
+@pytest.mark.parametrize("B,P", [(3, 200), (40, 9473)])
+def test_attention_offsets_past_32_bits(far, B, P):
+    """KV heads further apart than 2^31 elements, for either kernel of the prefix: the bits of adjacent ones."""
+    g = gen(51)
+    q, kp, vp = normal(g, B, 2, 8, 128), normal(g, 2, P, 128), normal(g, 2, P, 128)
+    k, v, lens = normal(g, B, 2, 70, 128), normal(g, B, 2, 70, 128), ints([70 - 2 * (i % 30) for i in range(B)])
+    want, wl = fl.prefix_attention(q, kp, vp, k, v, lens)
+    for i, x in enumerate((kp, vp)):
+        got, gl = fl.prefix_attention(q, *[far(y, 0) if j == i else y for j, y in enumerate((kp, vp))], k, v, lens)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+    for i in range(2):
+        got, gl = fl.prefix_attention(q, kp, vp, *[far(y, 1) if j == i else y for j, y in enumerate((k, v))], lens)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
+@pytest.mark.parametrize("Tq", [1, 40])
+def test_column_weights_offsets_past_32_bits(far, Tq):
+    g = gen(52)
+    q, k = normal(g, 2, Tq, 8, 64), normal(g, 2, 2, 700, 64)
+    lse, acc, lens = torch.full((2, Tq, 8), 7.0, device="cuda"), torch.rand((2, 2, 700), device="cuda"), ints([700, 333])
+    want = fl.column_weights(q, k, lse, acc, lens=lens)
+    assert torch.equal(fl.column_weights(q, far(k, 0), lse, acc, lens=lens), want)
+    assert torch.equal(fl.column_weights(far(q, 0), k, lse, acc, lens=lens), want)
+
+
+def test_evict_offsets_past_32_bits(far):
+    g = gen(53)
+    B, Hkv, S, hd, keep = 2, 2, 900, 64, 500
+    k, v, acc, pos = evict_inputs(g, B, Hkv, S, hd, False)
+    lens = ints([900, 777])
+    want = fl.evict(*[x.clone() for x in (k, v, acc, pos, lens)], keep, recent=9, sinks=2)
+    y = far(k, 0)
+    got = fl.evict(y, v.clone(), acc.clone(), pos.clone(), lens.clone(), keep, recent=9, sinks=2)   # in place
+    for a, b in zip(got, want):
+        assert torch.equal(a[:, :, :keep] if a.dim() > 1 else a, b[:, :, :keep] if b.dim() > 1 else b)
+    y = far(v, 0)
+    out = (torch.empty_like(k[:, :, :keep].contiguous()), torch.empty_like(k[:, :, :keep].contiguous()),
+           torch.empty((B, Hkv, keep), device="cuda"), torch.empty((B, Hkv, keep), dtype=torch.int32, device="cuda"),
+           torch.empty_like(lens))
+    for a, b in zip(fl.evict(k, y, acc, pos, lens, keep, recent=9, sinks=2, out=out), want):
+        assert torch.equal(a, b[:, :, :keep] if b.dim() > 1 else b)
+
+
+def test_verify_offsets_past_32_bits():
+    gap = 2 ** 31 + 4097
+    buf = torch.empty(gap + 10 ** 6, device="cuda")
+    logits, dl, draft, u = verify_inputs(54, 2, 3, 5003, 1.0)
+    want = fl.verify_draft(logits, dl, draft, u)
+    for which in range(2):
+        x = (logits, dl)[which]
+        y = buf.as_strided(x.shape, (gap, 5003, 1))
+        y.copy_(x)
+        got = fl.verify_draft(y if which == 0 else logits, y if which == 1 else dl, draft, u)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y = buf.as_strided(logits.shape, (gap, 5003, 1))
+    y.copy_(logits)
+    greedy = fl.verify_draft(logits, None, draft, None, temperature=0.0)
+    assert all(torch.equal(a, b) for a, b in zip(fl.verify_draft(y, None, draft, None, temperature=0.0), greedy))

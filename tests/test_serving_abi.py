@@ -58,11 +58,12 @@ BAD = {
         dict(lse=PTR + 1), dict(k_prefix=None), dict(v_prefix=PTR + 4), dict(k=None), dict(v=PTR + 8), dict(lens=None),
         dict(q_stride=fl._I3(3 * 1024, 1023, 128)), dict(q_stride=fl._I3(0, 1024, 128)),
         dict(out_stride=fl._I3(3 * 1024, 1024, -128)), dict(kp_stride=fl._I2(12800, 4)),
-        dict(v_stride=fl._I3(12800, 6400, 0)), dict(q_stride=fl._I3(1 << 34, 1024, 128)), dict(B=1 << 20, Tq=64, H=64, Hkv=1)]),
+        dict(v_stride=fl._I3(12800, 6400, 0)), dict(q_stride=fl._I3(1 << 34, 1024, 128)), dict(B=1 << 20, Tq=64, H=64, Hkv=1), dict(P=(1 << 30) + 1),
+        dict(S=(1 << 30) + 1)]),
     "column_weights": (weights, [
         dict(B=0), dict(Tq=0), dict(H=9), dict(hd=32), dict(S=-1), dict(scale=INF), dict(q=None), dict(k=PTR + 8),
         dict(lse=None), dict(acc=None), dict(out=PTR + 2), dict(lens=PTR + 1), dict(k_stride=fl._I3(12800, 6400, 100)),
-        dict(q_stride=fl._I3(-8, 1024, 128))]),
+        dict(q_stride=fl._I3(-8, 1024, 128)), dict(S=2 ** 31 - 1)]),
     "evict": (evict, [
         dict(B=0), dict(Hkv=0), dict(S=0), dict(S=262145), dict(keep=0), dict(hd=12), dict(hd=2048), dict(recent=-1),
         dict(sinks=-1), dict(recent=19, sinks=2), dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), dict(k=None),
