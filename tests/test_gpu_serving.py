@@ -706,3 +706,72 @@ def test_verify_offsets_past_32_bits():
     y.copy_(logits)
     greedy = fl.verify_draft(logits, None, draft, None, temperature=0.0)
     assert all(torch.equal(a, b) for a, b in zip(fl.verify_draft(y, None, draft, None, temperature=0.0), greedy))
+
+
+# ---------------------------------------------------------------------------- calls side by side
+def operator_calls(seed):
+    """One call of each operator as call(scratch) -> outputs, and its scratch bytes; sizes that take each kernel."""
+    g = gen(seed)
+    calls = []
+    for B, P in ((5, 300), (40, 9473)):   # warp tiles; tensor cores
+        q, kp, vp = normal(g, B, 1, 16, 128), normal(g, 2, P, 128), normal(g, 2, P, 128)
+        k, v, lens = normal(g, B, 2, 90, 128), normal(g, B, 2, 90, 128), ints([90 - i for i in range(B)])
+        calls.append((lambda s, x=(q, kp, vp, k, v, lens): fl.prefix_attention(*x, scratch=s),
+                      fl.prefix_attention_scratch_bytes(B, 1, 16, 2, 128, P, 90)))
+    for Tq in (1, 60):
+        q, k = normal(g, 2, Tq, 8, 128), normal(g, 2, 2, 3001, 128)
+        lse, acc = torch.full((2, Tq, 8), 8.0, device="cuda"), torch.rand((2, 2, 3001), device="cuda", generator=g)
+        calls.append((lambda s, x=(q, k, lse, acc): (fl.column_weights(*x, scratch=s),),
+                      fl.column_weights_scratch_bytes(2, Tq, 8, 2, 128, 3001)))
+    for S, keep in ((700, 600), (20000, 3001)):   # one CTA, a cluster
+        k, v, acc, pos = evict_inputs(g, 2, 2, S, 64, True)
+        lens = ints([S, S - 90])
+
+        def evict(s, x=(k, v, acc, pos, lens), keep=keep):
+            out = tuple(torch.zeros_like(t[:, :, :keep]) if t.dim() > 1 else torch.zeros_like(t) for t in x)
+            return fl.evict(*x, keep, recent=5, sinks=1, out=out, scratch=s)
+        calls.append((evict, fl.evict_scratch_bytes(2, 2, S, keep)))
+    for B, D, V in ((3, 4, 5003), (24, 6, 300007)):   # every row; up to the first rejection
+        x = verify_inputs(seed, B, D, V, 1.0)
+        calls.append((lambda s, x=x: fl.verify_draft(*x, scratch=s), fl.verify_draft_scratch_bytes(B, D, V)))
+    return calls
+
+
+def test_calls_on_two_streams_at_once():
+    """Every operator on two streams at the same time, each with its own scratch: the bits of calls made alone."""
+    one, two = operator_calls(61), operator_calls(62)
+    alone = [[f(None) for f, _ in calls] for calls in (one, two)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(3):
+        for i, calls in enumerate((one, two)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append([f(torch.empty(n, dtype=torch.uint8, device="cuda")) for f, n in calls])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for rep in got[i]:
+            for a, b in zip(rep, alone[i]):
+                assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_two_graphs_share_a_scratch_buffer():
+    """Two captured sequences of all operators with one scratch buffer, replayed in turn."""
+    both = [operator_calls(63), operator_calls(64)]
+    alone = [[f(None) for f, _ in calls] for calls in both]
+    scratch = torch.full((max(n for calls in both for _, n in calls),), 170, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for calls in both:
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append([f(scratch) for f, _ in calls])
+        graphs.append(graph)
+    for _ in range(2):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(outs, alone):
+        for x, y in zip(a, b):
+            assert all(torch.equal(s, t) for s, t in zip(x, y))
+
