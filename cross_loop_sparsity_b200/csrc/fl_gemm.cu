@@ -853,39 +853,45 @@ bool encode_tmap_bf16(CUtensorMap* map, const void* base, uint64_t k, uint64_t r
   return r == CUDA_SUCCESS;
 }
 
-namespace {
-bool encode_tmap_4d(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2, int64_t s_row,
-                    int64_t s1, int64_t s2, uint32_t box_rows, uint32_t box_1) {
+bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2, int64_t s_row,
+                      int64_t s1, int64_t s2, uint32_t box_rows) {
   EncodeFn fn = get_encode();
-  if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || hd % 64 || rows < 1 || n1 < 1 || n2 < 1 ||
-      box_rows == 0 || box_rows > 256 || box_1 == 0 || box_1 > 256)
+  if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || hd % 64 || rows < 1 || n1 < 1 || n2 < 1 || box_rows == 0 ||
+      box_rows > 256)
     return false;
   // the stride of a dimension of one element is never used; give it a valid value
   if (rows == 1) s_row = hd;
   if (n1 == 1) s1 = s_row;
   if (n2 == 1) s2 = s1;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(n1),
+  const cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(hd / 64), static_cast<cuuint64_t>(n1),
                               static_cast<cuuint64_t>(n2)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s_row) * 2, static_cast<cuuint64_t>(s1) * 2,
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(s_row) * 2, 128, static_cast<cuuint64_t>(s1) * 2,
                                  static_cast<cuuint64_t>(s2) * 2};
-  const cuuint32_t box[4] = {64, box_rows, box_1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
-         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-}  // namespace
-
-bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2, int64_t s_row,
-                      int64_t s1, int64_t s2, uint32_t box_rows) {
-  return encode_tmap_4d(map, base, hd, rows, n1, n2, s_row, s1, s2, box_rows, 1);
+  const cuuint32_t box[5] = {64, box_rows, static_cast<cuuint32_t>(hd / 64), 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool encode_tmap_queries(CUtensorMap* map, const void* base, int hd, int H, int Tq, int B, int64_t s_h, int64_t s_t,
                          int64_t s_b, uint32_t box_heads, uint32_t box_queries) {
-  return encode_tmap_4d(map, base, hd, H, Tq, B, s_h, s_t, s_b, box_heads, box_queries);
+  EncodeFn fn = get_encode();
+  if (!fn || !base || (reinterpret_cast<uintptr_t>(base) & 15) || hd % 64 || H < 1 || Tq < 1 || B < 1 || box_heads == 0 ||
+      box_heads > 256 || box_queries == 0 || box_queries > 256)
+    return false;
+  // the stride of a dimension of one element is never used; give it a valid value
+  if (H == 1) s_h = hd;
+  if (Tq == 1) s_t = s_h;
+  if (B == 1) s_b = s_t;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(Tq),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(s_h) * 2, static_cast<cuuint64_t>(s_t) * 2,
+                                 static_cast<cuuint64_t>(s_b) * 2};
+  const cuuint32_t box[4] = {64, box_heads, box_queries, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace fl

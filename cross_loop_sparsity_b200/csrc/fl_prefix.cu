@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(128, 2)
     k_prefix_split(const __grid_constant__ CUtensorMap kp, const __grid_constant__ CUtensorMap vp,
                    const __grid_constant__ CUtensorMap ks, const __grid_constant__ CUtensorMap vs, const PrefixArgs a) {
   constexpr int RB = 16 * NM;                       // query rows
-  constexpr int NB = HD / 64;                       // 128-byte boxes per row
   constexpr int TILE_BYTES = kPxTile * HD * 2;      // K or V of one tile
   constexpr int SLOTS = kPxRing / kPxWarps / TILE_BYTES;   // a warp's ring: K_0 V_0 K_1 V_1 .., a slot each
   constexpr int QBYTES = RB * HD * 2;
@@ -217,8 +216,7 @@ __global__ void __launch_bounds__(128, 2)
     const uint32_t st = smem_u32(wring + (n % SLOTS) * TILE_BYTES), fb = smem_u32(&full[warp][n % SLOTS]);
     const CUtensorMap* map = (n & 1) ? vm : km;
     mbar_arrive_expect_tx(fb, TILE_BYTES);
-#pragma unroll
-    for (int bx = 0; bx < NB; ++bx) tma_load_4d(st + bx * kPxTile * 128, map, fb, bx * 64, y, g, pre ? 0 : b);
+    tma_load_5d(st, map, fb, 0, y, 0, g, pre ? 0 : b);
   };
   int issued = 0;             // (lane 0)
   if (lane == 0 && (pre || r0 < nrows))
@@ -506,7 +504,7 @@ template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_prefix_tc(const __grid_constant__ CUtensorMap kp, const __grid_constant__ CUtensorMap vp, const PrefixArgs a) {
   using C = TcSmem<HD>;
-  constexpr int NB = HD / 64, KS = C::kKSlots, VS = C::kVSlots;
+  constexpr int KS = C::kKSlots, VS = C::kVSlots;
   constexpr int OLD = HD + 4;                            // padded row of the join buffer
   // no static shared memory: the tiles start at the (1024-byte aligned) start of the block's, which they nearly fill
   extern __shared__ __align__(1024) uint8_t tc_sm[];
@@ -586,15 +584,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto load_k = [&](int i) {                 // (TMA thread)
       const uint32_t bar = smem_u32(&k_full[nk % KS]), dst = smem_u32(ksm + (nk % KS) * C::kTileBytes);
       mbar_arrive_expect_tx(bar, C::kTileBytes);
-#pragma unroll
-      for (int bx = 0; bx < NB; ++bx) tma_load_4d(dst + bx * C::kBox, &kp, bar, bx * 64, (t0 + i) * kTcTile, g, 0);
+      tma_load_5d(dst, &kp, bar, 0, (t0 + i) * kTcTile, 0, g, 0);
       ++nk;
     };
     auto load_v = [&](int i) {
       const uint32_t bar = smem_u32(&v_full[nv % VS]), dst = smem_u32(vsm + (nv % VS) * C::kTileBytes);
       mbar_arrive_expect_tx(bar, C::kTileBytes);
-#pragma unroll
-      for (int bx = 0; bx < NB; ++bx) tma_load_4d(dst + bx * C::kBox, &vp, bar, bx * 64, (t0 + i) * kTcTile, g, 0);
+      tma_load_5d(dst, &vp, bar, 0, (t0 + i) * kTcTile, 0, g, 0);
       ++nv;
     };
     // ---- the segment's queries (every thread); the K and V rings fill meanwhile
@@ -1127,7 +1123,7 @@ struct Seen {
 constexpr int kWsWarps = 8, kWsStages = 3;
 template <int HD, int NM>
 __global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_constant__ CUtensorMap km, const WeightsArgs a) {
-  constexpr int NB = HD / 64, STAGE = kPxTile * HD * 2;
+  constexpr int STAGE = kPxTile * HD * 2;
   extern __shared__ uint8_t sm_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[kWsWarps][kWsStages];
@@ -1146,9 +1142,7 @@ __global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_c
     const int st = static_cast<int>((u - u0) % kWsStages), pair = static_cast<int>(u / tiles);
     const uint32_t dst = smem_u32(wring + st * STAGE), bar = smem_u32(&full[warp][st]);
     mbar_arrive_expect_tx(bar, STAGE);
-#pragma unroll
-    for (int bx = 0; bx < NB; ++bx)
-      tma_load_4d(dst + bx * kPxTile * 128, &km, bar, bx * 64, static_cast<int>(u % tiles) * kPxTile, pair % a.Hkv, pair / a.Hkv);
+    tma_load_5d(dst, &km, bar, 0, static_cast<int>(u % tiles) * kPxTile, 0, pair % a.Hkv, pair / a.Hkv);
   };
   long long last = u0 - 1;   // the last tile requested (lane 0)
   if (lane == 0)
@@ -1482,9 +1476,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       if (!ok) break;
       ++segs;
       mbar_arrive_expect_tx(smem_u32(&k_full[ks]), 2 * C::kTile);
-      for (int i = 0; i < 2 * NB; ++i)   // (keys past the tensor's last read as zero)
-        tma_load_4d(smem_u32(ksm) + ks * 2 * C::kTile + i * C::kBox, &km, smem_u32(&k_full[ks]), (i % NB) * 64,
-                    sg.col0 + i / NB * 128, sg.g, sg.b);
+      for (int i = 0; i < 2; ++i)   // (keys past the tensor's last read as zero)
+        tma_load_5d(smem_u32(ksm) + (ks * 2 + i) * C::kTile, &km, smem_u32(&k_full[ks]), 0, sg.col0 + i * 128, 0, sg.g, sg.b);
       for (int n = 0; n < sg.count; ++n) {
         const int st = blocks % QS;
         ok = blocks < QS || mbar_wait(smem_u32(&q_empty[st]), (blocks / QS - 1) & 1, nullptr);

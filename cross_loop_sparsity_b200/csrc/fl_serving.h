@@ -37,8 +37,8 @@ inline bool stride_ok(int64_t stride, int64_t dim, int64_t unit) {
   return dim <= 1 || (stride > 0 && stride % unit == 0 && stride < (int64_t(1) << 38));
 }
 
-// Tensor map over bf16 rows [n2][n1][rows][hd] with element strides, 128-byte
-// swizzle, box 64 dims x box_rows rows.
+// Tensor map over bf16 rows [n2][n1][rows][hd] with element strides, as [n2][n1][hd / 64][rows][64]: one copy brings
+// box_rows rows of all dims, the halves of a 128-dim row one behind the other, 128-byte swizzle.
 bool encode_tmap_rows(CUtensorMap* map, const void* base, int hd, int64_t rows, int64_t n1, int64_t n2,
                       int64_t s_row, int64_t s1, int64_t s2, uint32_t box_rows);
 
