@@ -40,7 +40,7 @@ struct PrefixArgs {
   float scale2;           // scale * log2(e): the softmax runs in powers of two
   int rb_p, n_p;          // prefix: row blocks per KV head, column splits
   int rb_s, n_s;          // own rows: row blocks per (sequence, KV head), column splits
-  int items_p;            // CTAs of the prefix part
+  int items_p;            // row blocks x splits of the prefix part (CTAs, or warps of k_prefix_rows)
   long long rows;         // B * Tq * H
   float* part_o;          // [n_p + n_s][rows][hd]
   float2* part_ml;        // [n_p + n_s][rows]: max (log2 domain), sum
@@ -133,6 +133,142 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// One warp's tiles: scores, running softmax and products for its 16 NM query rows (bf16 in shared memory at qs,
+// HILO: their low parts QBYTES behind).  tile(n): where load n lies (K even, V odd); columns(i): those of tile i that
+// are in range; arrived(n), refill(): wait for a load, give its slot to the next.  Returns the tiles
+// done, fewer than `mine` when a load never arrived.
+template <int HD, int NM, bool HILO, class Tile, class Columns, class Arrived, class Refill>
+__device__ __forceinline__ int warp_tiles(int mine, uint32_t qs, float scale2, Tile tile, Columns columns, Arrived arrived,
+                                          Refill refill, float (&m_run)[NM][2], float (&l_run)[NM][2],
+                                          float (&acc)[NM][HD / 8][4]) {
+  constexpr int RB = 16 * NM, QBYTES = RB * HD * 2, NT = HD / 8;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < NM; ++i) {
+    m_run[i][0] = m_run[i][1] = -INFINITY;
+    l_run[i][0] = l_run[i][1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
+  }
+  int done = 0;
+  for (; done < mine; ++done) {
+    if (!arrived(2 * done)) break;
+    const uint32_t Kt = smem_u32(tile(2 * done));
+    const int nc = min(kPxTile, columns(done));   // columns of this tile in range
+    // ---- scores of the tile's 32 keys
+    float s[NM][4][4] = {};
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+      uint32_t kf[2][4];
+#pragma unroll
+      for (int n2 = 0; n2 < 2; ++n2)
+        ldsm_x4(Kt + sw_off(kPxTile, n2 * 16 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), kf[n2]);
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
+#pragma unroll
+        for (int part = 0; part < (HILO ? 2 : 1); ++part) {
+          uint32_t qf[4];
+          ldsm_x4(qs + part * QBYTES + sw_off(RB, i * 16 + (lane & 15), k * 2 + (lane >> 4)), qf);
+#pragma unroll
+          for (int n2 = 0; n2 < 2; ++n2) {
+            mma_bf16_16816(s[i][n2 * 2], qf, kf[n2][0], kf[n2][1]);
+            mma_bf16_16816(s[i][n2 * 2 + 1], qf, kf[n2][2], kf[n2][3]);
+          }
+        }
+      }
+    }
+    refill();
+    // ---- running softmax: thread holds rows lane/4 (+8), columns 8n + 2(lane%4) + {0, 1}
+    uint32_t pf[NM][2][4], pl[HILO ? NM : 1][2][4];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[i][n][e] * scale2;
+          if (nc < kPxTile && n * 8 + 2 * (lane & 3) + (e & 1) >= nc) x = -INFINITY;
+          s[i][n][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      float al[2], ms[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+        const float mn = fmaxf(m_run[i][e], mx[e]);
+        ms[e] = mn == -INFINITY ? 0.f : mn;   // nothing finite yet: weights of 0, not NaN
+        al[e] = exp2f(m_run[i][e] - ms[e]);
+        m_run[i][e] = mn;
+        l_run[i][e] *= al[e];
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = exp2f(s[i][n][e] - ms[e >> 1]);
+          s[i][n][e] = p;
+          l_run[i][e >> 1] += p;
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        acc[i][n][0] *= al[0];
+        acc[i][n][1] *= al[0];
+        acc[i][n][2] *= al[1];
+        acc[i][n][3] *= al[1];
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = s[i][2 * k + (j >> 1)][(j & 1) * 2], x1 = s[i][2 * k + (j >> 1)][(j & 1) * 2 + 1];
+          pf[i][k][j] = pack_bf16x2(x0, x1);
+          if (HILO)
+            pl[HILO ? i : 0][k][j] = pack_bf16x2(x0 - bf16_to_f(pf[i][k][j] & 0xFFFF), x1 - bf16_to_f(pf[i][k][j] >> 16));
+        }
+    }
+    // ---- output += P V
+    if (!arrived(2 * done + 1)) break;
+    uint8_t* vt = tile(2 * done + 1);
+    const uint32_t Vt = smem_u32(vt);
+    if (nc < kPxTile) {
+      // rows past the range (another query's tokens, or never written): their
+      // probabilities are 0, and 0 times what they hold must stay 0
+      for (int e = lane; e < (kPxTile - nc) * (HD / 8); e += 32)
+        *reinterpret_cast<uint4*>(vt + sw_off(kPxTile, nc + e / (HD / 8), e % (HD / 8))) = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int n2 = 0; n2 < NT / 2; ++n2) {
+        uint32_t vf[4];
+        ldsm_x4_t(Vt + sw_off(kPxTile, k * 16 + (lane & 15), n2 * 2 + (lane >> 4)), vf);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          mma_bf16_16816(acc[i][n2 * 2], pf[i][k], vf[0], vf[1]);
+          mma_bf16_16816(acc[i][n2 * 2 + 1], pf[i][k], vf[2], vf[3]);
+          if (HILO) {
+            mma_bf16_16816(acc[i][n2 * 2], pl[HILO ? i : 0][k], vf[0], vf[1]);
+            mma_bf16_16816(acc[i][n2 * 2 + 1], pl[HILO ? i : 0][k], vf[2], vf[3]);
+          }
+        }
+      }
+    }
+    refill();
+  }
+  // the sums of a row, over its four lanes
+#pragma unroll
+  for (int i = 0; i < NM; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l_run[i][e] += __shfl_xor_sync(0xffffffffu, l_run[i][e], 1);
+      l_run[i][e] += __shfl_xor_sync(0xffffffffu, l_run[i][e], 2);
+    }
+  return done;
 }
 
 // ============================================================================
@@ -287,122 +423,9 @@ __global__ void __launch_bounds__(128, 2)
   __syncthreads();
 
   float m_run[NM][2], l_run[NM][2], acc[NM][NT][4];
-#pragma unroll
-  for (int i = 0; i < NM; ++i) {
-    m_run[i][0] = m_run[i][1] = -INFINITY;
-    l_run[i][0] = l_run[i][1] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[i][n][0] = acc[i][n][1] = acc[i][n][2] = acc[i][n][3] = 0.f;
-  }
-  const uint32_t qs = smem_u32(qsm);
-  int done = 0;
-  for (; done < mine; ++done) {
-    if (!arrived(2 * done)) break;
-    const uint32_t Kt = smem_u32(wring + (2 * done) % SLOTS * TILE_BYTES);
-    const int nc = min(kPxTile, ncols - (tb + warp + done * kPxWarps) * kPxTile);   // columns of this tile in range
-    // ---- scores of the tile's 32 keys
-    float s[NM][4][4] = {};
-#pragma unroll
-    for (int k = 0; k < HD / 16; ++k) {
-      uint32_t kf[2][4];
-#pragma unroll
-      for (int n2 = 0; n2 < 2; ++n2)
-        ldsm_x4(Kt + sw_off(kPxTile, n2 * 16 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), kf[n2]);
-#pragma unroll
-      for (int i = 0; i < NM; ++i) {
-#pragma unroll
-        for (int part = 0; part < (HILO ? 2 : 1); ++part) {
-          uint32_t qf[4];
-          ldsm_x4(qs + part * QBYTES + sw_off(RB, i * 16 + (lane & 15), k * 2 + (lane >> 4)), qf);
-#pragma unroll
-          for (int n2 = 0; n2 < 2; ++n2) {
-            mma_bf16_16816(s[i][n2 * 2], qf, kf[n2][0], kf[n2][1]);
-            mma_bf16_16816(s[i][n2 * 2 + 1], qf, kf[n2][2], kf[n2][3]);
-          }
-        }
-      }
-    }
-    refill();
-    // ---- running softmax: thread holds rows lane/4 (+8), columns 8n + 2(lane%4) + {0, 1}
-    uint32_t pf[NM][2][4], pl[HILO ? NM : 1][2][4];
-#pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[i][n][e] * a.scale2;
-          if (nc < kPxTile && n * 8 + 2 * (lane & 3) + (e & 1) >= nc) x = -INFINITY;
-          s[i][n][e] = x;
-          mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
-      float al[2], ms[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
-        const float mn = fmaxf(m_run[i][e], mx[e]);
-        ms[e] = mn == -INFINITY ? 0.f : mn;   // nothing finite yet: weights of 0, not NaN
-        al[e] = exp2f(m_run[i][e] - ms[e]);
-        m_run[i][e] = mn;
-        l_run[i][e] *= al[e];
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = exp2f(s[i][n][e] - ms[e >> 1]);
-          s[i][n][e] = p;
-          l_run[i][e >> 1] += p;
-        }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        acc[i][n][0] *= al[0];
-        acc[i][n][1] *= al[0];
-        acc[i][n][2] *= al[1];
-        acc[i][n][3] *= al[1];
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x0 = s[i][2 * k + (j >> 1)][(j & 1) * 2], x1 = s[i][2 * k + (j >> 1)][(j & 1) * 2 + 1];
-          pf[i][k][j] = pack_bf16x2(x0, x1);
-          if (HILO)
-            pl[HILO ? i : 0][k][j] = pack_bf16x2(x0 - bf16_to_f(pf[i][k][j] & 0xFFFF), x1 - bf16_to_f(pf[i][k][j] >> 16));
-        }
-    }
-    // ---- output += P V
-    if (!arrived(2 * done + 1)) break;
-    uint8_t* vt = wring + (2 * done + 1) % SLOTS * TILE_BYTES;
-    const uint32_t Vt = smem_u32(vt);
-    if (nc < kPxTile) {
-      // rows past the range (another query's tokens, or never written): their
-      // probabilities are 0, and 0 times what they hold must stay 0
-      for (int e = lane; e < (kPxTile - nc) * (HD / 8); e += 32)
-        *reinterpret_cast<uint4*>(vt + sw_off(kPxTile, nc + e / (HD / 8), e % (HD / 8))) = make_uint4(0, 0, 0, 0);
-      __syncwarp();
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int n2 = 0; n2 < NT / 2; ++n2) {
-        uint32_t vf[4];
-        ldsm_x4_t(Vt + sw_off(kPxTile, k * 16 + (lane & 15), n2 * 2 + (lane >> 4)), vf);
-#pragma unroll
-        for (int i = 0; i < NM; ++i) {
-          mma_bf16_16816(acc[i][n2 * 2], pf[i][k], vf[0], vf[1]);
-          mma_bf16_16816(acc[i][n2 * 2 + 1], pf[i][k], vf[2], vf[3]);
-          if (HILO) {
-            mma_bf16_16816(acc[i][n2 * 2], pl[HILO ? i : 0][k], vf[0], vf[1]);
-            mma_bf16_16816(acc[i][n2 * 2 + 1], pl[HILO ? i : 0][k], vf[2], vf[3]);
-          }
-        }
-      }
-    }
-    refill();
-  }
+  const int done = warp_tiles<HD, NM, HILO>(
+      mine, smem_u32(qsm), a.scale2, [&](int n) { return wring + n % SLOTS * TILE_BYTES; },
+      [&](int i) { return ncols - (tb + warp + i * kPxWarps) * kPxTile; }, arrived, refill, m_run, l_run, acc);
   if (done < mine && lane == 0) {
     // a tile never arrived: let the copies in flight land (bounded); the result becomes NaN
     bad_sm = 1;
@@ -413,12 +436,9 @@ __global__ void __launch_bounds__(128, 2)
   for (int i = 0; i < NM; ++i)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float l = l_run[i][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
       if ((lane & 3) == 0) {
         sm_m[warp][i * 16 + e * 8 + (lane >> 2)] = m_run[i][e];
-        sm_l[warp][i * 16 + e * 8 + (lane >> 2)] = l;
+        sm_l[warp][i * 16 + e * 8 + (lane >> 2)] = l_run[i][e];
       }
     }
   __syncthreads();   // every warp is done with its ring
@@ -464,6 +484,124 @@ __global__ void __launch_bounds__(128, 2)
     }
     if (id >= 0) *reinterpret_cast<float4*>(a.part_o + (split * a.rows + id) * HD + d) = o;
   }
+  if (a.tc_ctas) pdl_wait();
+}
+
+// ============================================================================
+// The same for many rows and few columns: a row block per warp over all tiles of its
+// split, with rows, queries and results of its own and no step that the CTA takes together.  The
+// queries take the first slot of the warp's ring.  Bound by each warp's chain of latencies (lengths,
+// rows, queries, tile, products), which four row blocks per CTA share instead of one.
+// ============================================================================
+template <int HD, int NM>
+__global__ void __launch_bounds__(128, 2)
+    k_prefix_rows(const __grid_constant__ CUtensorMap kp, const __grid_constant__ CUtensorMap vp,
+                  const __grid_constant__ CUtensorMap ks, const __grid_constant__ CUtensorMap vs, const PrefixArgs a, int items) {
+  constexpr int RB = 16 * NM, TILE_BYTES = kPxTile * HD * 2, NT = HD / 8;
+  constexpr int SLOTS = kPxRing / kPxWarps / TILE_BYTES - 1;   // of tiles, behind the queries
+  static_assert(RB * HD * 2 <= TILE_BYTES && SLOTS >= 2 && SLOTS <= 12, "the warp's ring");
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t full[kPxWarps][12];
+  __shared__ int slot_sm[kPxWarps][RB + 1];
+  __shared__ long long row_id[kPxWarps][RB], q_at[kPxWarps][RB];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* wring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(sm_raw) + 1023) & ~uintptr_t(1023)) +
+                   warp * (kPxRing / kPxWarps);
+  if (!a.tc_ctas) pdl_wait();   // (else at the end, as in k_prefix_split)
+  int it = blockIdx.x * kPxWarps + warp;
+  if (it >= items) {
+    if (a.tc_ctas) pdl_wait();
+    return;
+  }
+  if (lane == 0) {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const bool pre = it < a.items_p;
+  if (!pre) it -= a.items_p;
+  const int rbs = pre ? a.rb_p : a.rb_s, nsp = pre ? a.n_p : a.n_s;
+  const int rb = it % rbs;
+  it /= rbs;
+  const int sp = it % nsp;
+  it /= nsp;
+  const int g = it % a.Hkv, b = it / a.Hkv, r0 = rb * RB;
+  int ncols = a.P, nrows = 0, ql = 0;
+  if (!pre) {
+    const int len = len_of(a, b);
+    ql = q_len_of(a, b);
+    nrows = ql * a.G;
+    ncols = min(max(len - ql + 1, 0), len);
+  } else if (lane < a.B) {
+    ql = q_len_of(a, lane);
+  }
+  const int ntiles = (ncols + kPxTile - 1) / kPxTile;
+  const int tb = static_cast<int>(quick_div(static_cast<long long>(sp) * ntiles, nsp));
+  const int mine = static_cast<int>(quick_div(static_cast<long long>(sp + 1) * ntiles, nsp)) - tb;
+  auto slot_at = [&](int n) { return wring + (1 + n % SLOTS) * TILE_BYTES; };
+  auto issue = [&](int n) {   // load n: K (even) or V (odd) of tile n / 2
+    const uint32_t fb = smem_u32(&full[warp][n % SLOTS]);
+    mbar_arrive_expect_tx(fb, TILE_BYTES);
+    tma_load_5d(smem_u32(slot_at(n)), pre ? ((n & 1) ? &vp : &kp) : ((n & 1) ? &vs : &ks), fb, 0, (tb + (n >> 1)) * kPxTile, 0, g,
+                pre ? 0 : b);
+  };
+  int issued = 0;             // (lane 0)
+  if (lane == 0 && (pre || r0 < nrows))
+    for (; issued < SLOTS && issued < 2 * mine; ++issued) issue(issued);
+  auto arrived = [&](int n) {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr)) != 0;
+  };
+  auto refill = [&]() {
+    __syncwarp();
+    if (lane == 0 && issued < 2 * mine) issue(issued++);
+  };
+  const int first = r0 / a.G;
+  if (pre) {
+    nrows = pack_queries(a, first, (r0 + RB - 1) / a.G - first + 1, ql, slot_sm[warp]) * a.G;
+    __syncwarp();
+  }
+  if (r0 >= nrows) {
+    if (lane == 0)            // (no rows after all: the copies land before the warp ends)
+      for (int n = 0; n < issued; ++n) mbar_wait(smem_u32(&full[warp][n]), 0, nullptr);
+    if (a.tc_ctas) pdl_wait();
+    return;
+  }
+  if (lane < RB) {
+    const int q = (r0 + lane) / a.G, h = g * a.G + r0 + lane - q * a.G;
+    const int slot = r0 + lane >= nrows ? -1 : pre ? slot_sm[warp][q - first] : b * a.Tq + q, sb = slot / a.Tq;
+    row_id[warp][lane] = slot < 0 ? -1 : static_cast<long long>(slot) * a.H + h;
+    q_at[warp][lane] = sb * a.q_sb + (slot - sb * a.Tq) * a.q_st + h * a.q_sh;
+  }
+  __syncwarp();
+#pragma unroll 8
+  for (int e = lane; e < RB * (HD / 8); e += 32) {   // (rows past the last: zero)
+    const int r = e / (HD / 8), c = e % (HD / 8);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (row_id[warp][r] >= 0) x = *reinterpret_cast<const uint4*>(a.q + q_at[warp][r] + c * 8);
+    *reinterpret_cast<uint4*>(wring + sw_off(RB, r, c)) = x;
+  }
+  __syncwarp();
+  float m_run[NM][2], l_run[NM][2], acc[NM][NT][4];
+  const int done = warp_tiles<HD, NM, false>(
+      mine, smem_u32(wring), a.scale2, slot_at, [&](int i) { return ncols - (tb + i) * kPxTile; }, arrived, refill, m_run, l_run,
+      acc);
+  if (done < mine && lane == 0)   // a tile never arrived: let the copies in flight land (bounded); the rows become NaN
+    for (int n = max(0, issued - SLOTS); n < issued; ++n) mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr);
+  const long long split = pre ? sp : a.n_p + sp;
+#pragma unroll
+  for (int i = 0; i < NM; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long id = row_id[warp][i * 16 + e * 8 + (lane >> 2)];
+      if (id < 0) continue;
+      const long long at = split * a.rows + id;
+      if ((lane & 3) == 0) a.part_ml[at] = done < mine ? make_float2(0.f, NAN) : make_float2(m_run[i][e], l_run[i][e]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(a.part_o + at * HD + n * 8 + 2 * (lane & 3)) =
+            make_float2(acc[i][n][2 * e], acc[i][n][2 * e + 1]);
+    }
   if (a.tc_ctas) pdl_wait();
 }
 
@@ -1595,6 +1733,18 @@ cudaError_t run_split_hd(int nm, bool hilo, const CUtensorMap* m, const PrefixAr
   return hilo ? run_split<HD, 2, true>(m, a, grid, pdl, s) : run_split<HD, 2, false>(m, a, grid, pdl, s);
 }
 
+// A row block per warp when the CTAs of a block each would take more than one wave and no split is long (a chain of up
+// to eight tiles per warp, half of that for half the blocks).  Whole calls, a block per warp against one per
+// CTA, us: 117 x 6 queries of 64/8 heads x 128, 2 + 8 columns 91 / 134; 128 x 1, 32/8 heads, 100 + 200 columns 30 / 43; 49 x 7,
+// 64/8 heads x 64, 103 + 20 columns 28 / 40; but 64 x 1, 32/8 heads, 8192 + 250 columns 45 / 44.
+constexpr int kRowsMaxCols = 256;
+template <int HD>
+cudaError_t run_rows(int nm, const CUtensorMap* m, const PrefixArgs& a, int items, bool pdl, cudaStream_t s) {
+  const dim3 grid((items + kPxWarps - 1) / kPxWarps);
+  return nm == 1 ? launch_k(pdl, k_prefix_rows<HD, 1>, grid, dim3(128), 1024 + kPxRing, s, m[0], m[1], m[2], m[3], a, items)
+                 : launch_k(pdl, k_prefix_rows<HD, 2>, grid, dim3(128), 1024 + kPxRing, s, m[0], m[1], m[2], m[3], a, items);
+}
+
 size_t stream_smem(int hd) { return 1024 + static_cast<size_t>(kWsWarps) * kWsStages * kPxTile * hd * 2; }
 
 // Column weights on tcgen05 when a (sequence, KV head) has more rows than two warp tiles hold (tensor cores
@@ -1640,6 +1790,10 @@ cudaError_t serving_init_attrs() {
   set(k_prefix_split<128, 1, true>, split_smem(128, 1, true));
   set(k_prefix_split<128, 2, false>, split_smem(128, 2, false));
   set(k_prefix_split<128, 2, true>, split_smem(128, 2, true));
+  set(k_prefix_rows<64, 1>, 1024 + kPxRing);
+  set(k_prefix_rows<64, 2>, 1024 + kPxRing);
+  set(k_prefix_rows<128, 1>, 1024 + kPxRing);
+  set(k_prefix_rows<128, 2>, 1024 + kPxRing);
   set(k_prefix_tc<64>, TcSmem<64>::kBytes);
   set(k_prefix_tc<128>, TcSmem<128>::kBytes);
   set(k_weights_stream<64, 1>, stream_smem(64));
@@ -1705,8 +1859,13 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
     pdl = true;
   }
   if (grid > 0) {
-    e = c.hd == 128 ? run_split_hd<128>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s)
-                    : run_split_hd<64>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s);
+    const int cols = std::max(p.n_p ? ceil_div_i(c.P, p.n_p) : 0, p.n_s ? ceil_div_i(c.S, p.n_s) : 0);   // of a split
+    if (!L.q32 && grid > 2 * kNumSM && cols <= std::min<long long>(kRowsMaxCols, grid / 4))
+      e = c.hd == 128 ? run_rows<128>(p.nm, m, a, static_cast<int>(grid), pdl, s)
+                      : run_rows<64>(p.nm, m, a, static_cast<int>(grid), pdl, s);
+    else
+      e = c.hd == 128 ? run_split_hd<128>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s)
+                      : run_split_hd<64>(p.nm, L.q32 != nullptr, m, a, static_cast<int>(grid), pdl, s);
     if (e != cudaSuccess) return e;
     pdl = true;
   }

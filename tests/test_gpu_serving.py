@@ -79,6 +79,12 @@ ATT = [
     (33, 4, 4, 2, 128, 5000, 6, [6, 5, 4] * 11, [4, 3, 2] * 11),
     (64, 8, 2, 1, 64, 3333, 9, [9] * 64, [i % 9 for i in range(64)]),
     (9, 4, 8, 2, 128, 300, 4, [4] * 9, [0] * 9),
+    # many rows, few columns: a row block per warp
+    (117, 6, 64, 8, 128, 2, 8, [i % 9 for i in range(117)], [i % 7 for i in range(117)]),
+    (128, 1, 12, 4, 128, 100, 200, [200 - i for i in range(128)], None),
+    (100, 7, 16, 4, 64, 103, 130, [130 - (7 * i) % 131 for i in range(100)], [i % 8 for i in range(100)]),
+    (80, 3, 30, 6, 64, 0, 33, [33, 1, 0, 32] * 20, [3, 1, 0, 2] * 20),
+    (128, 2, 8, 8, 64, 1500, 17, [17 - i % 18 for i in range(128)], [2, 1] * 64),
     # prefixes long enough for the tensor-core kernel: lengths off its 128-column tiles, one row tile and several blocks
     # of two, a last block with one, sequences without queries
     (40, 1, 4, 4, 128, 12007, 0, None, None),
