@@ -1064,13 +1064,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // n-th column of the causal tail, and their (max, sum, output) meet in shared
 // memory; for few rows, where latency counts.  Otherwise a row per group.  The
 // causal tail: columns this query sees and an earlier one of its sequence does
-// not, at most Tq - 1, as fp32 dot products.
+// not, at most Tq - 1, as fp32 dot products, while the launch in front still runs.
+//   A row per group: eight CTAs per SM and four splits requested together (117 x 6 queries of 64 heads, two splits:
+// the whole call 70 us; five CTAs and eight splits 83, six and eight 81, eight and six 73; 160 queries
+// over a long prefix 130 us against 132, 64 with 18 parts a row 70 against 69).
 // ============================================================================
 template <int HD, bool Q32, bool ALL>
-__global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
+__global__ void __launch_bounds__(128, ALL ? 4 : 8) k_prefix_merge(const PrefixArgs a) {
   constexpr int LPG = HD / 4;          // lanes of a group, 4 dims each
   constexpr int NG = 128 / LPG;        // groups
-  constexpr int MB = 8;                // splits requested together
+  constexpr int MB = ALL ? 8 : 4;      // splits requested together
   __shared__ float gm[NG], gl[NG];
   __shared__ float4 go[NG][LPG];
   __shared__ int cnt[2][4];
@@ -1083,8 +1086,6 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
   // (a decode step's fp32 queries and lengths come from kernels the wait covers; a caller's were there before the first launch)
   if (Q32) pdl_wait();
   const int ql = q_len_of(a, b), len = len_of(a, b);
-  if (!Q32) pdl_wait();
-  if (ALL && t >= ql) return;
   const bool valid = last && t < ql;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1119,6 +1120,46 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
         if (i0 + u * GS < n) add(ml[u].x, ml[u].y, x[u]);
     }
   };
+  // the causal tail (a caller's inputs: before the wait, four columns' loads together)
+  const int base = min(max(len - ql + 1, 0), len), lim = min(max(len - ql + t + 1, 0), len);
+  if (valid && lim > base) {
+    const int g = h / a.G;
+    float4 q4;
+    const long long qo = b * a.q_sb + t * a.q_st + h * a.q_sh + gl_lane * 4;
+    if (Q32) {
+      q4 = *reinterpret_cast<const float4*>(a.q32 + qo);
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(a.q + qo);
+      q4 = make_float4(bf16_to_f(u.x & 0xFFFF), bf16_to_f(u.x >> 16), bf16_to_f(u.y & 0xFFFF), bf16_to_f(u.y >> 16));
+    }
+    const unsigned mask = LPG == 32 ? 0xffffffffu : (0xffffu << (threadIdx.x & 16));
+    constexpr int TB = Q32 ? 1 : 4;   // (a decode step's tail is empty: one query)
+    for (int j0 = base + grp; j0 < lim; j0 += GS * TB) {
+      uint2 ku[TB], vu[TB];
+      float sc[TB];
+#pragma unroll
+      for (int u = 0; u < TB; ++u) {
+        const int j = min(j0 + u * GS, lim - 1);
+        ku[u] = *reinterpret_cast<const uint2*>(a.k + b * a.k_sb + g * a.k_sg + j * a.k_sr + gl_lane * 4);
+        vu[u] = *reinterpret_cast<const uint2*>(a.v + b * a.v_sb + g * a.v_sg + j * a.v_sr + gl_lane * 4);
+      }
+#pragma unroll
+      for (int u = 0; u < TB; ++u)
+        sc[u] = q4.x * bf16_to_f(ku[u].x & 0xFFFF) + q4.y * bf16_to_f(ku[u].x >> 16) + q4.z * bf16_to_f(ku[u].y & 0xFFFF) +
+                q4.w * bf16_to_f(ku[u].y >> 16);
+#pragma unroll
+      for (int d = LPG / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < TB; ++u) sc[u] += __shfl_xor_sync(mask, sc[u], d);
+#pragma unroll
+      for (int u = 0; u < TB; ++u)
+        if (j0 + u * GS < lim)
+          add(sc[u] * a.scale2, 1.f, make_float4(bf16_to_f(vu[u].x & 0xFFFF), bf16_to_f(vu[u].x >> 16),
+                                                 bf16_to_f(vu[u].y & 0xFFFF), bf16_to_f(vu[u].y >> 16)));
+    }
+  }
+  if (!Q32) pdl_wait();
+  if (ALL && t >= ql) return;
   add_parts(a.part_o, a.part_ml, row, a.rows, valid ? a.n_p + a.n_s : 0);
   if (a.tc_ctas > 0) {
     // this query's number among the valid ones, and all of them
@@ -1159,29 +1200,6 @@ __global__ void __launch_bounds__(128) k_prefix_merge(const PrefixArgs a) {
     const int c0 = plan.cta_of(static_cast<long long>(pair) * plan.ntiles);
     const int c1 = plan.cta_of(static_cast<long long>(pair + 1) * plan.ntiles - 1);
     add_parts(a.tc_o, a.tc_ml, static_cast<long long>(c0 + pair) * kTcRows + r % kTcRows, kTcRows, valid ? c1 - c0 + 1 : 0);
-  }
-  const int base = min(max(len - ql + 1, 0), len), lim = min(max(len - ql + t + 1, 0), len);
-  if (valid && lim > base) {
-    const int g = h / a.G;
-    float4 q4;
-    const long long qo = b * a.q_sb + t * a.q_st + h * a.q_sh + gl_lane * 4;
-    if (Q32) {
-      q4 = *reinterpret_cast<const float4*>(a.q32 + qo);
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(a.q + qo);
-      q4 = make_float4(bf16_to_f(u.x & 0xFFFF), bf16_to_f(u.x >> 16), bf16_to_f(u.y & 0xFFFF), bf16_to_f(u.y >> 16));
-    }
-    const unsigned mask = LPG == 32 ? 0xffffffffu : (0xffffu << (threadIdx.x & 16));
-    for (int j = base + grp; j < lim; j += GS) {
-      const uint2 ku = *reinterpret_cast<const uint2*>(a.k + b * a.k_sb + g * a.k_sg + j * a.k_sr + gl_lane * 4);
-      const uint2 vu = *reinterpret_cast<const uint2*>(a.v + b * a.v_sb + g * a.v_sg + j * a.v_sr + gl_lane * 4);
-      float s = q4.x * bf16_to_f(ku.x & 0xFFFF) + q4.y * bf16_to_f(ku.x >> 16) + q4.z * bf16_to_f(ku.y & 0xFFFF) +
-                q4.w * bf16_to_f(ku.y >> 16);
-#pragma unroll
-      for (int d = LPG / 2; d > 0; d >>= 1) s += __shfl_xor_sync(mask, s, d);
-      add(s * a.scale2, 1.f, make_float4(bf16_to_f(vu.x & 0xFFFF), bf16_to_f(vu.x >> 16), bf16_to_f(vu.y & 0xFFFF),
-                                         bf16_to_f(vu.y >> 16)));
-    }
   }
   float M = m, L = l;
   float4 r = o;
@@ -1735,8 +1753,8 @@ cudaError_t run_split_hd(int nm, bool hilo, const CUtensorMap* m, const PrefixAr
 
 // A row block per warp when the CTAs of a block each would take more than one wave and no split is long (a chain of up
 // to eight tiles per warp, half of that for half the blocks).  Whole calls, a block per warp against one per
-// CTA, us: 117 x 6 queries of 64/8 heads x 128, 2 + 8 columns 91 / 134; 128 x 1, 32/8 heads, 100 + 200 columns 30 / 43; 49 x 7,
-// 64/8 heads x 64, 103 + 20 columns 28 / 40; but 64 x 1, 32/8 heads, 8192 + 250 columns 45 / 44.
+// CTA, us: 117 x 6 queries of 64/8 heads x 128, 2 + 8 columns 70 / 114; 128 x 1, 32/8 heads, 100 + 200 columns 28 / 41; 49 x 7,
+// 64/8 heads x 64, 103 + 20 columns 22 / 35; but 64 x 1, 32/8 heads, 8192 + 250 columns 47 / 45, and 32 x 3, 320 + 43 25 / 16.
 constexpr int kRowsMaxCols = 256;
 template <int HD>
 cudaError_t run_rows(int nm, const CUtensorMap* m, const PrefixArgs& a, int items, bool pdl, cudaStream_t s) {
