@@ -279,8 +279,8 @@ __device__ __forceinline__ int warp_tiles(int mine, uint32_t qs, float scale2, T
 // HBM-bound: a tile's 16 KB feed 16 NM rows.  mma.sync, because a query row block of a decode
 // step has 1 to 32 rows: a 128-row tcgen05 tile would be mostly padding (k_prefix_tc takes over from 33 rows).
 // Two CTAs per SM, 24 KB of ring per warp, reused by halves (K, then V): with 64 samples' own 500 to 1000
-// columns of 8 heads x 128 behind an 8192-column prefix the whole call takes 68 us, 74 with one CTA
-// per SM and twice the ring.  A row sees every column of
+// columns of 8 heads x 128 behind an 8192-column prefix the whole call took 68 us then, 74 with one
+// CTA per SM and twice the ring (70 now, with the merge's later form).  A row sees every column of
 // the range -- a sequence's columns stop at the last one all its queries see;
 // the few that only later queries see are added by the merge -- so what a masked
 // row of V holds never meets a product.  HILO: fp32 queries and probabilities as
