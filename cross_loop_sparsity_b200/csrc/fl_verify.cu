@@ -573,11 +573,11 @@ __global__ void __launch_bounds__(256) k_verify_greedy(const VerifyArgs a) {
     }
     const float mm = warp_max(m);
     at = __reduce_min_sync(0xffffffffu, m == mm ? at : INT_MAX);
-    if (lane == 0) best[i] = at;
+    if (lane == 0) best[i] = mm > -INFINITY ? at : -1;   // (only NaN, or nothing above -inf: no candidate)
   }
   __syncthreads();
   int acc = 0;
-  while (acc < n && draft[acc] == best[acc]) ++acc;
+  while (acc < n && best[acc] >= 0 && draft[acc] == best[acc]) ++acc;
   for (int i = tid; i <= D; i += 256) tokens[i] = i < acc ? draft[i] : i == acc ? best[acc] : -1;
   if (tid == 0) c.n_accepted[b] = acc;
 }

@@ -487,7 +487,8 @@ fl_status flashloop_evict(const flashloop_evict_args* a, void* scratch, size_t s
  * probabilities (q_i one at x_i).  temperature 0: draft i is accepted while it is
  * the argmax of logits[b][i] (ties to the lowest index; NaN ignored), y the argmax
  * of row m; u and draft_logits are not read.  A draft token outside [0, V) is rejected.  y = -1 when the
- * row's distribution is not finite or empty (NaN, +inf, or no finite logit).
+ * row's distribution is not finite or empty (NaN, +inf, or no finite logit); at temperature 0, when no logit of
+ * the row is above -inf (and no draft is accepted there).
  *   logits fp32 [B][D+1][V], draft_logits fp32 [B][D][V]: rows contiguous, 4-byte aligned, strides of b and i;
  *   draft int32 [B][D]; u fp32 [B][D+1] in [0, 1); n_draft int32 [B] or NULL for D;
  *   tokens int32 [B][D+1]; n_accepted int32 [B], all contiguous.
