@@ -51,11 +51,12 @@ __device__ __forceinline__ const float* row_of(const VerifyArgs& a, int b, int r
 
 // exp((x - m) / temperature) in 64 bits, to 4e-14: with z = 64 log2(e) (x - m) / temperature = k + r, k = rint(z),
 // it is 2^(k / 64) e^(r ln 2 / 64); table[i] = 2^(i / 64), and the second factor's series to
-// its fourth power, |r ln 2 / 64| <= 0.0055 (the next term is below 4e-14).  scale64 and
-// offset give z = scale64 x + offset, x a 32-bit value with z in [-65000, 0.5].
+// its fourth power, |r ln 2 / 64| <= 0.0055 (the next term is below 4e-14).  z = scale64 (x - m), x and m 32-bit
+// values, z in [-65000, 0].  The difference comes first: as scale64 x + (-scale64 m), one operation less, z would be off by
+// the rounding of scale64 m, which is beyond any exponent at low temperatures or with large logits.
 constexpr int kExpTable = 64;
-__device__ __forceinline__ double exp64(float x, double scale64, double offset, const double* table) {
-  const double z = fma(static_cast<double>(x), scale64, offset);
+__device__ __forceinline__ double exp64(float x, double scale64, double m, const double* table) {
+  const double z = (static_cast<double>(x) - m) * scale64;
   const double t = z + 6755399441055744.0;                  // + 1.5 * 2^52: k in the low word
   const int k = __double2loint(t);
   const double r = z - (t - 6755399441055744.0);
@@ -67,8 +68,8 @@ __device__ __forceinline__ double exp64(float x, double scale64, double offset, 
 }
 
 // The same, 0 for x below lo.
-__device__ __forceinline__ double exp64_from(float x, float lo, double scale64, double offset, const double* table) {
-  const double e = exp64(fmaxf(x, lo), scale64, offset, table);
+__device__ __forceinline__ double exp64_from(float x, float lo, double scale64, double m, const double* table) {
+  const double e = exp64(fmaxf(x, lo), scale64, m, table);
   return x >= lo ? e : 0.0;
 }
 
@@ -81,7 +82,7 @@ struct Deciding {
   int x_out;        // a token left out (the rejected one of a draft without probabilities), or -1
   int fine;         // both rows have finite, positive totals
   float lo_p, lo_q; // logits below these (2^-1000 of the maximum, -inf among them) count as nothing
-  double op, oq;    // exp64's offsets: -64 log2(e) m / temperature
+  double mp, mq;    // the rows' maxima
   double ratio;
 };
 
@@ -297,7 +298,7 @@ __device__ void describe(const VerifyArgs& a, int row, int n, const Ahead& h, co
     const bool fine = isfinite(zp) && zp > 0.0 && (!with_draft || (isfinite(zq) && zq > 0.0));
     *d = Deciding{row, residual && verdict[row] == 2, with_draft,
                   residual && !with_draft ? h.x[row] : -1, fine, mp - reach, mq - reach,
-                  -64.0 * a.scale2 * mp, -64.0 * a.scale2 * mq, zq / zp};
+                  mp, mq, zq / zp};
   }
   __syncthreads();
 }
@@ -317,14 +318,14 @@ __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int
   const int lane = threadIdx.x & 31;
   const float* xp = row_of(a, b, d.row);
   const float* xq = DRAFT ? row_of(a, b, a.c.D + 1 + d.row) : nullptr;
-  const double s64 = 64.0 * a.scale2, op = d.op, oq = d.oq, ratio = d.ratio;
+  const double s64 = 64.0 * a.scale2, mp = d.mp, mq = d.mq, ratio = d.ratio;
   const float lo_p = d.lo_p, lo_q = d.lo_q;
   const int x_out = d.x_out;
   double ap = 0.0, aq = 0.0, np = 0.0, nq = 0.0;   // tokens of positive weight, and the others
   auto add = [&](float fp, float fq, int j) {
-    const double ep = exp64_from(fp, lo_p, s64, op, table);
+    const double ep = exp64_from(fp, lo_p, s64, mp, table);
     if (DRAFT) {
-      const double eq = exp64_from(fq, lo_q, s64, oq, table);
+      const double eq = exp64_from(fq, lo_q, s64, mq, table);
       if (ratio * ep > eq) {
         ap += ep;
         aq += eq;
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
   __syncthreads();
   if (!last) return;
   const double s64 = 64.0 * a.scale2;
-  auto prob = [&](float x, float lo, double offset) { return exp64_from(x, lo, s64, offset, table); };
+  auto prob = [&](float x, float lo, double m) { return exp64_from(x, lo, s64, m, table); };
   Sums s{0.0, 0.0, 0.0, 0.0};   // n_sub <= threads: one range each
   double zp, zq;
   auto totals = [&]() {
@@ -479,8 +480,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
   };
   totals();
   while (d.near && d.fine) {
-    const double p = prob(ahead.xp[d.row], d.lo_p, d.op) / zp;   // (a token outside the vocabulary is never near)
-    const double q = c.draft_logits ? prob(ahead.xq[d.row], d.lo_q, d.oq) / zq : 1.0;
+    const double p = prob(ahead.xp[d.row], d.lo_p, d.mp) / zp;   // (a token outside the vocabulary is never near)
+    const double q = c.draft_logits ? prob(ahead.xq[d.row], d.lo_q, d.mq) / zq : 1.0;
     if (!(static_cast<double>(ahead.u[d.row]) * q < p)) break;   // rejected after all
     int row = d.row + 1;
     judge(a, b, row, n, ahead, verdict, &norms);
@@ -521,8 +522,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
   const float* xp = row_of(a, b, acc);
   const float* xq = with_draft ? row_of(a, b, D + 1 + acc) : nullptr;
   auto weight = [&](int j) {
-    const double ep = prob(xp[j], d.lo_p, d.op);
-    if (with_draft) return fmax(ratio * ep - prob(xq[j], d.lo_q, d.oq), 0.0);
+    const double ep = prob(xp[j], d.lo_p, d.mp);
+    if (with_draft) return fmax(ratio * ep - prob(xq[j], d.lo_q, d.mq), 0.0);
     return j == d.x_out ? 0.0 : ep;
   };
   double mass = 0.0;

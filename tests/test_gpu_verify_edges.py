@@ -1,9 +1,10 @@
 """Draft verification at the ends of what it accepts."""
+import numpy as np
 import pytest
 import torch
 
 from cross_loop_sparsity_b200 import flashloop as fl
-from test_gpu_serving import ints
+from test_gpu_serving import check_verify, ints, verify_inputs
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -35,3 +36,34 @@ def test_greedy_candidates_beside_nan_and_infinities():
     logits[3, 0, 3] = -INF
     tok, _ = fl.verify_draft(logits, None, None, None, temperature=0.0)
     assert tok[:, 0].tolist() == [19999, 9001, 12000, -1]
+
+
+# ---------------------------------------------------------------------------- temperatures
+@pytest.mark.parametrize("T", [1e-20, 1e-19, 1e-18, 1e-17, 1e-16, 1e-14, 1e-10])
+@pytest.mark.parametrize("B,D,V", [(64, 0, 300), (16, 3, 900), (4, 2, 40000)])
+def test_smallest_temperatures(B, D, V, T):
+    """Everything at the maximum, as (x - max) / T says, and never a row given up for its scale."""
+    logits, dl, draft, u = verify_inputs(int(-np.log10(T)) + V, B, D, V, 1.0)
+    logits += 12.0
+    if D:
+        draft[::2] = logits[::2, :D].argmax(-1).to(torch.int32)
+    wt, wa = check_verify(logits, dl, draft, u, None, T)
+    assert all(wt[b, wa[b]] >= 0 for b in range(B) if wa[b] == D)
+    check_verify(logits, None, draft, u, None, T)
+
+
+def test_logits_near_the_ends_of_fp32():
+    """A forced token, rows masked with the type's lowest value, all of one value, and both ends in one row."""
+    B, V = 8, 5003
+    logits, _, _, u = verify_inputs(3, B, 0, V, 1.0)
+    logits[0, 0, 4321] = 1e30
+    logits[1, 0] = -MAX
+    logits[2, 0] = MAX
+    logits[3, 0, 100:] = -MAX
+    logits[4, 0, 7], logits[4, 0, 8] = MAX, -MAX
+    logits[5, 0] += 1e20
+    logits[6, 0] = -1e30
+    logits[6, 0, 5000:] = -1e30 * (1 + 2.0 ** -20)
+    logits[7, 0] += 1e9
+    for T in (1.0, 0.3, 1e-6):
+        check_verify(logits, None, torch.empty((B, 0), dtype=torch.int32, device="cuda"), u, None, T)
