@@ -29,7 +29,7 @@ struct VerifyArgs {
   flashloop_verify_args c;
   int n_chunks;
   double scale2;   // log2(e) / temperature
-  float reach;     // logits further than this below the maximum, 2^-1000 of it, count as nothing
+  double reach;    // logits further than this below the maximum, 2^-1000 of it, count as nothing
   RowPart* part;   // [B][2D + 1][n_chunks]: target rows, then draft rows
   unsigned* done;              // [B] finished CTAs of the second launch
   struct Sums* sums;           // [B][n_sub] of the deciding row's token ranges
@@ -81,7 +81,9 @@ struct Deciding {
   int with_draft;   // the weights are max(p - q, 0)
   int x_out;        // a token left out (the rejected one of a draft without probabilities), or -1
   int fine;         // both rows have finite, positive totals
-  float lo_p, lo_q; // logits below these (2^-1000 of the maximum, -inf among them) count as nothing
+  // Logits below these (2^-1000 of the maximum, -inf among them) count as nothing.  Rounded up, so that no logit counts
+  // whose exponent would not fit, and finite however far they reach.
+  float lo_p, lo_q;
   double mp, mq;    // the rows' maxima
   double ratio;
 };
@@ -293,11 +295,11 @@ __device__ void judge(const VerifyArgs& a, int b, int first, int n, const Ahead&
 __device__ void describe(const VerifyArgs& a, int row, int n, const Ahead& h, const Norms& norms, const int* verdict, Deciding* d) {
   if (threadIdx.x == 0) {
     const bool residual = row < n, with_draft = residual && a.c.draft_logits;
-    const float mp = norms.mp[row], mq = with_draft ? norms.mq[row] : 0.f, reach = a.reach;
+    const float mp = norms.mp[row], mq = with_draft ? norms.mq[row] : 0.f;
     const double zp = norms.zp[row], zq = with_draft ? norms.zq[row] : 1.0;
     const bool fine = isfinite(zp) && zp > 0.0 && (!with_draft || (isfinite(zq) && zq > 0.0));
     *d = Deciding{row, residual && verdict[row] == 2, with_draft,
-                  residual && !with_draft ? h.x[row] : -1, fine, mp - reach, mq - reach,
+                  residual && !with_draft ? h.x[row] : -1, fine, __double2float_ru(mp - a.reach), __double2float_ru(mq - a.reach),
                   mp, mq, zq / zp};
   }
   __syncthreads();
@@ -630,7 +632,7 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   if (c->temperature == 0.f) a.c.draft_logits = nullptr;   // greedy: the target's rows alone
   a.n_chunks = verify_chunks(c->V);
   a.scale2 = c->temperature > 0.f ? 1.4426950408889634 / static_cast<double>(c->temperature) : 0.0;
-  a.reach = c->temperature > 0.f ? static_cast<float>(1000.0 / a.scale2) : 0.f;
+  a.reach = c->temperature > 0.f ? 1000.0 / a.scale2 : 0.0;
   a.part = static_cast<RowPart*>(scratch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rows = c->D + 1 + (a.c.draft_logits ? c->D : 0);

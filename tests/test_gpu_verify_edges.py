@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from cross_loop_sparsity_b200 import flashloop as fl
-from test_gpu_serving import check_verify, ints, verify_inputs
+from test_gpu_serving import check_verify, gen, ints, verify_inputs
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -67,3 +67,27 @@ def test_logits_near_the_ends_of_fp32():
     logits[7, 0] += 1e9
     for T in (1.0, 0.3, 1e-6):
         check_verify(logits, None, torch.empty((B, 0), dtype=torch.int32, device="cuda"), u, None, T)
+
+
+@pytest.mark.parametrize("T", [1e30, 1e35, 1e36, 1e38, 3e38])
+def test_largest_temperatures(T):
+    """Every token that is not masked alike; the masked ones (-inf) never."""
+    logits, dl, draft, u = verify_inputs(8, 16, 2, 4001, 1.0)
+    logits[:, :, ::3] = -INF
+    dl[:, :, ::5] = -INF
+    wt, wa = check_verify(logits, None, draft, u, None, T)
+    assert all(wt[b, wa[b]] % 3 for b in range(16))
+    check_verify(logits[:, :1].contiguous(), None, torch.empty((16, 0), dtype=torch.int32, device="cuda"), u[:, :1].contiguous(), None, T)
+
+
+@pytest.mark.parametrize("top", [3.0, 20.0, -50.0, 1e20])
+@pytest.mark.parametrize("part", [0.3, 0.55, 0.75, 0.97, 1.2])
+def test_temperatures_at_the_spacing_of_the_logits(top, part):
+    """The logit next to the maximum lies between 2^-800 and 2^-4000 of it: it counts as nothing, or as that little."""
+    x = np.float32(top)
+    below = np.nextafter(x, np.float32(-INF))
+    T = part * float(x - below) / (1000 * np.log(2.0))
+    logits = torch.full((4, 1, 900), float(below), device="cuda")
+    logits[:, 0, 555] = float(x)
+    tok, _ = fl.verify_draft(logits, None, None, torch.rand((4, 1), generator=gen(1), device="cuda"), temperature=T)
+    assert tok[:, 0].tolist() == [555] * 4
