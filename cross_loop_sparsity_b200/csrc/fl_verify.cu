@@ -102,8 +102,8 @@ __device__ __forceinline__ void row_norm(const VerifyArgs& a, int b, int r, floa
       p.s = f.y;
     }
     const float mn = fmaxf(m, warp_max(p.m));
-    if (mn > m) z *= static_cast<double>(exp2f(static_cast<float>((m - mn) * a.scale2)));
-    z += p.m == -INFINITY ? p.s : p.s * exp2f(static_cast<float>((p.m - mn) * a.scale2));   // (no finite logit: 0, or NaN)
+    if (mn > m) z *= static_cast<double>(exp2f(static_cast<float>((static_cast<double>(m) - mn) * a.scale2)));
+    z += p.m == -INFINITY ? p.s : p.s * exp2f(static_cast<float>((static_cast<double>(p.m) - mn) * a.scale2));   // (no finite logit: 0, or NaN)
     m = mn;
   }
 #pragma unroll
@@ -220,12 +220,13 @@ __global__ void __launch_bounds__(kVfThreads, 5) k_verify_rows(const VerifyArgs 
       }
       return;
     }
-    const float c2 = static_cast<float>(a.scale2), ms = m == -INFINITY ? 0.f : m;
+    // (halves, exact but for denormals: the difference of two logits may be beyond fp32)
+    const float c2 = static_cast<float>(2.0 * a.scale2), ms = m == -INFINITY ? 0.f : 0.5f * m;
     float s = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s += exp2f((v[u][e] - ms) * c2);
+      for (int e = 0; e < 4; ++e) s += exp2f(fmaf(v[u][e], 0.5f, -ms) * c2);
     s = warp_sum(s);
     if (lane == 0) red[warp] = s;
     __syncthreads();

@@ -91,3 +91,17 @@ def test_temperatures_at_the_spacing_of_the_logits(top, part):
     logits[:, 0, 555] = float(x)
     tok, _ = fl.verify_draft(logits, None, None, torch.rand((4, 1), generator=gen(1), device="cuda"), temperature=T)
     assert tok[:, 0].tolist() == [555] * 4
+
+
+@pytest.mark.parametrize("T", [5e37, 3e38])
+def test_logits_further_apart_than_fp32_reaches(T):
+    """The lowest and the largest value in one row, at a temperature where both have weight."""
+    B, D, V = 64, 3, 900
+    g = gen(2)
+    kind = torch.randint(0, 3, (B, D + 1, V), generator=g, device="cuda")
+    logits = torch.where(kind == 0, -MAX, torch.where(kind == 1, 0.0, MAX))
+    dl = torch.where(torch.randint(0, 3, (B, D, V), generator=g, device="cuda") == 0, -MAX, 0.5 * MAX)
+    draft = torch.randint(0, V, (B, D), generator=g, device="cuda", dtype=torch.int32)
+    u = torch.rand((B, D + 1), generator=g, device="cuda")
+    check_verify(logits, dl, draft, u, None, T)
+    check_verify(logits, None, draft, (u / V).contiguous(), None, T)
