@@ -310,11 +310,15 @@ __device__ void describe(const VerifyArgs& a, int row, int n, const Ahead& h, co
 // all exponentials; ap and aq, those of tokens whose weight is positive.  The weight of token j is
 //   max(e_p / Z_p - e_q / Z_q, 0) = max(ratio e_p - e_q, 0) / Z_q,  ratio = Z_q / Z_p,
 // so a range's weight is ratio * ap - aq, and the exact ratio need not be known
-// before the pass: which tokens are positive is decided with the 32-bit one, and a
-// token it gets wrong weighs less than 1e-6 of its probability.
+// before the pass: which tokens are positive is decided with the 32-bit one (good to 4e-6: its sums' roundings), and
+// a token it gets wrong weighs less than that much of its e_q.  `near` is the e_q of all tokens that it could get wrong,
+// those whose two terms are within kNearWords of each other in the high words (1e-5 of either at the least):
+// what the pick allows for.
 struct Sums {
-  double p, q, ap, aq;
+  double p, q, ap, aq, near, pad;
 };
+constexpr int kNearWords = 22;
+constexpr double kNearError = 1e-5;
 template <bool DRAFT>
 __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
   constexpr int U = DRAFT ? 4 : 8;   // tokens of a lane in flight
@@ -324,12 +328,14 @@ __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int
   const double s64 = 64.0 * a.scale2, mp = d.mp, mq = d.mq, ratio = d.ratio;
   const float lo_p = d.lo_p, lo_q = d.lo_q;
   const int x_out = d.x_out;
-  double ap = 0.0, aq = 0.0, np = 0.0, nq = 0.0;   // tokens of positive weight, and the others
+  double ap = 0.0, aq = 0.0, np = 0.0, nq = 0.0, near = 0.0;   // tokens of positive weight, the others, those near 0
   auto add = [&](float fp, float fq, int j) {
     const double ep = exp64_from(fp, lo_p, s64, mp, table);
     if (DRAFT) {
       const double eq = exp64_from(fq, lo_q, s64, mq, table);
-      if (ratio * ep > eq) {
+      const double rp = ratio * ep;
+      if (abs(__double2hiint(rp) - __double2hiint(eq)) <= kNearWords) near += eq;
+      if (rp > eq) {
         ap += ep;
         aq += eq;
       } else {
@@ -367,7 +373,7 @@ __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int
   }
   int j = j0 + rounds * 32 * U + lane;
   for (; j < j1; j += 32) add(xp[j], DRAFT ? xq[j] : 0.f, j);
-  Sums s{ap + np, aq + nq, ap, aq};
+  Sums s{ap + np, aq + nq, ap, aq, near, 0.0};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s.p += __shfl_xor_sync(0xffffffffu, s.p, o);
@@ -375,30 +381,38 @@ __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int
     s.ap += __shfl_xor_sync(0xffffffffu, s.ap, o);
     s.aq += __shfl_xor_sync(0xffffffffu, s.aq, o);
   }
+  if (DRAFT && __any_sync(0xffffffffu, near > 0.0)) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.near += __shfl_xor_sync(0xffffffffu, s.near, o);
+  }
   return s;
 }
 __device__ __forceinline__ Sums range_sums(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
-  if (!d.fine) return Sums{0.0, 0.0, 0.0, 0.0};   // (the token will be -1)
+  if (!d.fine) return Sums{};   // (the token will be -1)
   return d.with_draft ? range_sums_of<true>(a, b, d, j0, j1, table) : range_sums_of<false>(a, b, d, j0, j1, table);
 }
 
-// both sums over the block
-__device__ double2 block_sums_f64(double x, double y, double2* buf /*[kSumWarps]*/) {
+// the sums of x, y and z over the block
+struct Three {
+  double x, y, z;
+};
+__device__ Three block_sums_f64(Three v, Three* buf /*[kSumWarps]*/) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
   }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_double2(x, y);
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
-  double2 t = make_double2(0.0, 0.0);
+  Three t{0.0, 0.0, 0.0};
 #pragma unroll
-  for (int w = 0; w < kSumWarps; ++w) t = make_double2(t.x + buf[w].x, t.y + buf[w].y);
+  for (int w = 0; w < kSumWarps; ++w) t = Three{t.x + buf[w].x, t.y + buf[w].y, t.z + buf[w].z};
   return t;
 }
 // exclusive prefix sum over the block's threads, in thread order, and the sum of all
-__device__ double block_scan_f64(double v, double2* buf, double& total) {
+__device__ double block_scan_f64(double v, Three* buf, double& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double incl = v;
 #pragma unroll
@@ -434,12 +448,13 @@ __device__ double block_scan_f64(double v, double2* buf, double& total) {
 // ============================================================================
 __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs a) {
   __shared__ double table[kExpTable], start_of[kSumThreads];
-  __shared__ double2 buf[kSumWarps];
+  __shared__ Three buf[kSumWarps];
   __shared__ Ahead ahead;
   __shared__ int verdict[kMaxDraft];
   __shared__ Norms norms;
   __shared__ Deciding d;
   __shared__ int last, cross[2], top[2];
+  __shared__ bool sure;
   const flashloop_verify_args& c = a.c;
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < kExpTable) table[tid] = exp2(tid * (1.0 / kExpTable));
@@ -469,17 +484,19 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
   if (!last) return;
   const double s64 = 64.0 * a.scale2;
   auto prob = [&](float x, float lo, double m) { return exp64_from(x, lo, s64, m, table); };
-  Sums s{0.0, 0.0, 0.0, 0.0};   // n_sub <= threads: one range each
-  double zp, zq;
+  Sums s{};                     // n_sub <= threads: one range each
+  double zp, zq, unsure;
   auto totals = [&]() {
     if (tid < a.n_sub) {   // (from L2: other CTAs wrote most of them)
       const double2* from = reinterpret_cast<const double2*>(&sums[tid]);
-      const double2 x = __ldcg(from), y = __ldcg(from + 1);
-      s = Sums{x.x, x.y, y.x, y.y};
+      const double2 x = __ldcg(from), y = __ldcg(from + 1), z = __ldcg(from + 2);
+      s = Sums{x.x, x.y, y.x, y.y, z.x, 0.0};
     }
-    const double2 z = block_sums_f64(s.p, s.q, buf);
-    zp = z.x;
-    zq = z.y;
+    const Three t = block_sums_f64(Three{s.p, s.q, s.near}, buf);
+    zp = t.x;
+    zq = t.y;
+    // The ranges' weights may be off, together, by what the 32-bit ratio got wrong; so may the target.
+    unsure = 2.0 * kNearError * t.z;
   };
   totals();
   while (d.near && d.fine) {
@@ -501,27 +518,6 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
   const int acc = d.row;
   const bool with_draft = d.with_draft;
   const double ratio = with_draft ? zq / zp : 1.0;
-  const double w = ratio * s.ap - s.aq, mine = w > 0.0 ? w : 0.0;
-  double total;
-  const double before = block_scan_f64(mine, buf, total);
-  const bool fine = d.fine && isfinite(total) && total > 0.0;
-  for (int i = tid; i <= D; i += kSumThreads)
-    if (i != acc || !fine) tokens[i] = i < acc ? ahead.x[i] : -1;
-  if (tid == 0) c.n_accepted[b] = acc;
-  if (!fine) return;
-  const double target = static_cast<double>(ahead.u[D]) * total;
-  // the first range whose end is past the target (the last with any weight, should rounding leave none)
-  start_of[tid] = before;
-  if (mine > 0.0) {
-    atomicMax(&top[0], tid);
-    if (target < before + mine) atomicMin(&cross[0], tid);
-  }
-  __syncthreads();
-  const int sub = cross[0] != INT_MAX ? cross[0] : top[0];
-  const double start = start_of[sub];
-  const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
-  const int per = (j1 - j0 + kSumThreads - 1) / kSumThreads;
-  const int t0 = min(j1, j0 + tid * per), t1 = min(j1, t0 + per);
   const float* xp = row_of(a, b, acc);
   const float* xq = with_draft ? row_of(a, b, D + 1 + acc) : nullptr;
   auto weight = [&](int j) {
@@ -529,27 +525,73 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
     if (with_draft) return fmax(ratio * ep - prob(xq[j], d.lo_q, d.mq), 0.0);
     return j == d.x_out ? 0.0 : ep;
   };
-  double mass = 0.0;
-  for (int j = t0; j < t1; ++j) mass += weight(j);
-  double all;
-  const double at = start + block_scan_f64(mass, buf, all);
-  if (mass > 0.0) {
-    atomicMax(&top[1], tid);
-    if (target < at + mass) atomicMin(&cross[1], tid);
-  }
-  __syncthreads();
-  if (tid != (cross[1] != INT_MAX ? cross[1] : max(top[1], 0))) return;
-  double run = at;
-  int y = -1;   // (no weight at all where p and q differ by roundings alone: empty)
-  for (int j = t0; j < t1; ++j) {
-    const double x = weight(j);
-    run += x;
-    if (x > 0.0) {
-      y = j;
-      if (run > target) break;
+  for (int i = tid; i <= D; i += kSumThreads)
+    if (i != acc) tokens[i] = i < acc ? ahead.x[i] : -1;
+  if (tid == 0) c.n_accepted[b] = acc;
+  double mine = fmax(ratio * s.ap - s.aq, 0.0);   // (0 for NaN)
+  for (;;) {
+    double total;
+    const double before = block_scan_f64(mine, buf, total);
+    const bool fine = d.fine && isfinite(total) && total > 0.0;
+    if (fine) {
+      const double target = static_cast<double>(ahead.u[D]) * total;
+      // the first range whose end is past the target (the last with any weight, should rounding leave none)
+      start_of[tid] = before;
+      if (mine > 0.0) {
+        atomicMax(&top[0], tid);
+        if (target < before + mine) atomicMin(&cross[0], tid);
+      }
+      __syncthreads();
+      const int sub = cross[0] != INT_MAX ? cross[0] : top[0];
+      const double start = start_of[sub];
+      const int j0 = min(c.V, sub * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
+      const int per = (j1 - j0 + kSumThreads - 1) / kSumThreads;
+      const int t0 = min(j1, j0 + tid * per), t1 = min(j1, t0 + per);
+      double mass = 0.0;
+      for (int j = t0; j < t1; ++j) mass += weight(j);
+      double all;
+      const double at = start + block_scan_f64(mass, buf, all);
+      if (mass > 0.0) {
+        atomicMax(&top[1], tid);
+        if (target < at + mass) atomicMin(&cross[1], tid);
+      }
+      __syncthreads();
+      if (tid == (cross[1] != INT_MAX ? cross[1] : max(top[1], 0))) {
+        double run = at, x = 0.0;
+        int y = -1;   // (no weight at all where p and q differ by roundings alone: empty)
+        for (int j = t0; j < t1; ++j) {
+          x = weight(j);
+          run += x;
+          if (x > 0.0) {
+            y = j;
+            if (run > target) break;
+          }
+        }
+        sure = run - target > unsure && target - (run - x) >= unsure;
+        if (unsure == 0.0 || sure) tokens[acc] = y;
+      }
+      if (unsure == 0.0) return;
+      __syncthreads();
+      if (sure) return;
+    } else if (unsure == 0.0) {
+      if (tid == 0) tokens[acc] = -1;
+      return;
     }
+    // Too near to say: the ranges' weights again, token by token from the exact ratio (where target and draft
+    // nearly agree: a call on 64 equal rows of 131071 tokens, the slowest, takes 275 us, on unlike ones 50).
+    unsure = 0.0;
+    for (int r = warp; r < a.n_sub; r += kSumWarps) {
+      const int j0 = min(c.V, r * a.sub_len), j1 = min(c.V, j0 + a.sub_len);
+      double x = 0.0;
+      for (int j = j0 + lane; j < j1; j += 32) x += weight(j);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if (lane == 0) start_of[r] = x;
+    }
+    if (tid < 2) cross[tid] = INT_MAX, top[tid] = -1;
+    __syncthreads();
+    mine = tid < a.n_sub ? start_of[tid] : 0.0;
   }
-  tokens[acc] = y;
 }
 
 // ============================================================================

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import serving_ref as ref
 from cross_loop_sparsity_b200 import flashloop as fl
 from test_gpu_serving import check_verify, gen, ints, verify_inputs
 
@@ -105,3 +106,44 @@ def test_logits_further_apart_than_fp32_reaches(T):
     u = torch.rand((B, D + 1), generator=g, device="cuda")
     check_verify(logits, dl, draft, u, None, T)
     check_verify(logits, None, draft, (u / V).contiguous(), None, T)
+
+
+# ---------------------------------------------------------------------------- targets next to the draft
+def tokens_of_the_residual(logits, dl, u):
+    """Token of max(p_0 - q_0, 0) at u in 64 bits, and whether u is further than 2e-6 of the total from a border: the
+    64-bit sums are good to 4e-14 of p, and p - q is about 1e-7 of p at the least here."""
+    def soft(x):
+        e = np.exp(x.astype(np.float64) - x.max(-1, keepdims=True))
+        return e / e.sum(-1, keepdims=True)
+
+    w = np.maximum(soft(logits) - soft(dl), 0.0)
+    cdf = np.cumsum(w, -1)
+    target = u.astype(np.float64) * cdf[:, -1]
+    y = (cdf <= target[:, None]).sum(-1)
+    rows = np.arange(len(y))
+    lo, hi = cdf[rows, y] - w[rows, y], cdf[rows, y]
+    return y, np.minimum(target - lo, hi - target) > 2e-6 * cdf[:, -1]
+
+
+@pytest.mark.parametrize("share", [1.0, 0.5, 0.02])
+@pytest.mark.parametrize("V", [777, 20011])
+def test_target_next_to_the_draft(V, share):
+    """The draft's logits are the target's next fp32 value, up or down, for a share of the tokens (the others' the target's
+    own, but for one in a hundred, where they differ by 1e-4): the residual's signs hang on the totals' last bits."""
+    B, g = 64, gen(V)
+    x = 3.0 * torch.randn((B, V), generator=g, device="cuda")
+    up = torch.rand((B, V), generator=g, device="cuda") < 0.5
+    q = torch.nextafter(x, torch.where(up, INF, -INF))
+    kind = torch.rand((B, V), generator=g, device="cuda")
+    q = torch.where(kind < share, q, torch.where(kind > 0.99, x + 1e-4 * torch.randn((B, V), generator=g, device="cuda"), x))
+    draft = (q - x).argmax(-1).to(torch.int32)[:, None]     # the least p / q: rejected at the largest u
+    u = torch.rand((B, 2), generator=g, device="cuda")
+    u[:, 0] = 1.0 - 2.0 ** -24
+    logits = torch.stack([x, x], 1)
+    want, sure = tokens_of_the_residual(x.cpu().numpy(), q.cpu().numpy(), u[:, 1].cpu().numpy())
+    tok, acc = fl.verify_draft(logits, q[:, None].contiguous(), draft, u)
+    _, wa = ref.verify(logits.cpu().numpy(), q[:, None].cpu().numpy(), draft.cpu().numpy(), u.cpu().numpy(), None, 1.0)
+    assert np.array_equal(acc.cpu().numpy(), wa)      # (a row's q may be below its p everywhere that it could be rejected)
+    sure &= wa == 0
+    assert sure.mean() >= 0.85
+    assert np.array_equal(tok[:, 0].cpu().numpy()[sure], want[sure])
