@@ -247,6 +247,7 @@ class FlashLoop:
         _check(st, "flashloop_init")
         self.ctx = ctx
         self.lazy = self.c.resid_bits != 16
+        self._share_scratch, self._share_kept = None, []
 
     def close(self):
         if getattr(self, "ctx", None):
@@ -265,6 +266,8 @@ class FlashLoop:
                "flashloop_prefill", self.ctx)
 
     def decode_step(self, h0, B: int, h_out=None, logits=None, stream=None):
+        if self._share_scratch is not None:
+            self._share_used(stream)
         _check(lib().flashloop_decode_step(self.ctx, _ptr(h0), B, _ptr(h_out), _ptr(logits), _stream_ptr(stream)),
                "flashloop_decode_step", self.ctx)
 
@@ -283,17 +286,34 @@ class FlashLoop:
             self._lens_keep = v
         _check(lib().flashloop_reset(self.ctx, arr, _stream_ptr(stream)), "flashloop_reset", self.ctx)
 
-    def share_prefix(self, n_seq: int, n: int):
+    def share_prefix(self, n_seq: int, n: int, stream=None):
         """Sequences 0..n_seq-1 hold the same first n positions: decode steps read them once for
-        the batch (``flashloop_share_prefix``).  n = 0 ends it."""
+        the batch (``flashloop_share_prefix``).  n = 0 ends it.  ``stream``: the stream of the steps to come, to
+        which the scratch belongs; a scratch that another call replaces goes back to torch's allocator when the
+        steps issued until then are done, on whatever stream they run.  (One that a captured step uses is kept.)"""
         import torch
         scratch, nbytes = None, 0
         if n:
             nbytes = int(lib().flashloop_share_prefix_scratch_bytes(ctypes.byref(self.c), n_seq, n))
-            scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.workspace.device)
+            with torch.cuda.stream(self._stream_of(stream)):
+                scratch = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.workspace.device)
         _check(lib().flashloop_share_prefix(self.ctx, n_seq, n, None if scratch is None else _ptr(scratch), nbytes),
                "flashloop_share_prefix", self.ctx)
         self._share_scratch = scratch   # keep alive: the library borrows it
+
+    def _stream_of(self, stream):
+        """The torch stream of a context's call (None: the legacy default stream)."""
+        import torch
+        return torch.cuda.default_stream(self.workspace.device) if stream is None else stream
+
+    def _share_used(self, stream):
+        """A step on ``stream`` writes the scratch of a shared prefix: not to be given out again before it is done."""
+        import torch
+        if torch.cuda.is_current_stream_capturing():   # replays come at any time
+            if not any(t is self._share_scratch for t in self._share_kept):
+                self._share_kept.append(self._share_scratch)
+        else:
+            self._share_scratch.record_stream(self._stream_of(stream))
 
     def sync_status(self, stream=None) -> int:
         return int(lib().flashloop_sync_status(self.ctx, _stream_ptr(stream)))

@@ -198,7 +198,8 @@ fl_status flashloop_reset(flashloop_ctx* ctx, const int* seq_len, fl_stream_t st
  * n = 0 ends it, and so does an import, or a reset that sets one of those
  * sequences shorter than n.  scratch: device memory of
  * flashloop_share_prefix_scratch_bytes(), 256-byte aligned, the caller's, in use
- * until sharing ends.  Captured decode graphs are dropped and captured again.
+ * until sharing ends and the steps issued until then are done.  The context's own captured decode
+ * graphs are dropped and captured again; a graph that the caller captured keeps using the scratch.
  * Errors: FL_ERR_INVALID_ARG (n_seq < 2, n < 0, or a sequence shorter than n),
  * FL_ERR_CAPACITY (n_seq > max_batch, n >= max_ctx), FL_ERR_WORKSPACE. */
 size_t flashloop_share_prefix_scratch_bytes(const flashloop_config* cfg, int n_seq, int n);
