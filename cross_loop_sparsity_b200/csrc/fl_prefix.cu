@@ -366,6 +366,10 @@ __global__ void __launch_bounds__(128, 2)
     __syncwarp();
     if (lane == 0 && issued < 2 * mine) issue(issued++);
   };
+  // lane 0: the copies in flight land (bounded) before the block can end
+  auto land = [&]() {
+    each_in_flight(issued, SLOTS, [&](int slot, int parity) { mbar_wait(smem_u32(&full[warp][slot]), parity, nullptr); });
+  };
   auto place = [&](int slot, int in_group) {   // (thread tid's row)
     const int h = g * a.G + in_group, sb = slot / a.Tq;
     row_id[tid] = slot < 0 ? -1 : static_cast<long long>(slot) * a.H + h;
@@ -389,8 +393,7 @@ __global__ void __launch_bounds__(128, 2)
   }
   __syncthreads();   // row_id
   if (r0 >= nrows) {
-    if (lane == 0)     // (no rows after all: the copies land before the block ends)
-      for (int n = 0; n < issued; ++n) mbar_wait(smem_u32(&full[warp][n]), 0, nullptr);
+    if (lane == 0) land();   // (no rows after all)
     if (a.tc_ctas) pdl_wait();
     return;
   }
@@ -427,9 +430,9 @@ __global__ void __launch_bounds__(128, 2)
       mine, smem_u32(qsm), a.scale2, [&](int n) { return wring + n % SLOTS * TILE_BYTES; },
       [&](int i) { return ncols - (tb + warp + i * kPxWarps) * kPxTile; }, arrived, refill, m_run, l_run, acc);
   if (done < mine && lane == 0) {
-    // a tile never arrived: let the copies in flight land (bounded); the result becomes NaN
+    // a tile never arrived; the result becomes NaN
     bad_sm = 1;
-    for (int n = max(0, issued - SLOTS); n < issued; ++n) mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr);
+    land();
   }
   // ---- the four warps' parts become one
 #pragma unroll
@@ -556,14 +559,17 @@ __global__ void __launch_bounds__(128, 2)
     __syncwarp();
     if (lane == 0 && issued < 2 * mine) issue(issued++);
   };
+  // lane 0: the copies in flight land (bounded) before the block can end
+  auto land = [&]() {
+    each_in_flight(issued, SLOTS, [&](int slot, int parity) { mbar_wait(smem_u32(&full[warp][slot]), parity, nullptr); });
+  };
   const int first = r0 / a.G;
   if (pre) {
     nrows = pack_queries(a, first, (r0 + RB - 1) / a.G - first + 1, ql, slot_sm[warp]) * a.G;
     __syncwarp();
   }
   if (r0 >= nrows) {
-    if (lane == 0)            // (no rows after all: the copies land before the warp ends)
-      for (int n = 0; n < issued; ++n) mbar_wait(smem_u32(&full[warp][n]), 0, nullptr);
+    if (lane == 0) land();    // (no rows after all)
     if (a.tc_ctas) pdl_wait();
     return;
   }
@@ -586,8 +592,7 @@ __global__ void __launch_bounds__(128, 2)
   const int done = warp_tiles<HD, NM, false>(
       mine, smem_u32(wring), a.scale2, slot_at, [&](int i) { return ncols - (tb + i) * kPxTile; }, arrived, refill, m_run, l_run,
       acc);
-  if (done < mine && lane == 0)   // a tile never arrived: let the copies in flight land (bounded); the rows become NaN
-    for (int n = max(0, issued - SLOTS); n < issued; ++n) mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr);
+  if (done < mine && lane == 0) land();   // a tile never arrived; the rows become NaN
   const long long split = pre ? sp : a.n_p + sp;
 #pragma unroll
   for (int i = 0; i < NM; ++i)
@@ -1038,8 +1043,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
       if (bad) {   // let every copy in flight land (bounded) before the block can end
-        for (int i = max(0, nk - KS); i < nk; ++i) mbar_wait(smem_u32(&k_full[i % KS]), (i / KS) & 1, nullptr);
-        for (int i = max(0, nv - VS); i < nv; ++i) mbar_wait(smem_u32(&v_full[i % VS]), (i / VS) & 1, nullptr);
+        each_in_flight(nk, KS, [&](int slot, int parity) { mbar_wait(smem_u32(&k_full[slot]), parity, nullptr); });
+        each_in_flight(nv, VS, [&](int slot, int parity) { mbar_wait(smem_u32(&v_full[slot]), parity, nullptr); });
       }
     }
     __syncthreads();
@@ -1389,8 +1394,8 @@ __global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_c
     __syncwarp();
   }
   if (!ok && lane == 0)   // a tile never arrived: let the copies in flight land (bounded) before the warp ends
-    for (long long u = max(u0, last + 1 - kWsStages); u <= last; ++u)
-      mbar_wait(smem_u32(&full[warp][(u - u0) % kWsStages]), static_cast<int>((u - u0) / kWsStages) & 1, nullptr);
+    each_in_flight(last + 1 - u0, kWsStages,
+                   [&](int slot, int parity) { mbar_wait(smem_u32(&full[warp][slot]), parity, nullptr); });
 }
 
 // ---- many rows: S^T = K Q^T on tcgen05, blocks of 256 keys (two products of 128) x 128 rows, so that a
@@ -1648,8 +1653,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     if (!ok) {   // the products stopped: let the copies in flight land (bounded) before the block can end
       bad = 1;
-      if (segs) mbar_wait(smem_u32(&k_full), (segs - 1) & 1, nullptr);
-      for (int i = max(0, blocks - QS); i < blocks; ++i) mbar_wait(smem_u32(&q_full[i % QS]), (i / QS) & 1, nullptr);
+      each_in_flight(segs, 2, [&](int slot, int parity) { mbar_wait(smem_u32(&k_full[slot]), parity, nullptr); });
+      each_in_flight(blocks, QS, [&](int slot, int parity) { mbar_wait(smem_u32(&q_full[slot]), parity, nullptr); });
     }
   }
   tc_fence_before();

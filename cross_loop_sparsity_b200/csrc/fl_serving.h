@@ -32,6 +32,14 @@ inline fl_status cuda_status(cudaError_t e) {
   return e == cudaSuccess ? FL_OK : refuse(FL_ERR_CUDA, cudaGetErrorString(e));
 }
 
+// A ring of `slots` barriers, load n on slot n % slots in its phase n / slots: wait(slot, parity) for each of the
+// `issued` loads that may still be under way, the oldest first (those before them had to arrive for their slots).
+template <class N, class Wait>
+__host__ __device__ inline void each_in_flight(N issued, int slots, Wait wait) {
+  for (N n = issued > slots ? issued - slots : 0; n < issued; ++n)
+    wait(static_cast<int>(n % slots), static_cast<int>(n / slots) & 1);
+}
+
 // A stride is usable when its dimension has one element or it is a positive multiple of `unit`.
 inline bool stride_ok(int64_t stride, int64_t dim, int64_t unit) {
   return dim <= 1 || (stride > 0 && stride % unit == 0 && stride < (int64_t(1) << 38));
