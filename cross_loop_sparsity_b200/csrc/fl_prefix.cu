@@ -47,6 +47,7 @@ struct PrefixArgs {
   int tc_ctas;            // > 0: the prefix part runs on k_prefix_tc with at most this many CTAs (n_p = items_p = 0)
   float* tc_o;            // [tc_ctas + Hkv * row blocks][kTcRows][hd]
   float2* tc_ml;          // [tc_ctas + Hkv * row blocks][kTcRows]
+  int* status;            // where a context's step records a wait that ran out, or nullptr (its result is NaN either way)
 };
 
 // a / b for a, b >= 0: most quotients here fit the 32-bit divider, several times faster than the 64-bit one
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(128, 2)
     for (; issued < SLOTS && issued < 2 * mine; ++issued) issue(issued);
   // whole warp: load n has arrived, or (false) its wait ran out
   auto arrived = [&](int n) {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, nullptr)) != 0;
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&full[warp][n % SLOTS]), (n / SLOTS) & 1, a.status)) != 0;
   };
   // whole warp: a slot has been read; the next load takes it
   auto refill = [&]() {
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(128, 2)
   };
   // lane 0: the copies in flight land (bounded) before the block can end
   auto land = [&]() {
-    each_in_flight(issued, SLOTS, [&](int slot, int parity) { mbar_wait(smem_u32(&full[warp][slot]), parity, nullptr); });
+    each_in_flight(issued, SLOTS, [&](int slot, int parity) { mbar_wait(smem_u32(&full[warp][slot]), parity, a.status); });
   };
   auto place = [&](int slot, int in_group) {   // (thread tid's row)
     const int h = g * a.G + in_group, sb = slot / a.Tq;
@@ -1847,7 +1848,7 @@ cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s) 
   a.out32 = L.out32; a.lse = c.lse; a.k = c.k; a.v = c.v;
   a.k_sb = c.k_stride[0]; a.k_sg = c.k_stride[1]; a.k_sr = c.k_stride[2];
   a.v_sb = c.v_stride[0]; a.v_sg = c.v_stride[1]; a.v_sr = c.v_stride[2];
-  a.lens = c.lens; a.q_lens = c.q_lens; a.lens_add = L.lens_add;
+  a.lens = c.lens; a.q_lens = c.q_lens; a.lens_add = L.lens_add; a.status = L.status;
   a.B = c.B; a.Tq = c.Tq; a.H = c.H; a.Hkv = c.Hkv; a.G = c.H / c.Hkv; a.P = c.P; a.S = c.S;
   a.rb_p = p.rb_p; a.n_p = p.n_p; a.rb_s = p.rb_s; a.n_s = p.n_s;
   a.items_p = p.rb_p * p.n_p * c.Hkv;

@@ -676,7 +676,7 @@ fl_status run_layer(flashloop_ctx* ctx, const LayerRef& L, const CallShape& cs, 
         st[2] = hd;
       }
       pl.q32 = ctx->q_cur; pl.out32 = L.o_st; pl.lens_add = 1 - ctx->share_n;   // pos holds the new token's position
-      pl.pdl = ctx->pdl != 0;
+      pl.pdl = ctx->pdl != 0; pl.status = ctx->status;
       FL_LAUNCH(FL_KIND_ATTN, launch_prefix(pl, ctx->share_scratch, s));
       ++ctx->launches;   // two kernels: the splits and their merge
     } else if (cs.decode) {

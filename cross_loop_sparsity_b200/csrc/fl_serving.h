@@ -63,6 +63,7 @@ struct PrefixLaunch {
   float* out32;         // fp32 copy of the output rows [B*Tq*H][hd], or nullptr
   int lens_add;         // added to lens[b] before it is clamped
   bool pdl;             // the first launch may overlap its predecessor
+  int* status;          // fp32 queries: error bits of waits that ran out, or nullptr
 };
 size_t prefix_scratch_bytes(int B, int Tq, int H, int Hkv, int hd, int P, int S, bool fp32_queries);
 cudaError_t launch_prefix(const PrefixLaunch& L, void* scratch, cudaStream_t s);
