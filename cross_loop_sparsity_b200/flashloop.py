@@ -292,6 +292,7 @@ class FlashLoop:
         which the scratch belongs; a scratch that another call replaces goes back to torch's allocator when the
         steps issued until then are done, on whatever stream they run.  (One that a captured step uses is kept.)"""
         import torch
+        _need_sizes("flashloop_share_prefix", n_seq=n_seq, n=n)
         scratch, nbytes = None, 0
         if n:
             nbytes = int(lib().flashloop_share_prefix_scratch_bytes(ctypes.byref(self.c), n_seq, n))
@@ -558,6 +559,20 @@ def _need(ok: bool, what: str, why: str):
         raise FlashLoopError(1, what, why)
 
 
+def _fits(*sizes):
+    """Whether the sizes are what the library's ints hold (ctypes would cut them to 32 bits)."""
+    return all(-2 ** 31 <= n < 2 ** 31 for n in sizes)
+
+
+def _need_sizes(what: str, **sizes):
+    for name, n in sizes.items():
+        _need(_fits(n), what, f"{name} = {n} is out of range")
+
+
+def _scratch_bytes(what: str, *sizes) -> int:
+    return int(getattr(lib(), what + "_scratch_bytes")(*sizes)) if _fits(*sizes) else 0
+
+
 def _sig(t):
     return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
 
@@ -617,7 +632,7 @@ _ptrs7, _ptrs9, _ptrs10 = (struct.Struct(f"={n}Q").pack for n in (7, 9, 10))
 
 
 def prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S) -> int:
-    return int(lib().flashloop_prefix_attention_scratch_bytes(B, Tq, H, Hkv, hd, P, S))
+    return _scratch_bytes("flashloop_prefix_attention", B, Tq, H, Hkv, hd, P, S)
 
 
 def prefix_attention(q, k_prefix, v_prefix, k, v, lens, q_lens=None, scale=None, out=None, lse=None, scratch=None,
@@ -649,6 +664,7 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, lens, q_lens=None, scale=None,
         _need(own is not None or pre is not None, what, "neither a prefix nor rows of the sequences' own")
         Hkv = own.shape[1] if own is not None else pre.shape[0]
         S, P = own.shape[2] if own is not None else 0, pre.shape[1] if pre is not None else 0
+        _need_sizes(what, B=B, Tq=Tq, H=H, Hkv=Hkv, hd=hd, P=P, S=S)
         bf = torch.bfloat16
         for name, t, dt, shape, contiguous in (
                 ("q", q, bf, (B, Tq, H, hd), False), ("out", out, bf, (B, Tq, H, hd), False),
@@ -674,7 +690,7 @@ def prefix_attention(q, k_prefix, v_prefix, k, v, lens, q_lens=None, scale=None,
 
 
 def column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S) -> int:
-    return int(lib().flashloop_column_weights_scratch_bytes(B, Tq, H, Hkv, hd, S))
+    return _scratch_bytes("flashloop_column_weights", B, Tq, H, Hkv, hd, S)
 
 
 def column_weights(q, k, lse, acc, lens=None, q_lens=None, scale=None, out=None, scratch=None, stream=None):
@@ -698,6 +714,7 @@ def column_weights(q, k, lse, acc, lens=None, q_lens=None, scale=None, out=None,
         _need(q_lens is None or lens is not None, what, "q_lens goes with lens")
         B, Tq, H, hd = q.shape
         Hkv, S = k.shape[1], k.shape[2]
+        _need_sizes(what, B=B, Tq=Tq, H=H, Hkv=Hkv, hd=hd, S=S)
         bf, f32 = torch.bfloat16, torch.float32
         for name, t, dt, shape, contiguous in (
                 ("q", q, bf, (B, Tq, H, hd), False), ("k", k, bf, (B, Hkv, S, hd), False),
@@ -717,7 +734,7 @@ def column_weights(q, k, lse, acc, lens=None, q_lens=None, scale=None, out=None,
 
 
 def evict_scratch_bytes(B, Hkv, S, keep) -> int:
-    return int(lib().flashloop_evict_scratch_bytes(B, Hkv, S, keep))
+    return _scratch_bytes("flashloop_evict", B, Hkv, S, keep)
 
 
 def evict(k, v, acc, pos, lens, keep: int, recent: int = 0, sinks: int = 0, out=None, scratch=None, stream=None):
@@ -734,6 +751,7 @@ def evict(k, v, acc, pos, lens, keep: int, recent: int = 0, sinks: int = 0, out=
     def make():
         _need(k.dim() == 4 and k.element_size() == 2, what, "k must be [B, Hkv, S, hd] of a 2-byte type")
         B, Hkv, S, hd = k.shape
+        _need_sizes(what, B=B, Hkv=Hkv, S=S, hd=hd, keep=keep, recent=recent, sinks=sinks)
         f32, i32 = torch.float32, torch.int32
         n = S if out is None else keep
         for name, t, dt, shape, contiguous in (
@@ -757,7 +775,7 @@ def evict(k, v, acc, pos, lens, keep: int, recent: int = 0, sinks: int = 0, out=
 
 
 def verify_draft_scratch_bytes(B, D, V) -> int:
-    return int(lib().flashloop_verify_draft_scratch_bytes(B, D, V))
+    return _scratch_bytes("flashloop_verify_draft", B, D, V)
 
 
 def verify_draft(logits, draft_logits, draft, u, n_draft=None, temperature: float = 1.0, tokens=None, n_accepted=None,
@@ -784,6 +802,9 @@ def verify_draft(logits, draft_logits, draft, u, n_draft=None, temperature: floa
 
     def make():
         B, D, V = logits.shape[0], logits.shape[1] - 1, logits.shape[2]
+        _need_sizes(what, B=B, D=D, V=V)
+        # (a smaller one may become 0 in 32 bits, and be taken for greedy)
+        _need(temperature == 0 or temperature >= 1e-20, what, "temperature must be 0, or finite and at least 1e-20")
         f32, i32 = torch.float32, torch.int32
         for name, t, dt, shape, contiguous in (
                 ("logits", logits, f32, (B, D + 1, V), False), ("draft_logits", draft_logits, f32, (B, D, V), False),
