@@ -310,15 +310,15 @@ __device__ void describe(const VerifyArgs& a, int row, int n, const Ahead& h, co
 // all exponentials; ap and aq, those of tokens whose weight is positive.  The weight of token j is
 //   max(e_p / Z_p - e_q / Z_q, 0) = max(ratio e_p - e_q, 0) / Z_q,  ratio = Z_q / Z_p,
 // so a range's weight is ratio * ap - aq, and the exact ratio need not be known
-// before the pass: which tokens are positive is decided with the 32-bit one (good to 4e-6: its sums' roundings), and
-// a token it gets wrong weighs less than that much of its e_q.  `near` is the e_q of all tokens that it could get wrong,
-// those whose two terms are within kNearWords of each other in the high words (1e-5 of either at the least):
-// what the pick allows for.
+// before the pass: which tokens are positive is decided with the 32-bit one (good to 4e-6, by its sums' roundings), and
+// a token it gets wrong weighs less than the ratios' difference times its e_q.  `near` is the e_q of all tokens that it
+// could get wrong, those whose two terms are within kNearWords of each other in the high words (kNearReach of either at
+// the least): that difference times `near` is what the pick allows for.
 struct Sums {
   double p, q, ap, aq, near, pad;
 };
 constexpr int kNearWords = 22;
-constexpr double kNearError = 1e-5;
+constexpr double kNearReach = 1e-5;
 template <bool DRAFT>
 __device__ Sums range_sums_of(const VerifyArgs& a, int b, const Deciding& d, int j0, int j1, const double* table) {
   constexpr int U = DRAFT ? 4 : 8;   // tokens of a lane in flight
@@ -495,8 +495,10 @@ __global__ void __launch_bounds__(kSumThreads, 4) k_verify_sums(const VerifyArgs
     const Three t = block_sums_f64(Three{s.p, s.q, s.near}, buf);
     zp = t.x;
     zq = t.y;
-    // The ranges' weights may be off, together, by what the 32-bit ratio got wrong; so may the target.
-    unsure = 2.0 * kNearError * t.z;
+    // The ranges' weights may be off, together, by what the 32-bit ratio got wrong; so may the target.  (1e-13: this
+    // one's own roundings; a 32-bit ratio beyond its bound: nothing is sure.)
+    const double off = fabs(zq / zp / d.ratio - 1.0) + 1e-13;
+    unsure = !d.with_draft || !d.fine ? 0.0 : off <= kNearReach ? 2.0 * off * t.z : INFINITY;
   };
   totals();
   while (d.near && d.fine) {
