@@ -200,6 +200,8 @@ fl_status flashloop_reset(flashloop_ctx* ctx, const int* seq_len, fl_stream_t st
  * flashloop_share_prefix_scratch_bytes(), 256-byte aligned, the caller's, in use
  * until sharing ends and the steps issued until then are done.  The context's own captured decode
  * graphs are dropped and captured again; a graph that the caller captured keeps using the scratch.
+ * The attention's work is divided by max_ctx, not by the lengths: with max_ctx several times the lengths a
+ * step can take longer with sharing than without.
  * Errors: FL_ERR_INVALID_ARG (n_seq < 2, n < 0, or a sequence shorter than n),
  * FL_ERR_CAPACITY (n_seq > max_batch, n >= max_ctx), FL_ERR_WORKSPACE. */
 size_t flashloop_share_prefix_scratch_bytes(const flashloop_config* cfg, int n_seq, int n);
@@ -377,6 +379,10 @@ fl_status fl_gemm_skinny_noalloc(const uint16_t* A, const uint16_t* B, float* D,
 /*    at the same time need one each.  The buffers belong to the current      */
 /*    device.  Every call may be captured into a CUDA graph.                  */
 /*  - outputs may not overlap inputs or each other except where stated.       */
+/*  - B and Hkv are at most 65535, B * Tq * H at most 2^30, strides below      */
+/*    2^38.                                                                   */
+/*  - every wait inside a kernel is bounded; should one of the attention or    */
+/*    the column weights run out, the result of its rows or columns is NaN.    */
 /*  - a refused call launches nothing; its reason is                          */
 /*    flashloop_last_cuda_error(NULL).                                        */
 /* ------------------------------------------------------------------------ */
@@ -387,7 +393,8 @@ fl_status fl_gemm_skinny_noalloc(const uint16_t* A, const uint16_t* B, float* D,
  * queries are the last q_lens[b] tokens of that cache, causally masked.
  *   out = softmax(scale * q . [Kprefix, K]) [Vprefix, V],  lse = log sum exp
  * bf16 inputs and output, fp32 sums, P rounded to bf16 in front of the product
- * with V.  A query that sees nothing gets out = 0 and lse = -inf.  Rows t >=
+ * with V (a weight is off by at most 2^-8 of itself; lse and the sum that divides are formed from the unrounded
+ * ones).  A query that sees nothing gets out = 0 and lse = -inf.  Rows t >=
  * q_lens[b] of out and lse are left as they were.  K / V rows past a query's
  * last visible one are never used, whatever they hold.
  *   q, out [B][Tq][H][hd]; k_prefix, v_prefix [Hkv][P][hd]; k, v [B][Hkv][S][hd]
@@ -449,7 +456,7 @@ fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratc
  * first in this order: protected ones (pos < sinks, or pos > the largest pos
  * among the n columns - recent), then by acc descending -- compared as IEEE bit patterns
  * (uint32), like the other selections; acc holds sums of weights, never
- * negative -- then by slot ascending.  A kept column in a slot < keep stays there; the slots < keep
+ * negative, and not -0.0, which as bits would rank above every weight -- then by slot ascending.  A kept column in a slot < keep stays there; the slots < keep
  * freed by the others take the kept columns from slots >= keep, both in ascending
  * slot order: what moves is as little as can be, and pos says which token a slot
  * holds.  n <= keep keeps everything.  lens_out[b] = min(lens[b], keep).
@@ -457,7 +464,7 @@ fl_status flashloop_column_weights(const flashloop_weights_args* a, void* scratc
  *   lens int32 [B]; *_out alike with `keep` slots, or the inputs' own pointers: then the cache is
  *   compacted in place, with the inputs' strides.  Slots from lens_out[b] on are left as they were.
  * acc and pos (and their outputs) have contiguous rows, 4-byte aligned, with strides of b and g.
- * Limits: keep >= 1, recent >= 0, sinks >= 0, recent + sinks <= keep; all outputs in place, or none. */
+ * Limits: 1 <= S <= 262144, keep >= 1, recent >= 0, sinks >= 0, recent + sinks <= keep; all outputs in place, or none. */
 typedef struct {
   const uint16_t* k;
   const uint16_t* v;
