@@ -285,7 +285,9 @@ __device__ __forceinline__ int warp_tiles(int mine, uint32_t qs, float scale2, T
 // the range -- a sequence's columns stop at the last one all its queries see;
 // the few that only later queries see are added by the merge -- so what a masked
 // row of V holds never meets a product.  HILO: fp32 queries and probabilities as
-// bf16 hi + lo pairs (about 16 significant bits).
+// bf16 hi + lo pairs (about 16 significant bits); otherwise P enters the
+// product with V rounded to bf16, as one product of the tensor cores takes it: a weight is off by at most 2^-8 of
+// itself, and the outputs' error against 64 bits goes from 0.0017 (their own rounding to bf16) to 0.0018 relative.
 // ============================================================================
 template <int HD, int NM, bool HILO>
 __global__ void __launch_bounds__(128, 2)
@@ -626,8 +628,9 @@ __global__ void __launch_bounds__(128, 2)
 //   Running maximum: O is rescaled only when a row's maximum has grown by more
 // than 8 (log2 domain) -- until then the old one stays, the probabilities are at
 // most 2^8, and bf16's relative precision is the same there.
-//   P enters the second product rounded to bf16 (as in the prefill attention);
-// the sums use the fp32 values.
+//   P enters the second product rounded to bf16 (as in the prefill attention), by at most 2^-8 of a weight, so that it takes
+// one product instead of two; the sums use the fp32 values.  Outputs are then 0.0022 from 64 bits, relative, 0.0017
+// of it their own rounding to bf16.
 //   Measured: 256 rows x 65536 columns x 8 heads, hd 128, 69 GFLOP: 75 us (42 at the measured GEMM rate; about 20
 // of the 75 are start and end: queries in, TMEM, pipeline fill, partial results out).  Two softmax
 // warpgroups instead of four took 84.  In the steady state Q K^T, with both operands in
@@ -1407,8 +1410,12 @@ __global__ void __launch_bounds__(32 * kWsWarps) k_weights_stream(const __grid_c
 // this one's exponentials).  Bound by the exponentials, 16 a clock and SM, with shared memory
 // (the products' operands) close behind.  512 queries of 16 heads x 16384 columns of 4 KV heads x 128, causal: 52 us,
 // of which the exponentials alone would take 30 and the products 21; warpgroups that take alternate
-// blocks 54, or half the rows of a key 57, mma.sync warp tiles 206.
-constexpr int kWtPoly = 1;   // of 8 pairs of exponentials, those formed on the FMA pipe (0: 56 us there, 1: 52, 2: 54, 3: 55)
+// blocks 54, or half the rows of a key 57, mma.sync warp tiles 206.  18 warps leave 96 registers a thread, beside
+// two score tiles of 32: 116 bytes are spilled (264 read back).
+// Of 8 pairs of exponentials, those formed on the FMA pipe: 0 / 1 / 2 / 3 of them take, us, there 54 / 51 / 50 / 52, with heads of
+// 64 53 / 50 / 50 / 52, 4 x 128 queries of 32/8 heads x 8192 columns 74 / 71 / 71 / 72 (64: 71 / 69 / 70 / 70), 8 x 40
+// queries x 30000 columns 87 / 86 / 86 / 85.
+constexpr int kWtPoly = 1;
 constexpr int kWtCols = 256, kWtRows = 128, kWtThreads = 576;
 constexpr int kWtStaged = 24;   // row blocks whose lse are in shared memory at once
 template <int HD>

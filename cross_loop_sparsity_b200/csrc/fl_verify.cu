@@ -438,9 +438,9 @@ __device__ double block_scan_f64(double v, Three* buf, double& total) {
 // Second launch: every CTA finds its sequence's deciding row from the first
 // launch's sums, then each of its warps forms the 64-bit sums of a contiguous
 // range of that row's tokens, two exponentials a token, once.  Bound by the 64-bit pipe
-// (about 11 operations per exponential) and its conversions for many sequences, by a chain of round
+// (about 12 operations per exponential) and its conversions for many sequences, by a chain of round
 // trips for few: 64 rows of 131071 tokens about 37 us (18 of them the sums), one sequence of
-// 32000 8 us.
+// 32000 8 us.  Four CTAs per SM leave 64 registers a thread, of which 160 bytes spill.
 //   The CTA that finishes a sequence's last ranges picks its token: totals of the
 // ranges' sums, the range that holds the crossing, and the crossing token in it.  A near
 // decision is settled by the 64-bit totals of its row; when it turns out accepted, this CTA
@@ -691,9 +691,11 @@ fl_status flashloop_verify_draft(const flashloop_verify_args* c, void* scratch, 
   a.tickets = reinterpret_cast<unsigned*>(ws);
   a.dead = a.tickets + static_cast<size_t>(c->B) * c->D;
   a.done = a.dead + c->B;
-  // Skipping rows behind a rejection costs a memset in front and a ticket per chunk, and pays when most rows
-  // have not started by the first verdicts: with drafts of which most are accepted, with against
-  // without it, 45 MB of logits 27.6 / 20.8 us, 139 MB 44.2 / 37.8, 570 MB 110 / 117 (with more rejections 92).
+  // Skipping rows behind a rejection costs a memset in front, a ticket per chunk and the place of each skipped CTA, and pays
+  // when most rows have not started by the first verdicts.  With against without it, us, where 1 to 2 drafts are accepted,
+  // and where nearly all are: 45 MB of logits 29 / 22 and 29 / 22, 141 MB 47 / 42 and 50 / 41, 218 MB 53 / 53 and 61 / 54,
+  // 359 MB 68 / 80 and 85 / 78, 570 MB 92 / 119 and 124 / 117.  The host cannot know which it will be: from 350 MB on,
+  // where the first case wins about twice what the second loses.
   const bool early = c->temperature > 0.f && c->D >= 2 && static_cast<double>(c->B) * rows * c->V * 4.0 > 350e6;
   cudaError_t e;
   const dim3 grid(a.n_chunks, c->B, rows);
